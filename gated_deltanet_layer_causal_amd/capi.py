@@ -33,7 +33,9 @@ EXPORTS = (
     "gdn_gated_norm_bwd_workspace", "gdn_chunk_prepare", "gdn_chunk_prepare_bwd",
     "gdn_chunk_fwd_states", "gdn_chunk_fwd_states_save",
     "gdn_chunk_bwd_states", "gdn_chunk_bwd_reverse", "gdn_chunk_bwd_grads",
-    "gdn_check_cu_seqlens",
+    "gdn_check_cu_seqlens", "gdn_recurrent_fwd", "gdn_step_fwd", "gdn_check_slots",
+    "gdn_cache_copy", "gdn_cache_fork", "gdn_cache_retain", "gdn_cache_release",
+    "gdn_cache_compact", "gdn_cache_workspace",
 )
 
 
@@ -41,6 +43,13 @@ class Shape(ctypes.Structure):
     _fields_ = [("n_seq", c_int32), ("total_tokens", c_int64), ("hk", c_int32), ("hv", c_int32),
                 ("dk", c_int32), ("dv", c_int32), ("conv_k", c_int32), ("chunk", c_int32),
                 ("dtype", c_int), ("seg_chunks", c_int32)]
+
+
+class Cache(ctypes.Structure):
+    """gdn_cache: the slots of one layer's states.  Made by make_cache, which
+    checks the tensors and keeps them (`S`, `conv`)."""
+    _fields_ = [("S_ptr", c_void_p), ("S_stride", c_int64), ("conv_ptr", c_void_p),
+                ("conv_stride", c_int64), ("n_slots", c_int32)]
 
 
 class GDNError(RuntimeError):
@@ -98,6 +107,18 @@ def load(path: str = LIB_PATH):
     lib.gdn_check_cu_seqlens.argtypes = [SP, V, V, V]
     lib.gdn_gated_norm_bwd.argtypes = [I64, c_int32, c_int, V, V, V, F, c_int, V, V, V, V, V,
                                        c_size_t, V]
+    CP, I32 = POINTER(Cache), c_int32
+    lib.gdn_recurrent_fwd.argtypes = [SP, V, V, V, I64, I64, I64, V, V, F, CP, V, V, V, V, V, V]
+    lib.gdn_step_fwd.argtypes = [SP, V, I64, V, V, I64, V, I64, V, V, V, I64, V, F, F, F, c_int, CP,
+                                 V, V, V, V, V, V]
+    lib.gdn_check_slots.argtypes = [SP, I32, V, V, V, V, V, V]
+    lib.gdn_cache_copy.argtypes = [V, I64, I32, V, V, I64, I32, V, I64, I32, V]
+    lib.gdn_cache_fork.argtypes = [V, I64, I32, V, V, I32, V, V, c_size_t, V]
+    lib.gdn_cache_retain.argtypes = [V, I32, V, I32, V]
+    lib.gdn_cache_release.argtypes = [V, I32, V, I32, V]
+    lib.gdn_cache_compact.argtypes = [V, I64, I32, V, V, V, I32, V, c_size_t, V]
+    lib.gdn_cache_workspace.argtypes = [I32]
+    lib.gdn_cache_workspace.restype = c_size_t
     for name in ("gdn_conv_bwd_workspace", "gdn_gate_bwd_workspace", "gdn_chunk_fwd_workspace",
                  "gdn_chunk_bwd_workspace"):
         getattr(lib, name).argtypes = [SP]
@@ -109,7 +130,9 @@ def load(path: str = LIB_PATH):
                  "gdn_chunk_bwd", "gdn_gated_norm_fwd", "gdn_gated_norm_bwd", "gdn_chunk_prepare",
                  "gdn_chunk_prepare_bwd", "gdn_chunk_fwd_states", "gdn_chunk_fwd_states_save",
                  "gdn_chunk_bwd_states", "gdn_chunk_bwd_reverse",
-                 "gdn_chunk_bwd_grads", "gdn_check_cu_seqlens"):
+                 "gdn_chunk_bwd_grads", "gdn_check_cu_seqlens", "gdn_recurrent_fwd", "gdn_step_fwd",
+                 "gdn_check_slots", "gdn_cache_copy", "gdn_cache_fork", "gdn_cache_retain",
+                 "gdn_cache_release", "gdn_cache_compact"):
         getattr(lib, name).restype = c_int
     _lib = lib
     return lib
@@ -509,3 +532,222 @@ def gdn_gated_norm_bwd(o, z, w, dy, dout, dz, dw, ws, eps=1e-6, act=GDN_ACT_SILU
     _ok("gdn_gated_norm_bwd", load().gdn_gated_norm_bwd(rows, dv, _dt(o), _p(o), _p(z), _p(w), eps,
                                                         act, _p(dy), _p(dout), _p(dz), _p(dw),
                                                         _p(ws), ws.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- serving: cached states
+def make_cache(S, conv=None) -> Cache:
+    """The C ABI's gdn_cache from the slots' views: S fp32 [n_slots, hv, dv,
+    dk] and (for the step) conv [n_slots, 3, C] in the storage type, each slot
+    dense, any stride between slots."""
+    if S.dtype != torch.float32 or S.dim() != 4 or S.shape[2] != S.shape[3] or S.shape[0] < 1:
+        raise ValueError(f"S must be float32 [n_slots, hv, d, d], got {S.dtype} {tuple(S.shape)}")
+    n, hv, d = S.shape[:3]
+    if S.stride()[1:] != (d * d, d, 1):
+        raise ValueError(f"each slot of S must be contiguous, got strides {S.stride()}")
+    c = Cache(S.data_ptr(), S.stride(0) if n > 1 else hv * d * d, None, 0, n)
+    if conv is not None:
+        if conv.dtype not in _GDN_DT or conv.dim() != 3 or tuple(conv.shape[:2]) != (n, 3):
+            raise ValueError(f"conv must be [{n}, 3, C] in a storage type, got {conv.dtype} "
+                             f"{tuple(conv.shape)}")
+        C = conv.shape[2]
+        if conv.stride()[1:] != (C, 1) or conv.device != S.device:
+            raise ValueError("each slot of conv must be contiguous and on S's device")
+        c.conv_ptr = conv.data_ptr()
+        c.conv_stride = conv.stride(0) if n > 1 else 3 * C
+    c.S, c.conv, c.device, c.heads = S, conv, S.device, (hv, d)
+    return c
+
+
+def _slot_call(name, dev, stream, fn, *args):
+    """Runs a serving entry point on `dev` (which need not be the current
+    device) and the given stream, or dev's current one."""
+    if dev.type != "cuda":
+        raise ValueError("libgdn takes device tensors only; got a host tensor")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream))
+    else:
+        st = fn(*args, _stream(stream))
+    _ok(name, st)
+
+
+def _on(dev, *named):
+    for nm, t in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{nm} is on {t.device}, the cache on {dev}")
+
+
+def _slot_tables(shape, dev, cu, slot_in, slot_out, slot_tok):
+    _cu_ok(shape, cu)
+    _need("slot_in", slot_in, torch.int32, shape.n_seq, optional=True)
+    _need("slot_out", slot_out, torch.int32, shape.n_seq, optional=True)
+    _need("slot_tok", slot_tok, torch.int32, shape.total_tokens, optional=True)
+    _on(dev, ("cu_seqlens", cu), ("slot_in", slot_in), ("slot_out", slot_out),
+        ("slot_tok", slot_tok))
+
+
+def _cache_ok(shape, cache):
+    if cache.heads != (shape.hv, shape.dv):
+        raise ValueError(f"the cache's states are of {cache.heads[0]} heads of {cache.heads[1]}, the "
+                         f"shape's of {shape.hv} of {shape.dv}")
+    return cache.device
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _row_ld(t):
+    """The row stride of a matrix; of fewer than two rows any serves (torch
+    leaves a single row's stride open), so their width."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def gdn_recurrent_fwd(shape, q, k, v, g, beta, scale, cache, slot_in, slot_out, slot_tok,
+                      cu_seqlens, o, stream=None):
+    """cache: make_cache(S).  slot_in, slot_out [n_seq] and slot_tok [T]:
+    int32 device tables, each may be None; see libgdn.h."""
+    dev = _cache_ok(shape, cache)
+    _chunk_qk(shape, q, k)
+    _rows("v", v, _tdt(shape), shape.total_tokens, shape.hv * shape.dv)
+    _per_token("g", shape, g)
+    _per_token("beta", shape, beta)
+    _heads("o", shape, o)
+    _slot_tables(shape, dev, cu_seqlens, slot_in, slot_out, slot_tok)
+    _on(dev, ("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("o", o))
+    _slot_call("gdn_recurrent_fwd", dev, stream, load().gdn_recurrent_fwd, byref(shape), _ptr(q),
+               _ptr(k), _ptr(v), _row_ld(q), _row_ld(k), _row_ld(v), _ptr(g), _ptr(beta), scale, byref(cache),
+               _ptr(slot_in), _ptr(slot_out), _ptr(slot_tok), _ptr(cu_seqlens), _ptr(o))
+
+
+def gdn_step_fwd(shape, x, w_conv, a, b, A_log, dt_bias, z, w_norm, scale, cache, slot_in,
+                 slot_out, slot_tok, cu_seqlens, out, l2_eps=1e-6, norm_eps=1e-6,
+                 act=GDN_ACT_SILU, stream=None):
+    """x [T, C], a, b [T, hv] and z [T, hv*d]: rows may be strided.  cache:
+    make_cache(S, conv); slot tables as gdn_recurrent_fwd."""
+    dev = _cache_ok(shape, cache)
+    dt, T = _tdt(shape), shape.total_tokens
+    C = _conv_ok(shape, x, w_conv, cu_seqlens)
+    if cache.conv is None or cache.conv.dtype != dt or cache.conv.shape[2] != C:
+        raise ValueError(f"the cache needs conv rows [n_slots, 3, {C}] of {dt}")
+    _rows("a", a, dt, T, shape.hv)
+    _rows("b", b, dt, T, shape.hv)
+    _need("A_log", A_log, torch.float32, shape.hv)
+    _need("dt_bias", dt_bias, torch.float32, shape.hv)
+    _rows("z", z, dt, T, shape.hv * shape.dv)
+    _need("w_norm", w_norm, torch.float32, shape.dv)
+    _heads("out", shape, out)
+    _slot_tables(shape, dev, cu_seqlens, slot_in, slot_out, slot_tok)
+    _on(dev, ("x", x), ("w_conv", w_conv), ("a", a), ("b", b), ("A_log", A_log),
+        ("dt_bias", dt_bias), ("z", z), ("w_norm", w_norm), ("out", out))
+    _slot_call("gdn_step_fwd", dev, stream, load().gdn_step_fwd, byref(shape), _ptr(x), _row_ld(x),
+               _ptr(w_conv), _ptr(a), _row_ld(a), _ptr(b), _row_ld(b), _ptr(A_log), _ptr(dt_bias), _ptr(z),
+               _row_ld(z), _ptr(w_norm), scale, l2_eps, norm_eps, act, byref(cache), _ptr(slot_in),
+               _ptr(slot_out), _ptr(slot_tok), _ptr(cu_seqlens), _ptr(out))
+
+
+SLOT_RANGE, SLOT_WRITTEN_TWICE, SLOT_WRITTEN_AND_READ = 1, 2, 4
+
+
+def gdn_check_slots(shape, n_slots, slot_in, slot_out, slot_tok, cu_seqlens, violations,
+                    stream=None):
+    """Writes to violations (an int32 device tensor of one element) the bit
+    mask of what is wrong with the slot tables (SLOT_*; 0 when valid)."""
+    dev = cu_seqlens.device
+    _slot_tables(shape, dev, cu_seqlens, slot_in, slot_out, slot_tok)
+    _need("violations", violations, torch.int32, 1)
+    _on(dev, ("violations", violations))
+    _slot_call("gdn_check_slots", dev, stream, load().gdn_check_slots, byref(shape), n_slots,
+               _ptr(slot_in), _ptr(slot_out), _ptr(slot_tok), _ptr(cu_seqlens), _ptr(violations))
+
+
+def _slot_rows(name, t):
+    """[n_slots, ...] with each slot dense: (slots, bytes of a slot, bytes between slots)"""
+    if t.dim() < 2 or t.shape[0] < 1 or not t[0].is_contiguous():
+        raise ValueError(f"{name} must be [n_slots, ...] with each slot contiguous, got shape "
+                         f"{tuple(t.shape)} strides {t.stride()}")
+    size = t[0].numel() * t.element_size()
+    return t.shape[0], size, t.stride(0) * t.element_size() if t.shape[0] > 1 else size
+
+
+def _indexes(name, dev, t, n=None):
+    _need(name, t, torch.int32, n)
+    _on(dev, (name, t))
+    return t.numel()
+
+
+def gdn_cache_copy(src, dst, src_idx=None, dst_idx=None, stream=None):
+    """dst[dst_idx[i]] = src[src_idx[i]], whole slots of two tensors [n_slots,
+    ...] of the same slot size; see libgdn.h for entries out of range."""
+    n_src, size, ss = _slot_rows("src", src)
+    n_dst, dsize, ds = _slot_rows("dst", dst)
+    if src.dtype != dst.dtype or size != dsize:
+        raise ValueError(f"slots of {size} bytes of {src.dtype} into slots of {dsize} of {dst.dtype}")
+    dev = src.device
+    _on(dev, ("dst", dst))
+    n = min(n_src, n_dst)
+    if src_idx is not None:
+        n = _indexes("src_idx", dev, src_idx)
+        if dst_idx is None and n > n_dst:
+            raise ValueError(f"{n} slots into {n_dst}")
+    if dst_idx is not None:
+        n = _indexes("dst_idx", dev, dst_idx, n if src_idx is not None else None)
+        if src_idx is None and n > n_src:
+            raise ValueError(f"{n} slots out of {n_src}")
+    if src_idx is None and dst_idx is None and n_src != n_dst:
+        raise ValueError(f"{n_src} slots into {n_dst} without indexes")
+    _slot_call("gdn_cache_copy", dev, stream, load().gdn_cache_copy, _ptr(src), ss, n_src,
+               _ptr(src_idx), _ptr(dst), ds, n_dst, _ptr(dst_idx), size, n)
+
+
+def gdn_cache_workspace(n_slots):
+    return int(load().gdn_cache_workspace(n_slots))
+
+
+def _cache_buf(buf, refs):
+    if buf.dim() != 2 or not buf.is_contiguous():
+        raise ValueError("the cache must be a contiguous [n_slots, slot] tensor")
+    _indexes("refs", buf.device, refs, buf.shape[0])
+    return buf.shape[0], buf.shape[1] * buf.element_size(), buf.device
+
+
+def gdn_cache_fork(buf, refs, src, dst, ws, stream=None):
+    """Takes a free slot of buf [n_slots, slot] for every request in src and
+    fills it; the slots go to dst (int32, as long as src)."""
+    n_slots, size, dev = _cache_buf(buf, refs)
+    n = _indexes("src", dev, src)
+    _indexes("dst", dev, dst, n)
+    _ws(ws)
+    _on(dev, ("workspace", ws))
+    _slot_call("gdn_cache_fork", dev, stream, load().gdn_cache_fork, _ptr(buf), size, n_slots,
+               _ptr(refs), _ptr(src), n, _ptr(dst), _ptr(ws), ws.numel() if ws is not None else 0)
+
+
+def _count(name, refs, slots, stream):
+    dev = refs.device
+    n_slots = _indexes("refs", dev, refs)
+    n = _indexes("slots", dev, slots)
+    _slot_call(name, dev, stream, getattr(load(), name), _ptr(refs), n_slots, _ptr(slots), n)
+
+
+def gdn_cache_retain(refs, slots, stream=None):
+    _count("gdn_cache_retain", refs, slots, stream)
+
+
+def gdn_cache_release(refs, slots, stream=None):
+    _count("gdn_cache_release", refs, slots, stream)
+
+
+def gdn_cache_compact(buf, refs, remap, table, ws, stream=None):
+    """Moves the live slots of buf to its front; remap [n_slots] receives
+    where each went, and table (int32, or None) is rewritten by it."""
+    n_slots, size, dev = _cache_buf(buf, refs)
+    _indexes("remap", dev, remap, n_slots)
+    n = 0 if table is None else _indexes("table", dev, table)
+    _ws(ws)
+    _on(dev, ("workspace", ws))
+    _slot_call("gdn_cache_compact", dev, stream, load().gdn_cache_compact, _ptr(buf), size, n_slots,
+               _ptr(refs), _ptr(remap), _ptr(table), n, _ptr(ws),
+               ws.numel() if ws is not None else 0)

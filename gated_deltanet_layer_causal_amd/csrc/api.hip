@@ -374,3 +374,136 @@ gdn_status gdn_check_cu_seqlens(const gdn_shape* s, const int32_t* cu, int32_t* 
 }
 
 }  // extern "C"
+
+namespace {
+
+gdn_status check_cache(const gdn_shape* s, const gdn_cache* c, bool conv) {
+  if (!c || !c->S || c->n_slots < 1) return GDN_ERR_INVALID_ARG;
+  if (c->S_stride < (int64_t)s->hv * s->dv * s->dk) return GDN_ERR_INVALID_ARG;
+  if (!aligned16(c->S) || c->S_stride % 4) return GDN_ERR_ALIGNMENT;
+  if (conv) {
+    if (!c->conv || c->conv_stride < 3 * channels(s)) return GDN_ERR_INVALID_ARG;
+    if (!aligned16(c->conv) || c->conv_stride * (int64_t)esize(s->dtype) % 16)
+      return GDN_ERR_ALIGNMENT;
+  }
+  return GDN_OK;
+}
+
+// base of rows of bytes: every slot starts at a multiple of 16 bytes
+gdn_status check_slot_rows(const void* base, int64_t stride, int64_t bytes, int32_t n) {
+  if (!base || n < 1 || bytes < 0 || stride < bytes) return GDN_ERR_INVALID_ARG;
+  if (!aligned16(base) || stride % 16 || bytes % 16) return GDN_ERR_ALIGNMENT;
+  return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_recurrent_fwd(const gdn_shape* s, const void* q, const void* k, const void* v,
+                             int64_t ldq, int64_t ldk, int64_t ldv, const float* g,
+                             const float* beta, float scale, const gdn_cache* cache,
+                             const int32_t* slot_in, const int32_t* slot_out,
+                             const int32_t* slot_tok, const int32_t* cu, void* o, void* stream) {
+  GDN_TRY(check_shape(s));
+  GDN_TRY(check_cache(s, cache, false));
+  if (!cu) return GDN_ERR_INVALID_ARG;
+  if (s->total_tokens > 0) {   // no tokens: states pass through, token tensors may be null
+    GDN_TRY(check_ptrs({q, k, v, o}));
+    if (!g || !beta) return GDN_ERR_INVALID_ARG;
+  }
+  GDN_TRY(check_ld(ldq, (int64_t)s->hk * s->dk));
+  GDN_TRY(check_ld(ldk, (int64_t)s->hk * s->dk));
+  GDN_TRY(check_ld(ldv, (int64_t)s->hv * s->dv));
+  StepArgs a = {};
+  a.q = q; a.k = k; a.v = v; a.ldq = ldq; a.ldk = ldk; a.ldv = ldv;
+  a.g = g; a.beta = beta; a.scale = scale; a.cache = *cache;
+  a.slot_in = slot_in; a.slot_out = slot_out; a.slot_tok = slot_tok; a.cu = cu; a.out = o;
+  return launched(launch_recurrent(*s, a, (hipStream_t)stream));
+}
+
+gdn_status gdn_step_fwd(const gdn_shape* s, const void* x, int64_t ldx, const float* w_conv,
+                        const void* a, int64_t lda, const void* b, int64_t ldb,
+                        const float* A_log, const float* dt_bias, const void* z, int64_t ldz,
+                        const float* w_norm, float scale, float l2_eps, float norm_eps,
+                        gdn_act act, const gdn_cache* cache, const int32_t* slot_in,
+                        const int32_t* slot_out, const int32_t* slot_tok, const int32_t* cu,
+                        void* out, void* stream) {
+  GDN_TRY(check_shape(s));
+  GDN_TRY(check_cache(s, cache, true));
+  GDN_TRY(check_ptrs({w_conv, w_norm}));
+  if (!A_log || !dt_bias || !cu) return GDN_ERR_INVALID_ARG;
+  if (s->total_tokens > 0) {
+    GDN_TRY(check_ptrs({x, z, out}));
+    if (!a || !b) return GDN_ERR_INVALID_ARG;
+  }
+  if (act != GDN_ACT_SILU && act != GDN_ACT_SIGMOID) return GDN_ERR_INVALID_ARG;
+  if (!(l2_eps >= 0.f) || !(norm_eps >= 0.f) || lda < s->hv || ldb < s->hv)
+    return GDN_ERR_INVALID_ARG;
+  GDN_TRY(check_ld(ldx, channels(s)));
+  GDN_TRY(check_ld(ldz, (int64_t)s->hv * s->dv));
+  StepArgs p = {};
+  p.x = x; p.ldx = ldx; p.w_conv = w_conv; p.a = a; p.lda = lda; p.b = b; p.ldb = ldb;
+  p.A_log = A_log; p.dt_bias = dt_bias; p.z = z; p.ldz = ldz; p.w_norm = w_norm;
+  p.scale = scale; p.l2_eps = l2_eps; p.norm_eps = norm_eps; p.act = (int)act; p.cache = *cache;
+  p.slot_in = slot_in; p.slot_out = slot_out; p.slot_tok = slot_tok; p.cu = cu; p.out = out;
+  return launched(launch_step(*s, p, (hipStream_t)stream));
+}
+
+gdn_status gdn_check_slots(const gdn_shape* s, int32_t n_slots, const int32_t* slot_in,
+                           const int32_t* slot_out, const int32_t* slot_tok, const int32_t* cu,
+                           int32_t* violations, void* stream) {
+  GDN_TRY(check_shape(s));
+  if (n_slots < 1 || !cu || !violations) return GDN_ERR_INVALID_ARG;
+  if (((uintptr_t)violations & 3u) != 0) return GDN_ERR_ALIGNMENT;
+  return launched(launch_check_slots(*s, n_slots, slot_in, slot_out, slot_tok, cu, violations,
+                                     (hipStream_t)stream));
+}
+
+gdn_status gdn_cache_copy(const void* src, int64_t src_stride, int32_t n_src,
+                          const int32_t* src_idx, void* dst, int64_t dst_stride, int32_t n_dst,
+                          const int32_t* dst_idx, int64_t bytes, int32_t n, void* stream) {
+  if (n < 0) return GDN_ERR_INVALID_ARG;
+  GDN_TRY(check_slot_rows(src, src_stride, bytes, n_src));
+  GDN_TRY(check_slot_rows(dst, dst_stride, bytes, n_dst));
+  return launched(launch_cache_copy(src, src_stride, n_src, src_idx, dst, dst_stride, n_dst,
+                                    dst_idx, bytes, n, (hipStream_t)stream));
+}
+
+size_t gdn_cache_workspace(int32_t n_slots) { return n_slots < 1 ? 0 : cache_ws_bytes(n_slots); }
+
+gdn_status gdn_cache_fork(void* base, int64_t stride, int32_t n_slots, int32_t* refs,
+                          const int32_t* src, int32_t n, int32_t* dst, void* ws, size_t ws_bytes,
+                          void* stream) {
+  if (n < 0) return GDN_ERR_INVALID_ARG;
+  GDN_TRY(check_slot_rows(base, stride, stride, n_slots));
+  if (!refs || (n > 0 && (!src || !dst))) return GDN_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < cache_ws_bytes(n_slots) || !aligned16(ws)) return GDN_ERR_WORKSPACE;
+  return launched(launch_cache_fork(base, stride, n_slots, refs, src, n, dst, ws,
+                                    (hipStream_t)stream));
+}
+
+gdn_status gdn_cache_retain(int32_t* refs, int32_t n_slots, const int32_t* slots, int32_t n,
+                            void* stream) {
+  if (!refs || n_slots < 1 || n < 0 || (n > 0 && !slots)) return GDN_ERR_INVALID_ARG;
+  return launched(launch_cache_count(refs, n_slots, slots, n, 1, (hipStream_t)stream));
+}
+
+gdn_status gdn_cache_release(int32_t* refs, int32_t n_slots, const int32_t* slots, int32_t n,
+                             void* stream) {
+  if (!refs || n_slots < 1 || n < 0 || (n > 0 && !slots)) return GDN_ERR_INVALID_ARG;
+  return launched(launch_cache_count(refs, n_slots, slots, n, -1, (hipStream_t)stream));
+}
+
+gdn_status gdn_cache_compact(void* base, int64_t stride, int32_t n_slots, int32_t* refs,
+                             int32_t* remap, int32_t* table, int32_t n_table, void* ws,
+                             size_t ws_bytes, void* stream) {
+  if (n_table < 0) return GDN_ERR_INVALID_ARG;
+  GDN_TRY(check_slot_rows(base, stride, stride, n_slots));
+  if (!refs || !remap || (n_table > 0 && !table)) return GDN_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < cache_ws_bytes(n_slots) || !aligned16(ws)) return GDN_ERR_WORKSPACE;
+  return launched(launch_cache_compact(base, stride, n_slots, refs, remap, table, n_table, ws,
+                                       (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -113,4 +113,43 @@ hipError_t launch_chunk_bwd(const gdn_shape& s, const void* q, const void* k, co
 
 hipError_t launch_check_cu(const gdn_shape& s, const int32_t* cu, int32_t* out, hipStream_t st);
 
+// The recurrent form over cached states (step.hip).  One argument block for
+// the rule alone (q, k, v, g, beta, out = o) and the whole step (x ... w_norm).
+struct StepArgs {
+  const void *q, *k, *v;                        // rule: q, k, v rows
+  int64_t ldq, ldk, ldv;
+  const float *g, *beta;
+  const void *x, *a, *b, *z;                    // step
+  int64_t ldx, lda, ldb, ldz;
+  const float *w_conv, *A_log, *dt_bias, *w_norm;
+  float scale, l2_eps, norm_eps;
+  int act;
+  gdn_cache cache;
+  const int32_t *slot_in, *slot_out, *slot_tok, *cu;
+  void* out;
+};
+hipError_t launch_recurrent(const gdn_shape& s, const StepArgs& a, hipStream_t st);
+hipError_t launch_step(const gdn_shape& s, const StepArgs& a, hipStream_t st);
+hipError_t launch_check_slots(const gdn_shape& s, int32_t n_slots, const int32_t* slot_in,
+                              const int32_t* slot_out, const int32_t* slot_tok, const int32_t* cu,
+                              int32_t* out, hipStream_t st);
+
+// Cache upkeep (cache.hip).  The workspace holds a list of moves: their
+// count (16 bytes), then cache_room sources and as many destinations; there
+// are never more moves than slots.
+inline int64_t cache_room(int32_t n_slots) { return ((int64_t)n_slots + 3) / 4 * 4; }
+inline size_t cache_ws_bytes(int32_t n_slots) {
+  return 16 + 2 * sizeof(int32_t) * (size_t)cache_room(n_slots);
+}
+hipError_t launch_cache_copy(const void* src, int64_t src_stride, int32_t n_src,
+                             const int32_t* src_idx, void* dst, int64_t dst_stride, int32_t n_dst,
+                             const int32_t* dst_idx, int64_t bytes, int32_t n, hipStream_t st);
+hipError_t launch_cache_fork(void* base, int64_t stride, int32_t n_slots, int32_t* refs,
+                             const int32_t* src, int32_t n, int32_t* dst, void* ws, hipStream_t st);
+hipError_t launch_cache_count(int32_t* refs, int32_t n_slots, const int32_t* slots, int32_t n,
+                              int delta, hipStream_t st);
+hipError_t launch_cache_compact(void* base, int64_t stride, int32_t n_slots, int32_t* refs,
+                                int32_t* remap, int32_t* table, int32_t n_table, void* ws,
+                                hipStream_t st);
+
 }  // namespace gdn

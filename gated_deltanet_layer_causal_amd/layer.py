@@ -15,6 +15,9 @@ from typing import Optional
 import torch
 
 from . import capi as L
+from .state_cache import GDNStateCache
+
+__all__ = ["CoreConfig", "GDNCore", "GDNLayer", "GDNStateCache"]
 
 
 @dataclasses.dataclass
@@ -29,6 +32,7 @@ class CoreConfig:
     norm_eps: float = 1e-6
     seg_chunks: int = 0                  # segment-parallel state scan (0: the library decides)
     check_cu_seqlens: bool = False       # debug: check the cu_seqlens contract (synchronises)
+    check_slots: bool = False            # debug: check the slot tables of cached calls (synchronises)
 
     @property
     def channels(self):
@@ -143,6 +147,81 @@ class GDNCore:
         if save_states:
             saved["chunk_ws"] = wc
         return saved
+
+    # ------------------------------------------------------------ serving
+    def step(self, x, w_conv, a, b, A_log, dt_bias, z, w_norm, cu_seqlens, cache, slot_in,
+             slot_out=None, slot_tok=None, layer=0):
+        """The core for the next tokens of cached sequences (usually one each):
+        x [T, C], a, b [T, hv], z [T, hv, d] or [T, hv * d], rows may be
+        strided -> out [T, hv, d].  Sequence n's state is read from slot
+        slot_in[n] of the GDNStateCache (-1: a new sequence) and written to
+        slot_out[n] (default: in place; -1: nowhere); slot_tok [T] names slots
+        for the states after single tokens (-1: none).  Rows behind
+        cu_seqlens[-1] are left alone, so a batch may be padded.  Results
+        match forward() up to rounding: nothing is rounded between the conv,
+        the rule and the norm.  No workspace, nothing synchronises."""
+        c = self.cfg
+        T = x.shape[0]
+        sh = self.shape(T, cu_seqlens.numel() - 1)
+        slot_out = slot_in if slot_out is None else slot_out
+        if c.check_slots:
+            self.check_slots(sh, cache, slot_in, slot_out, slot_tok, cu_seqlens)
+        out = torch.empty((T, c.hv, c.d), dtype=c.dtype, device=x.device)
+        L.gdn_step_fwd(sh, x, w_conv, a, b, A_log, dt_bias, z.view(T, c.hv * c.d), w_norm, c.q_scale,
+                       cache.layer(layer), slot_in, slot_out, slot_tok, cu_seqlens, out, c.l2_eps,
+                       c.norm_eps, c.act)
+        return out
+
+    def recurrent(self, q, k, v, g, beta, cu_seqlens, cache, slot_in, slot_out=None, slot_tok=None,
+                  layer=0):
+        """The gated delta rule alone, token by token over cached states: q, k
+        [T, hk * d] and v [T, hv * d] (rows may be strided), g, beta fp32
+        [T, hv] -> o [T, hv, d]; the slots as in step()."""
+        c = self.cfg
+        T = q.shape[0]
+        sh = self.shape(T, cu_seqlens.numel() - 1)
+        slot_out = slot_in if slot_out is None else slot_out
+        if c.check_slots:
+            self.check_slots(sh, cache, slot_in, slot_out, slot_tok, cu_seqlens)
+        o = torch.empty((T, c.hv, c.d), dtype=c.dtype, device=q.device)
+        L.gdn_recurrent_fwd(sh, q, k, v, g, beta, c.q_scale, cache.layer(layer), slot_in, slot_out,
+                            slot_tok, cu_seqlens, o)
+        return o
+
+    def prefill(self, x, w_conv, a, b, A_log, dt_bias, z, w_norm, cu_seqlens, cache, slot_in,
+                slot_out=None, layer=0):
+        """step() for long pieces: the chunked forward from and into slots
+        (contiguous a, b, z as forward(); cu_seqlens[-1] = T).  A slot_in
+        outside the cache gives NaN, a slot_out outside it is not written."""
+        c = self.cfg
+        n_seq = cu_seqlens.numel() - 1
+        slot_out = slot_in if slot_out is None else slot_out
+        if c.check_slots:
+            self.check_slots(self.shape(x.shape[0], n_seq), cache, slot_in, slot_out, None, cu_seqlens)
+        S, conv = cache.S(layer), cache.conv(layer)
+        S0 = torch.empty((n_seq,) + S.shape[1:], dtype=S.dtype, device=S.device)
+        rows = torch.empty((n_seq,) + conv.shape[1:], dtype=conv.dtype, device=S.device)
+        L.gdn_cache_copy(S, S0, src_idx=slot_in)
+        L.gdn_cache_copy(conv, rows, src_idx=slot_in)
+        f = self.forward(x, w_conv, a, b, A_log, dt_bias, z, w_norm, cu_seqlens, S0=S0,
+                         want_final=True, save_states=False, conv_state=rows, want_conv_state=True)
+        L.gdn_cache_copy(f["S_final"], S, dst_idx=slot_out)
+        L.gdn_cache_copy(f["conv_state_out"], conv, dst_idx=slot_out)
+        return f["out"]
+
+    def check_slots(self, sh, cache, slot_in, slot_out, slot_tok, cu_seqlens):
+        """Runs gdn_check_slots and raises ValueError naming what is wrong
+        with the slot tables (this waits for the stream)."""
+        out = torch.empty(1, dtype=torch.int32, device=cu_seqlens.device)
+        L.gdn_check_slots(sh, cache.n_slots, slot_in, slot_out, slot_tok, cu_seqlens, out)
+        bad = int(out.item())
+        if bad:
+            why = [msg for bit, msg in ((L.SLOT_RANGE, "a slot outside the cache"),
+                                        (L.SLOT_WRITTEN_TWICE, "a slot written twice"),
+                                        (L.SLOT_WRITTEN_AND_READ,
+                                         "a slot written by one sequence and read by another"))
+                   if bad & bit]
+            raise ValueError("invalid slot tables: " + "; ".join(why))
 
     def check_cu_seqlens(self, sh, cu_seqlens):
         """Runs gdn_check_cu_seqlens and raises ValueError naming each broken
@@ -260,6 +339,18 @@ class GDNLayer:
             Y = out @ self.W["out"].t()
         f.update(x=x, z=z, a=a, b=b, Y=Y)
         return f
+
+    def step(self, X, w_conv, A_log, dt_bias, w_norm, cu_seqlens, cache, slot_in, slot_out=None,
+             slot_tok=None, layer=0):
+        """The layer for the next tokens of cached sequences: X [T, H] ->
+        Y [T, H]; the slots as in GDNCore.step."""
+        c = self.cfg
+        x = X @ self.W["x"].t()
+        z = X @ self.W["z"].t()
+        ab = X @ self.W["ab"].t()
+        out = self.core.step(x, w_conv, ab[:, :c.hv], ab[:, c.hv:], A_log, dt_bias, z, w_norm,
+                             cu_seqlens, cache, slot_in, slot_out, slot_tok, layer)
+        return out.view(X.shape[0], c.hv * c.d) @ self.W["out"].t()
 
     def backward(self, saved, X, w_conv, A_log, dt_bias, w_norm, cu_seqlens, dY, S0=None,
                  dS_final=None, timer=None):

@@ -304,6 +304,128 @@ size_t gdn_gated_norm_bwd_workspace(int64_t rows, int32_t dv);
 gdn_status gdn_check_cu_seqlens(const gdn_shape* shape, const int32_t* cu_seqlens,
                                 int32_t* violations, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving: the recurrent form over a cache of states.
+ *
+ * A cache holds n_slots slots.  Slot i of one layer is the state of one
+ * sequence: S + i * S_stride, fp32 [hv][dv][dk], and conv + i * conv_stride,
+ * the last three conv input rows [3][C_ch] in the storage type, oldest first
+ * (as conv_state of gdn_conv_fwd_state).  Strides are counted in elements, so
+ * that several layers' states can share a slot; both pointers and strides are
+ * multiples of 16 bytes, S_stride >= hv*dv*dk, conv_stride >= 3*C_ch.  conv
+ * is not read by gdn_recurrent_fwd.
+ *
+ * Slot tables are device int32:
+ *   slot_in  [n_seq]  where sequence n's state before its first token is; an
+ *            entry < 0 (or slot_in == NULL): the zero state and zero rows.
+ *   slot_out [n_seq]  where its state after its last token goes; < 0 (or
+ *            NULL): nowhere.  slot_out[n] == slot_in[n] updates in place; a
+ *            sequence of no tokens passes its state through.
+ *   slot_tok [T]      where the state after token t goes as well; < 0 (or
+ *            NULL): nowhere.  With draft tokens this keeps every state that a
+ *            rejected draft may fall back to.
+ * An entry of slot_in or slot_out >= n_slots makes the sequence's output rows
+ * NaN and writes no state of it; an entry of slot_tok >= n_slots writes
+ * nothing.  No two states of a call may go to one slot, and no slot that one
+ * sequence writes may be read by another: such calls stay inside the cache
+ * but give undefined values (gdn_check_slots finds them).  Several sequences
+ * may read one slot that none of them writes.
+ *
+ * Unlike elsewhere cu[n_seq] may be less than total_tokens: rows behind the
+ * last sequence are neither read nor written, and entries of cu_seqlens are
+ * clamped to [0, total_tokens], so a batch can be padded to a fixed size (for
+ * a captured graph) with empty sequences and unused rows.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  float* S;
+  int64_t S_stride;
+  void* conv;
+  int64_t conv_stride;
+  int32_t n_slots; /* >= 1 */
+} gdn_cache;
+
+/* The gated delta rule (as gdn_chunk_fwd), token by token:
+ *   S_t = exp(g_t) S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T
+ *   o_t = S_t (scale * q_t)
+ * in fp32 whatever the storage type, with no limit on the range of the data.
+ * q, k, v, g, beta and o as gdn_chunk_fwd; every dtype at dk = dv = 32 and 128.
+ * For single tokens up to short pieces; gdn_chunk_fwd is faster for long ones
+ * (its state goes in and out of a cache by gdn_cache_copy). */
+gdn_status gdn_recurrent_fwd(const gdn_shape* shape, const void* q, const void* k, const void* v,
+                             int64_t ldq, int64_t ldk, int64_t ldv, const float* g,
+                             const float* beta, float scale, const gdn_cache* cache,
+                             const int32_t* slot_in, const int32_t* slot_out,
+                             const int32_t* slot_tok, const int32_t* cu_seqlens, void* o,
+                             void* stream);
+
+/* The whole core for the next tokens of cached sequences: conv (with its
+ * carried rows), SiLU and L2 as gdn_conv_fwd_state, gate as gdn_gate_fwd,
+ * the rule as above and the norm as gdn_gated_norm_fwd.  Nothing is rounded
+ * between them.  x [T][ldx], a [T][lda], b [T][ldb], z [T][ldz] in
+ * shape->dtype (ldx, ldz multiples of 8; lda, ldb >= hv), out [T][hv*dv]. */
+gdn_status gdn_step_fwd(const gdn_shape* shape, const void* x, int64_t ldx, const float* w_conv,
+                        const void* a, int64_t lda, const void* b, int64_t ldb,
+                        const float* A_log, const float* dt_bias, const void* z, int64_t ldz,
+                        const float* w_norm, float scale, float l2_eps, float norm_eps,
+                        gdn_act act, const gdn_cache* cache, const int32_t* slot_in,
+                        const int32_t* slot_out, const int32_t* slot_tok,
+                        const int32_t* cu_seqlens, void* out, void* stream);
+
+/* Check of the slot tables (device; slot_in, slot_out and slot_tok may be
+ * NULL): writes to *violations (device int32) a bit mask: 1 = an entry >=
+ * n_slots, 2 = a slot written twice, 4 = a slot that one sequence writes and
+ * another reads; 0 for valid tables.  Entries that no token reaches
+ * (slot_tok behind the last sequence) are not looked at. */
+gdn_status gdn_check_slots(const gdn_shape* shape, int32_t n_slots, const int32_t* slot_in,
+                           const int32_t* slot_out, const int32_t* slot_tok,
+                           const int32_t* cu_seqlens, int32_t* violations, void* stream);
+
+/* Upkeep of a cache whose slots are rows of bytes: slot i at
+ * base + i * stride.  Pointers, strides and sizes are multiples of 16 bytes;
+ * index tables are device int32.  refs [n_slots] counts each slot's users
+ * (0: the slot is free).  Everything is decided on the device: no call waits
+ * for it.  Calls on one cache must be ordered (one stream, or events).
+ *
+ * gdn_cache_copy: for i in [0, n): dst slot dst_idx[i] = src slot src_idx[i],
+ * `bytes` of each.  src_idx == NULL: slot i, dst_idx == NULL: slot i.  An
+ * entry of src_idx < 0 gives zeros, one >= n_src all bits set (NaN in every
+ * storage type); where dst_idx is < 0 or >= n_dst nothing is written.  No slot
+ * may be written twice, nor written and read, by one call (src and dst may be
+ * the same cache otherwise). */
+gdn_status gdn_cache_copy(const void* src, int64_t src_stride, int32_t n_src,
+                          const int32_t* src_idx, void* dst, int64_t dst_stride, int32_t n_dst,
+                          const int32_t* dst_idx, int64_t bytes, int32_t n, void* stream);
+
+/* gdn_cache_fork: takes a free slot for each request i in [0, n), in order,
+ * lowest slots first, and fills it: a copy of slot src[i], or zeros where
+ * src[i] == -1.  dst[i] receives the slot, and its count becomes 1.  Where
+ * src[i] < -1 (no request), src[i] >= n_slots, src[i] is a free slot, or no
+ * free slot is left, dst[i] = -1 and nothing is taken. */
+gdn_status gdn_cache_fork(void* base, int64_t stride, int32_t n_slots, int32_t* refs,
+                          const int32_t* src, int32_t n, int32_t* dst, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/* One more (retain) or one less (release) user of each slot in slots [n]; a
+ * slot named twice counts twice.  Entries outside [0, n_slots) and free slots
+ * are left alone, so a count never falls below 0 and retaining a free slot
+ * does not take it. */
+gdn_status gdn_cache_retain(int32_t* refs, int32_t n_slots, const int32_t* slots, int32_t n,
+                            void* stream);
+gdn_status gdn_cache_release(int32_t* refs, int32_t n_slots, const int32_t* slots, int32_t n,
+                             void* stream);
+
+/* gdn_cache_compact: moves the live slots into [0, live count) with as few
+ * moves as there can be: the m-th live slot at or behind that limit goes into
+ * the m-th free slot before it, the others stay.  remap [n_slots] receives
+ * each slot's new place (-1: it was free); counts move along.  Every entry of
+ * table [n_table] (NULL: none) in [0, n_slots) is replaced by its remap. */
+gdn_status gdn_cache_compact(void* base, int64_t stride, int32_t n_slots, int32_t* refs,
+                             int32_t* remap, int32_t* table, int32_t n_table, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* Workspace of gdn_cache_fork and gdn_cache_compact. */
+size_t gdn_cache_workspace(int32_t n_slots);
+
 #ifdef __cplusplus
 }
 #endif
