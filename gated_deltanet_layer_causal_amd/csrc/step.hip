@@ -2,31 +2,39 @@
 // rule token by token (gdn_recurrent_fwd), and the whole core for the next
 // tokens of every sequence (gdn_step_fwd).
 //
-// One workgroup owns one (sequence, value head).  The head's state S (D x D,
-// fp32) stays in registers from its load to its store, so a call reads and
-// writes each state once however many tokens a sequence has:
+// One workgroup owns one sequence and some value heads of one key head: the
+// step all of them (so that it alone reads and writes their conv rows), HW at
+// a time, the rule one.  A head's state S (D x D, fp32) stays in registers
+// from its load to its store, so a call reads and writes each state once
+// however many tokens a sequence has:
 //   s = S_{t-1} k,  r = S_{t-1} q   (both from the old state, reduced together)
 //   delta = beta (v - e^g s)
 //   o = e^g r + delta (k . q),  S_t = e^g S_{t-1} + delta k^T
 // which is the rule with o_t = S_t q_t expanded; q carries the scale.
 //
-// Tokens go through in blocks of STEP_TB: all threads form q, k, v (conv,
-// SiLU, L2), e^g and beta of the block in LDS, then each thread walks the
-// block's tokens for its part of the state, then all threads norm the block's
-// outputs.
-#include "chunk_common.h"
+// The state waves do only that.  The helper waves form q, k, v (conv, SiLU,
+// L2), e^g and beta of a block of STEP_TB tokens in LDS while the state waves
+// load the state or walk the block before, and norm and store the outputs of
+// the block behind them: neither their loads nor their arithmetic sit between
+// a state's load and its store.  One barrier per block joins the two; the
+// blocks of q, k, v alternate between two buffers.
+#include "chunk_stream.h"
 #include "launch.h"
 
 namespace gdn {
 
-constexpr int STEP_TB = 8;   // tokens per block
+constexpr int STEP_TB = 8;             // tokens per block
+constexpr unsigned STEP_THROUGH = 128; // workgroups from which states are written through
 
 // Tokens of sequence n, clamped so that no table can lead outside [0, T].
-__device__ __forceinline__ void token_range(const int32_t* cu, int n, int64_t T, int64_t& t0,
-                                            int64_t& t1) {
-  const int64_t a = cu[n], b = cu[n + 1];
+__device__ __forceinline__ void token_range(const int32_t* cu, int n, int T, int& t0, int& t1) {
+  const int a = __builtin_amdgcn_readfirstlane(cu[n]), b = __builtin_amdgcn_readfirstlane(cu[n + 1]);
   t0 = a < 0 ? 0 : a > T ? T : a;
   t1 = b < t0 ? t0 : b > T ? T : b;
+}
+// Entry n of a slot table (uniform n); -1 without one.
+__device__ __forceinline__ int slot_of(const int32_t* table, int n) {
+  return table ? __builtin_amdgcn_readfirstlane(table[n]) : -1;
 }
 
 __device__ __forceinline__ float softplus_full(float x) {
@@ -41,269 +49,424 @@ template <int N> __device__ __forceinline__ float lanes_sum(float x) {
 
 // Thread layout of the state: LPR lanes share a row of D columns; a lane
 // holds the columns 4 l + 4 LPR c + (0..3), c = 0..3, of R rows.
-template <int D> struct StepGeo {
+template <int D, int HW> struct StepGeo {
   static constexpr int LPR = D / 16;
   static constexpr int R = D == 128 ? 4 : 1;
   static constexpr int RPW = 64 / LPR;              // rows per wave and row slot
-  static constexpr int WAVES = D / (RPW * R);
-  static constexpr int THREADS = 64 * WAVES;
+  static constexpr int WAVES = D / (RPW * R);       // state waves of a head
+  // helper lanes: 8 channels each of q, k and HW times v, then a gate each
+  static constexpr int CONV_LANES = (2 + HW) * D / 8, HELPERS = (CONV_LANES + HW * STEP_TB + 63) / 64;
+  static constexpr int THREADS = 64 * (HW * WAVES + HELPERS);
 };
 
-template <typename T, int D, bool STEP>
-__global__ void __launch_bounds__(StepGeo<D>::THREADS) step_kernel(StepArgs p, int hk, int hv,
-                                                                   int64_t T_tok) {
-  typedef StepGeo<D> G;
-  constexpr int NT = G::THREADS, G8 = D / 8;
-  __shared__ float sq[STEP_TB][D], sk[STEP_TB][D], sv[STEP_TB][D];
-  __shared__ float seg[STEP_TB], sbeta[STEP_TB];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int n = blockIdx.x / hv, h = blockIdx.x % hv, kh = h / (hv / hk);
-  const int C = 2 * hk * D + hv * D;
-  int64_t t0, t1;
-  token_range(p.cu, n, T_tok, t0, t1);
-  const int s_in = p.slot_in ? p.slot_in[n] : -1;
-  const int s_out = p.slot_out ? p.slot_out[n] : -1;
-  T* out = (T*)p.out;
-  if (s_in >= p.cache.n_slots || s_out >= p.cache.n_slots) {   // a bad slot: NaN rows, no state
-    for (int64_t i = tid; i < (t1 - t0) * D; i += NT)
-      out[(t0 + i / D) * hv * D + (int64_t)h * D + i % D] = from_f<T>(__builtin_nanf(""));
-    return;
-  }
-  if (t0 == t1 && (s_out < 0 || s_out == s_in)) return;
+template <int D, int HW> struct StepLds {
+  float q[2][STEP_TB][D], k[2][STEP_TB][D], v[2][HW][STEP_TB][D];   // v, then o in its place
+  float eg[2][HW][STEP_TB], beta[2][HW][STEP_TB];
+  int tok[2][STEP_TB];                                              // slot_tok, -1: none
+};
 
-  const int row0 = wave * (G::RPW * G::R) + lane / G::LPR;
-  const int col0 = 4 * (lane % G::LPR);
-  float S[G::R][16];
-  if (s_in >= 0) {
-    const float* src = p.cache.S + (int64_t)s_in * p.cache.S_stride + (int64_t)h * D * D;
-#pragma unroll
-    for (int j = 0; j < G::R; ++j)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float4 v = *reinterpret_cast<const float4*>(src + (row0 + j * G::RPW) * D + col0 + 4 * G::LPR * c);
-        S[j][4 * c] = v.x; S[j][4 * c + 1] = v.y; S[j][4 * c + 2] = v.z; S[j][4 * c + 3] = v.w;
-      }
-  } else {
-#pragma unroll
-    for (int j = 0; j < G::R; ++j)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) S[j][i] = 0.f;
+// What a workgroup works on: value heads h0 .. h1 - 1 of key head kh, HW at a
+// time (a round), each round in nb blocks of STEP_TB tokens; item i = (round
+// i / nb, block i % nb).
+struct StepSpan {
+  int t0, t1, s_in, s_out, h0, h1, kh, nb, items;
+};
+
+// A head's state: its load, its tokens, its store.
+template <int D> struct StepState {
+  typedef StepGeo<D, 1> G;
+  floatx4 S[G::R][4];
+  uint32_t row0, col0, at;   // first row, first column, and the byte they are at
+
+  __device__ __forceinline__ StepState(int wave, int lane)
+      : row0(wave * (G::RPW * G::R) + lane / G::LPR), col0(4 * (lane % G::LPR)), at(4 * (row0 * D + col0)) {}
+
+  // Each state passes through once, in whole lines: non-temporal both ways (the
+  // rule, 200 sequences x 48 heads, bf16: 251 us with plain accesses, 245 us
+  // with the hint on one side, 220 us on both).  Stores that are written
+  // through as well (sc1) are faster where the chip is full (212 us) and
+  // slower from a few workgroups (the step, one sequence x 48 heads: 9.3 us
+  // without, 11.8 us with); see STEP_THROUGH.
+  __device__ __forceinline__ static __amdgpu_buffer_rsrc_t head(const StepArgs& p, int slot, int h) {
+    return buffer_of(p.cache.S + (int64_t)slot * p.cache.S_stride + (int64_t)h * D * D, 4 * D * D);
   }
-  auto put = [&](int slot) {
-    float* dst = p.cache.S + (int64_t)slot * p.cache.S_stride + (int64_t)h * D * D;
+  __device__ __forceinline__ void load(const StepArgs& p, int slot, int h) {
+    if (slot >= 0) {
+      const auto rs = head(p, slot, h);
+#pragma unroll
+      for (int j = 0; j < G::R; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          S[j][c] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(
+              rs, at + 16 * G::LPR * c, 4 * j * G::RPW * D, CACHE_NT));
+    } else {
+#pragma unroll
+      for (int j = 0; j < G::R; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) S[j][c] = zero4();
+    }
+  }
+  template <int AUX>
+  __device__ __forceinline__ void store_as(const __amdgpu_buffer_rsrc_t rs) const {
 #pragma unroll
     for (int j = 0; j < G::R; ++j)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        *reinterpret_cast<float4*>(dst + (row0 + j * G::RPW) * D + col0 + 4 * G::LPR * c) =
-            make_float4(S[j][4 * c], S[j][4 * c + 1], S[j][4 * c + 2], S[j][4 * c + 3]);
-  };
-
-  for (int64_t tb = t0; tb < t1; tb += STEP_TB) {
-    const int nt = t1 - tb < STEP_TB ? (int)(t1 - tb) : STEP_TB;
-    // q, k, v of the block: job = (token, 8 channels of q, k or v)
-    for (int job = tid; job < nt * 3 * G8; job += NT) {
-      const int i = job / (3 * G8), part = job % (3 * G8) / G8, e = job % G8 * 8;
-      const int64_t t = tb + i;
-      f8 y;
-      if constexpr (STEP) {
-        const int ch = (part == 0 ? kh : part == 1 ? hk + kh : 2 * hk + h) * D + e;
-        float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[j][c]), rs, at + 16 * G::LPR * c,
+                                               4 * j * G::RPW * D, AUX);
+  }
+  __device__ __forceinline__ void store(const StepArgs& p, int slot, int h) const {
+    const auto rs = head(p, slot, h);
+    if (gridDim.x >= STEP_THROUGH) store_as<CACHE_NT | CACHE_SC1>(rs);
+    else store_as<CACHE_NT>(rs);
+  }
+  // One token; its outputs take the place of v.  k and q pass through
+  // registers 4 columns at a time, and k again for the update: 16 columns of
+  // both would not fit beside the state.
+  __device__ __forceinline__ void token(const float* sq, const float* sk, float* sv, float eg,
+                                        float beta, int lane) {
+    float kq = 0.f, s[G::R], r[G::R], v[G::R];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t tr = t - 3 + j;
-          f8 xr;
-          if (tr >= t0) {
-            xr = load8((const T*)p.x + tr * p.ldx + ch);
-          } else if (s_in >= 0) {
-            xr = load8((const T*)p.cache.conv + (int64_t)s_in * p.cache.conv_stride +
-                       (tr - t0 + 3) * C + ch);
+    for (int j = 0; j < G::R; ++j) {
+      s[j] = r[j] = 0.f;
+      v[j] = sv[row0 + j * G::RPW];
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const floatx4 k = *reinterpret_cast<const floatx4*>(sk + col0 + 4 * G::LPR * c);
+      const floatx4 q = *reinterpret_cast<const floatx4*>(sq + col0 + 4 * G::LPR * c);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        kq = fmaf(k[m], q[m], kq);
+#pragma unroll
+        for (int j = 0; j < G::R; ++j) {
+          s[j] = fmaf(S[j][c][m], k[m], s[j]);
+          r[j] = fmaf(S[j][c][m], q[m], r[j]);
+        }
+      }
+    }
+    kq = lanes_sum<G::LPR>(kq);
+#pragma unroll
+    for (int j = 0; j < G::R; ++j) {
+      s[j] = lanes_sum<G::LPR>(s[j]);
+      r[j] = lanes_sum<G::LPR>(r[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < G::R; ++j) {
+      s[j] = beta * (v[j] - eg * s[j]);        // delta
+      r[j] = fmaf(s[j], kq, eg * r[j]);        // o
+    }
+    if (lane % G::LPR == 0) {                  // only a row's own lanes read its v
+#pragma unroll
+      for (int j = 0; j < G::R; ++j) sv[row0 + j * G::RPW] = r[j];
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const floatx4 k = *reinterpret_cast<const floatx4*>(sk + col0 + 4 * G::LPR * c);
+#pragma unroll
+      for (int j = 0; j < G::R; ++j)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) S[j][c][m] = fmaf(s[j], k[m], eg * S[j][c][m]);
+    }
+  }
+};
+
+template <int D, int HW>
+__device__ __forceinline__ void step_state_wave(const StepArgs& p, const StepSpan& w,
+                                                StepLds<D, HW>& lds, int wave, int lane) {
+  constexpr int WAVES = StepGeo<D, HW>::WAVES;
+  const int hw = wave / WAVES;                    // which of the round's heads
+  StepState<D> st(wave % WAVES, lane);
+  int h = w.h0 + hw, blk = 0;
+  if (h < w.h1) st.load(p, w.s_in, h);
+  for (int i = 0; i < w.items; ++i) {
+    const int buf = i & 1;
+    const int left = w.t1 - w.t0 - blk * STEP_TB;
+    const int nt = h >= w.h1 ? 0 : left < STEP_TB ? left : STEP_TB;
+    __syncthreads();   // q, k, v of item i are in LDS
+    for (int j = 0; j < nt; ++j) {
+      st.token(lds.q[buf][j], lds.k[buf][j], lds.v[buf][hw][j], lds.eg[buf][hw][j],
+               lds.beta[buf][hw][j], lane);
+      if (p.slot_tok) {
+        const int slot = __builtin_amdgcn_readfirstlane(lds.tok[buf][j]);
+        if (slot >= 0) st.store(p, slot, h);
+      }
+    }
+    if (++blk == w.nb) {
+      if (h < w.h1 && w.s_out >= 0) st.store(p, w.s_out, h);
+      blk = 0;
+      h += HW;
+      if (h < w.h1) st.load(p, w.s_in, h);
+    }
+  }
+  __syncthreads();     // the last outputs are in LDS
+}
+
+// The helper waves; `lane` counts through them.  A conv lane forms 8 channels
+// of q, k or one head's v of every token, with the conv's window in
+// registers; the lanes behind them form the gate of one token and head each.
+template <typename T, int D, int HW, bool STEP>
+__device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSpan& w,
+                                                 StepLds<D, HW>& lds, int hk, int hv, int lane) {
+  typedef StepGeo<D, HW> G;
+  constexpr int G8 = D / 8, NL = 64 * G::HELPERS, NP = (HW * STEP_TB * G8 + NL - 1) / NL;
+  constexpr int AHEAD = (sizeof(T) == 2 ? 4 : 2) / (HW == 3 ? 2 : 1);   // rows of x in flight (registers)
+  const int C = 2 * hk * D + hv * D;
+  const int part = lane / G8, e = lane % G8 * 8; // part: 0 q, 1 k, 2 + i v of the round's head i
+  const int vh = part < 2 ? 0 : part - 2;
+  const int gh = (lane - G::CONV_LANES) / STEP_TB, gt = (lane - G::CONV_LANES) % STEP_TB;   // the gate's
+  T* out = (T*)p.out;
+  // rule: this lane's tensor and its row stride
+  const T* lane_src = (const T*)p.q;
+  int64_t lane_ld = p.ldq;
+  if (part == 1) { lane_src = (const T*)p.k; lane_ld = p.ldk; }
+  if (part >= 2) { lane_src = (const T*)p.v; lane_ld = p.ldv; }
+  float wr[8][4];
+  f8 x3, x2, x1;                                 // the window: x[t-3], x[t-2], x[t-1]
+  Raw8<T> z[NP];
+
+  auto prep = [&](int i) __attribute__((always_inline)) {
+    const int buf = i & 1, hr = w.h0 + i / w.nb * HW;   // the round's first head
+    const int tb = w.t0 + i % w.nb * STEP_TB;
+    const int nt = w.t1 - tb < STEP_TB ? w.t1 - tb : STEP_TB;
+    if (lane < G::CONV_LANES) {
+      const int h = hr + vh;
+      if (part >= 2 && h >= w.h1) return;
+      // this lane's channel: of x, or of q, k or v
+      const int ch = (STEP ? part == 0 ? w.kh : part == 1 ? hk + w.kh : 2 * hk + h : part < 2 ? w.kh : h) * D + e;
+      float(*dst)[D] = part == 0 ? lds.q[buf] : part == 1 ? lds.k[buf] : lds.v[buf][vh];
+      if constexpr (STEP) {
+        if (tb == w.t0) {
+          const T* rows = (const T*)p.cache.conv + (int64_t)w.s_in * p.cache.conv_stride + ch;
+          if (w.s_in >= 0) {
+            x3 = load8(rows);
+            x2 = load8(rows + C);
+            x1 = load8(rows + 2 * C);
           } else {
 #pragma unroll
-            for (int m = 0; m < 8; ++m) xr.v[m] = 0.f;
+            for (int m = 0; m < 8; ++m) x3.v[m] = x2.v[m] = x1.v[m] = 0.f;
           }
 #pragma unroll
-          for (int m = 0; m < 8; ++m) u[m] += p.w_conv[(int64_t)(ch + m) * 4 + j] * xr.v[m];
+          for (int m = 0; m < 8; ++m) {
+            const float4 a = *reinterpret_cast<const float4*>(p.w_conv + (int64_t)(ch + m) * 4);
+            wr[m][0] = a.x; wr[m][1] = a.y; wr[m][2] = a.z; wr[m][3] = a.w;
+          }
         }
-        float sq2 = 0.f;
+        // the rows of v's channels have served when their head has; those of
+        // q and k are read again in the next round
+        const bool put_rows = part >= 2 || hr + HW >= w.h1;
+        auto put = [&](int slot) __attribute__((always_inline)) {
+          T* rows = (T*)p.cache.conv + (int64_t)slot * p.cache.conv_stride + ch;
+          store8(rows, x3);
+          store8(rows + C, x2);
+          store8(rows + 2 * C, x1);
+        };
+        for (int j0 = 0; j0 < nt; j0 += AHEAD) {
+          Raw8<T> raw[AHEAD];
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          y.v[m] = u[m] * sigmoidf_(u[m]);
-          sq2 += y.v[m] * y.v[m];
+          for (int j = 0; j < AHEAD; ++j) {        // rows past the last token: that one again
+            const int t = tb + j0 + j < w.t1 ? tb + j0 + j : w.t1 - 1;
+            raw[j] = ld_raw8((const T*)p.x + t * p.ldx + ch);
+          }
+#pragma unroll
+          for (int j = 0; j < AHEAD; ++j) {
+            if (j0 + j < nt) {
+              const f8 x0 = raw_f8(raw[j]);
+              f8 y;
+              float ss = 0.f;
+#pragma unroll
+              for (int m = 0; m < 8; ++m) {
+                const float u = wr[m][0] * x3.v[m] + wr[m][1] * x2.v[m] + wr[m][2] * x1.v[m] + wr[m][3] * x0.v[m];
+                y.v[m] = u * sigmoidf_(u);
+                ss += y.v[m] * y.v[m];
+              }
+              ss = lane_group_sum<G8>(ss);
+              const float r = part >= 2 ? 1.f : rsqrtf(ss + p.l2_eps) * (part == 0 ? p.scale : 1.f);
+#pragma unroll
+              for (int m = 0; m < 8; ++m) y.v[m] *= r;
+              store8(&dst[j0 + j][e], y);
+              x3 = x2;
+              x2 = x1;
+              x1 = x0;
+              if (put_rows && p.slot_tok) {
+                const int slot = p.slot_tok[tb + j0 + j];
+                if (slot >= 0 && slot < p.cache.n_slots) put(slot);
+              }
+            }
+          }
         }
-        sq2 = lane_group_sum<G8>(sq2);
-        const float r = part == 2 ? 1.f : rsqrtf(sq2 + p.l2_eps) * (part == 0 ? p.scale : 1.f);
-#pragma unroll
-        for (int m = 0; m < 8; ++m) y.v[m] *= r;
+        if (put_rows && w.s_out >= 0 && tb + nt == w.t1) put(w.s_out);
       } else {
-        y = part == 0   ? load8((const T*)p.q + t * p.ldq + kh * D + e)
-            : part == 1 ? load8((const T*)p.k + t * p.ldk + kh * D + e)
-                        : load8((const T*)p.v + t * p.ldv + h * D + e);
-        if (part == 0) {
+        const float r = part == 0 ? p.scale : 1.f;
+        Raw8<T> raw[STEP_TB];                    // rows past the last token: that one again
 #pragma unroll
-          for (int m = 0; m < 8; ++m) y.v[m] *= p.scale;
-        }
+        for (int j = 0; j < STEP_TB; ++j) raw[j] = ld_raw8(lane_src + (tb + j < w.t1 ? tb + j : w.t1 - 1) * lane_ld + ch);
+#pragma unroll
+        for (int j = 0; j < STEP_TB; ++j)
+          if (j < nt) {
+            f8 y = raw_f8(raw[j]);
+#pragma unroll
+            for (int m = 0; m < 8; ++m) y.v[m] *= r;
+            store8(&dst[j][e], y);
+          }
       }
-      store8(part == 0 ? &sq[i][e] : part == 1 ? &sk[i][e] : &sv[i][e], y);
-    }
-    if (tid < nt) {
-      const int64_t t = tb + tid;
+    } else if (gh < HW && gt < nt && hr + gh < w.h1) {
+      const int h = hr + gh;
+      const int64_t t = tb + gt;
       if constexpr (STEP) {
         const float xa = to_f(((const T*)p.a)[t * p.lda + h]) + p.dt_bias[h];
-        seg[tid] = expf(-expf(p.A_log[h]) * softplus_full(xa));
-        sbeta[tid] = sigmoidf_(to_f(((const T*)p.b)[t * p.ldb + h]));
+        lds.eg[buf][gh][gt] = expf(-expf(p.A_log[h]) * softplus_full(xa));
+        lds.beta[buf][gh][gt] = sigmoidf_(to_f(((const T*)p.b)[t * p.ldb + h]));
       } else {
-        seg[tid] = expf(p.g[t * hv + h]);
-        sbeta[tid] = p.beta[t * hv + h];
+        lds.eg[buf][gh][gt] = expf(p.g[t * hv + h]);
+        lds.beta[buf][gh][gt] = p.beta[t * hv + h];
+      }
+      if (p.slot_tok && gh == 0) {
+        const int slot = p.slot_tok[t];
+        lds.tok[buf][gt] = slot < p.cache.n_slots ? slot : -1;
       }
     }
-    __syncthreads();
-    for (int i = 0; i < nt; ++i) {
-      float k[16], q[16];
+  };
+  // outputs: lane = (head, token, 8 channels)
+  auto each_out = [&](int i, auto&& f) __attribute__((always_inline)) {
+    const int tb = w.t0 + i % w.nb * STEP_TB;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float4 a = *reinterpret_cast<const float4*>(&sk[i][col0 + 4 * G::LPR * c]);
-        const float4 b = *reinterpret_cast<const float4*>(&sq[i][col0 + 4 * G::LPR * c]);
-        k[4 * c] = a.x; k[4 * c + 1] = a.y; k[4 * c + 2] = a.z; k[4 * c + 3] = a.w;
-        q[4 * c] = b.x; q[4 * c + 1] = b.y; q[4 * c + 2] = b.z; q[4 * c + 3] = b.w;
-      }
-      float kq = 0.f, s[G::R], r[G::R];
-#pragma unroll
-      for (int m = 0; m < 16; ++m) kq += k[m] * q[m];
-#pragma unroll
-      for (int j = 0; j < G::R; ++j) {
-        s[j] = r[j] = 0.f;
-#pragma unroll
-        for (int m = 0; m < 16; ++m) {
-          s[j] += S[j][m] * k[m];
-          r[j] += S[j][m] * q[m];
-        }
-      }
-      kq = lanes_sum<G::LPR>(kq);
-      const float eg = seg[i], beta = sbeta[i];
-#pragma unroll
-      for (int j = 0; j < G::R; ++j) {
-        const int row = row0 + j * G::RPW;
-        const float sj = lanes_sum<G::LPR>(s[j]), rj = lanes_sum<G::LPR>(r[j]);
-        const float delta = beta * (sv[i][row] - eg * sj);
-#pragma unroll
-        for (int m = 0; m < 16; ++m) S[j][m] = eg * S[j][m] + delta * k[m];
-        // only this row's lanes, of one wave, read sv[i][row]: o takes its place
-        if (lane % G::LPR == 0) sv[i][row] = eg * rj + delta * kq;
-      }
-      if (p.slot_tok) {
-        const int st = p.slot_tok[tb + i];
-        if (st >= 0 && st < p.cache.n_slots) put(st);
-      }
+    for (int s = 0; s < NP; ++s) {
+      const int job = (s * NL + lane) / G8, hi = job / STEP_TB, j = job % STEP_TB;
+      const int h = w.h0 + i / w.nb * HW + hi;
+      if (hi < HW && h < w.h1 && tb + j < w.t1) f(s, hi, j, (int64_t)(tb + j), h);
     }
-    __syncthreads();
-    for (int job = tid; job < nt * G8; job += NT) {
-      const int i = job / G8, e = job % G8 * 8;
-      const int64_t t = tb + i;
-      f8 o = load8(&sv[i][e]);
+  };
+  const int oe = lane % G8 * 8;
+  auto load_z = [&](int i) __attribute__((always_inline)) {
+    if constexpr (STEP)
+      each_out(i, [&](int s, int hi, int j, int64_t t, int h) __attribute__((always_inline)) {
+        z[s] = ld_raw8((const T*)p.z + t * p.ldz + h * D + oe);
+      });
+  };
+  auto finish = [&](int i) __attribute__((always_inline)) {
+    each_out(i, [&](int s, int hi, int j, int64_t t, int h) __attribute__((always_inline)) {
+      f8 o = load8(&lds.v[i & 1][hi][j][oe]);
       if constexpr (STEP) {
         float ss = 0.f;
 #pragma unroll
         for (int m = 0; m < 8; ++m) ss += o.v[m] * o.v[m];
         ss = lane_group_sum<G8>(ss);
         const float rho = rsqrtf(ss * (1.f / D) + p.norm_eps);
-        const f8 z = load8((const T*)p.z + t * p.ldz + h * D + e);
-        const f8 w = load8(p.w_norm + e);
+        const f8 wn = load8(p.w_norm + oe), zv = raw_f8(z[s]);
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
-          const float sg = sigmoidf_(z.v[m]);
-          o.v[m] *= rho * (1.f + w.v[m]) * (p.act == 0 ? z.v[m] * sg : sg);
+          const float sg = sigmoidf_(zv.v[m]);
+          o.v[m] *= rho * (1.f + wn.v[m]) * (p.act == 0 ? zv.v[m] * sg : sg);
         }
       }
-      store8(out + t * hv * D + h * D + e, o);
-    }
-    __syncthreads();
-  }
-  if (s_out >= 0) put(s_out);
-}
-
-// The conv rows of the states: after token t the last three input rows are
-// x[t-2], x[t-1], x[t], reaching back into the rows of slot_in.  A second
-// launch, since several heads' workgroups of the step read those rows.  A
-// thread owns 8 channels of one sequence and reads the rows it needs before
-// it writes any, so that slots may be updated in place.
-template <typename T>
-__global__ void __launch_bounds__(256) step_rows_kernel(StepArgs p, int n_grp, int64_t T_tok) {
-  const int n = blockIdx.y, grp = blockIdx.x * 256 + threadIdx.x;
-  if (grp >= n_grp) return;
-  int64_t t0, t1;
-  token_range(p.cu, n, T_tok, t0, t1);
-  const int s_in = p.slot_in ? p.slot_in[n] : -1;
-  const int s_out = p.slot_out ? p.slot_out[n] : -1;
-  if (s_in >= p.cache.n_slots || s_out >= p.cache.n_slots) return;
-  const int64_t C = (int64_t)n_grp * 8;
-  const T* x = (const T*)p.x + grp * 8;
-  T* rows = (T*)p.cache.conv + grp * 8;
-  Raw8<T> w[3];
-#pragma unroll
-  for (int j = 0; j < 3; ++j)
-    w[j] = s_in >= 0 ? ld_raw8(rows + (int64_t)s_in * p.cache.conv_stride + j * C) : zero_raw8<T>();
-  auto put = [&](int slot) {
-#pragma unroll
-    for (int j = 0; j < 3; ++j)
-#pragma unroll
-      for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-        reinterpret_cast<uint4*>(rows + (int64_t)slot * p.cache.conv_stride + j * C)[i] = w[j].v[i];
+      store8(out + t * hv * D + h * D + oe, o);
+    });
   };
-  // without tables for single tokens only the last three rows matter
-  const int64_t tb = p.slot_tok || t1 - t0 < 3 ? t0 : t1 - 3;
-  for (int64_t t = tb; t < t1; ++t) {
-    w[0] = w[1];
-    w[1] = w[2];
-    w[2] = ld_raw8(x + t * p.ldx);
-    if (p.slot_tok) {
-      const int st = p.slot_tok[t];
-      if (st >= 0 && st < p.cache.n_slots) put(st);
-    }
+
+  if (w.items == 0) return;
+  prep(0);
+  for (int i = 0; i < w.items; ++i) {
+    __syncthreads();
+    if (i > 0) finish(i - 1);
+    load_z(i);
+    if (i + 1 < w.items) prep(i + 1);
   }
-  if (s_out >= 0 && (t1 > t0 || s_out != s_in)) put(s_out);
+  __syncthreads();
+  finish(w.items - 1);
 }
 
-template <typename T, bool STEP>
+template <typename T, int D, int HW, bool STEP>
+__global__ void __launch_bounds__((StepGeo<D, HW>::THREADS), 4) step_kernel(StepArgs p, int hk, int hv,
+                                                                          int T_tok) {
+  typedef StepGeo<D, HW> G;
+  __shared__ StepLds<D, HW> lds;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int heads = STEP ? hv / hk : 1, per = hv / heads, n = blockIdx.x / per;
+  StepSpan w;
+  w.h0 = blockIdx.x % per * heads;
+  w.h1 = w.h0 + heads;
+  w.kh = w.h0 / (hv / hk);
+  token_range(p.cu, n, T_tok, w.t0, w.t1);
+  w.s_in = slot_of(p.slot_in, n);
+  w.s_out = slot_of(p.slot_out, n);
+  if (w.s_in >= p.cache.n_slots || w.s_out >= p.cache.n_slots) {   // a bad slot: NaN rows, no state
+    T* out = (T*)p.out;
+    const int64_t width = (int64_t)heads * D;
+    for (int64_t i = tid; i < (w.t1 - w.t0) * width; i += G::THREADS)
+      out[(w.t0 + i / width) * hv * D + (int64_t)w.h0 * D + i % width] = from_f<T>(__builtin_nanf(""));
+    return;
+  }
+  if (w.t0 == w.t1) {   // no tokens: the state passes through
+    if (w.s_out < 0 || w.s_out == w.s_in) return;
+    if (wave < HW * G::WAVES) {
+      StepState<D> st(wave % G::WAVES, lane);
+      for (int h = w.h0 + wave / G::WAVES; h < w.h1; h += HW) {
+        st.load(p, w.s_in, h);
+        st.store(p, w.s_out, h);
+      }
+    } else if constexpr (STEP) {
+      const int C = 2 * hk * D + hv * D, n_grp = (2 + heads) * D / 8;
+      for (int g = tid - 64 * HW * G::WAVES; g < n_grp * 3; g += 64 * G::HELPERS) {
+        const int e = g % n_grp * 8, hd = e / D;
+        const int64_t ch = (hd == 0 ? w.kh : hd == 1 ? hk + w.kh : 2 * hk + w.h0 + hd - 2) * D + e % D +
+                           (int64_t)(g / n_grp) * C;
+        store8((T*)p.cache.conv + (int64_t)w.s_out * p.cache.conv_stride + ch,
+               w.s_in >= 0 ? load8((const T*)p.cache.conv + (int64_t)w.s_in * p.cache.conv_stride + ch) : f8{});
+      }
+    }
+    return;
+  }
+  w.nb = (w.t1 - w.t0 - 1) / STEP_TB + 1;
+  w.items = (heads + HW - 1) / HW * w.nb;
+  if (wave < HW * G::WAVES) step_state_wave<D, HW>(p, w, lds, wave, lane);
+  else step_helper_wave<T, D, HW, STEP>(p, w, lds, hk, hv, tid - 64 * HW * G::WAVES);
+}
+
+template <typename T, int D, bool STEP>
 static void launch_step_d(const gdn_shape& s, const StepArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)s.n_seq * (unsigned)s.hv);
-  if (s.dk == 128)
-    hipLaunchKernelGGL((step_kernel<T, 128, STEP>), grid, dim3(StepGeo<128>::THREADS), 0, st, a,
-                       s.hk, s.hv, s.total_tokens);
-  else
-    hipLaunchKernelGGL((step_kernel<T, 32, STEP>), grid, dim3(StepGeo<32>::THREADS), 0, st, a, s.hk,
-                       s.hv, s.total_tokens);
+  const int group = s.hv / s.hk;
+  const dim3 grid((unsigned)s.n_seq * (unsigned)(STEP ? s.hk : s.hv));
+  // Value heads at a time.  With few workgroups all of a key head's together
+  // (one sequence, 48 heads over 16: 9.4 us against 13.6 us one by one; 64
+  // sequences 77 against 88 us); with many, one by one in smaller workgroups
+  // overlap better (256 sequences 294 against 302 us, 32 heads 198 against
+  // 211 us).  They meet at about 2000 workgroups.
+  const int64_t groups = (int64_t)s.n_seq * s.hk;
+  const int hw = !STEP || group == 1 || groups >= 2048 ? 1 : group == 2 || group == 4 ? 2 : 3;
+#define GDN_STEP(HW)                                                                              \
+  hipLaunchKernelGGL((step_kernel<T, D, HW, STEP>), grid, dim3(StepGeo<D, HW>::THREADS), 0, st, a, \
+                     s.hk, s.hv, (int)s.total_tokens)
+  if constexpr (STEP) {
+    if (hw == 3) { GDN_STEP(3); return; }
+    if (hw == 2) { GDN_STEP(2); return; }
+  }
+  GDN_STEP(1);
+#undef GDN_STEP
+}
+
+template <bool STEP>
+static hipError_t launch_step_t(const gdn_shape& s, const StepArgs& a, hipStream_t st) {
+  const bool big = s.dk == 128;
+  if (s.dtype == GDN_BF16) big ? launch_step_d<bf16, 128, STEP>(s, a, st) : launch_step_d<bf16, 32, STEP>(s, a, st);
+  else if (s.dtype == GDN_FP16) big ? launch_step_d<fp16, 128, STEP>(s, a, st) : launch_step_d<fp16, 32, STEP>(s, a, st);
+  else big ? launch_step_d<float, 128, STEP>(s, a, st) : launch_step_d<float, 32, STEP>(s, a, st);
+  return hipGetLastError();
 }
 
 hipError_t launch_recurrent(const gdn_shape& s, const StepArgs& a, hipStream_t st) {
-  if (s.dtype == GDN_BF16) launch_step_d<bf16, false>(s, a, st);
-  else if (s.dtype == GDN_FP16) launch_step_d<fp16, false>(s, a, st);
-  else launch_step_d<float, false>(s, a, st);
-  return hipGetLastError();
-}
-
-template <typename T>
-static hipError_t launch_step_t(const gdn_shape& s, const StepArgs& a, hipStream_t st) {
-  launch_step_d<T, true>(s, a, st);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || (!a.slot_out && !a.slot_tok)) return e;
-  const int n_grp = (2 * s.hk * s.dk + s.hv * s.dv) / 8;
-  hipLaunchKernelGGL((step_rows_kernel<T>), dim3((n_grp + 255) / 256, s.n_seq), dim3(256), 0, st, a,
-                     n_grp, s.total_tokens);
-  return hipGetLastError();
+  return launch_step_t<false>(s, a, st);
 }
 
 hipError_t launch_step(const gdn_shape& s, const StepArgs& a, hipStream_t st) {
-  if (s.dtype == GDN_BF16) return launch_step_t<bf16>(s, a, st);
-  if (s.dtype == GDN_FP16) return launch_step_t<fp16>(s, a, st);
-  return launch_step_t<float>(s, a, st);
+  return launch_step_t<true>(s, a, st);
 }
 
 // Check of the slot tables, one workgroup: a table of each slot's writing
 // sequence in LDS, for a range of slots at a time.
 constexpr int CHECK_RANGE = 8192;
 __global__ void __launch_bounds__(256) check_slots_kernel(const int32_t* __restrict__ cu, int n_seq,
-                                                          int64_t T_tok, int n_slots,
+                                                          int T_tok, int n_slots,
                                                           const int32_t* __restrict__ slot_in,
                                                           const int32_t* __restrict__ slot_out,
                                                           const int32_t* __restrict__ slot_tok,
@@ -321,11 +484,11 @@ __global__ void __launch_bounds__(256) check_slots_kernel(const int32_t* __restr
       else if (slot >= lo && slot < lo + CHECK_RANGE && atomicCAS(&writer[slot - lo], -1, n) != -1) bad |= 2;
     };
     for (int n = threadIdx.x; n < n_seq; n += 256) {
-      int64_t t0, t1;
-      token_range(cu, n, T_tok, t0, t1);
       if (slot_out) claim(slot_out[n], n);
-      if (slot_tok)
-        for (int64_t t = t0; t < t1; ++t) claim(slot_tok[t], n);
+      if (slot_tok) {
+        const int t0 = cu[n] < 0 ? 0 : cu[n], t1 = cu[n + 1] < T_tok ? cu[n + 1] : T_tok;
+        for (int t = t0; t < t1; ++t) claim(slot_tok[t], n);
+      }
     }
     __syncthreads();
     if (slot_in)
@@ -344,7 +507,7 @@ __global__ void __launch_bounds__(256) check_slots_kernel(const int32_t* __restr
 hipError_t launch_check_slots(const gdn_shape& s, int32_t n_slots, const int32_t* slot_in,
                               const int32_t* slot_out, const int32_t* slot_tok, const int32_t* cu,
                               int32_t* out, hipStream_t st) {
-  hipLaunchKernelGGL(check_slots_kernel, dim3(1), dim3(256), 0, st, cu, s.n_seq, s.total_tokens,
+  hipLaunchKernelGGL(check_slots_kernel, dim3(1), dim3(256), 0, st, cu, s.n_seq, (int)s.total_tokens,
                      n_slots, slot_in, slot_out, slot_tok, out);
   return hipGetLastError();
 }
