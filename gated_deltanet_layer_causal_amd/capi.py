@@ -545,6 +545,7 @@ def make_cache(S, conv=None) -> Cache:
     if S.stride()[1:] != (d * d, d, 1):
         raise ValueError(f"each slot of S must be contiguous, got strides {S.stride()}")
     c = Cache(S.data_ptr(), S.stride(0) if n > 1 else hv * d * d, None, 0, n)
+    c.conv_rows = None
     if conv is not None:
         if conv.dtype not in _GDN_DT or conv.dim() != 3 or tuple(conv.shape[:2]) != (n, 3):
             raise ValueError(f"conv must be [{n}, 3, C] in a storage type, got {conv.dtype} "
@@ -554,23 +555,47 @@ def make_cache(S, conv=None) -> Cache:
             raise ValueError("each slot of conv must be contiguous and on S's device")
         c.conv_ptr = conv.data_ptr()
         c.conv_stride = conv.stride(0) if n > 1 else 3 * C
-    c.S, c.conv, c.device, c.heads = S, conv, S.device, (hv, d)
+        c.conv_rows = (conv.dtype, C)
+    c.S, c.conv, c.device, c.index, c.heads = S, conv, S.device, S.get_device(), (hv, d)
     return c
 
 
-def _slot_call(name, dev, stream, fn, *args):
-    """Runs a serving entry point on `dev` (which need not be the current
-    device) and the given stream, or dev's current one."""
-    if dev.type != "cuda":
+# Serving calls are as short as a few microseconds, so their wrappers ask first
+# whether every tensor is as it should be, as cheaply as Python can (dtype,
+# shape, layout and device index), and look for what is wrong only if one is
+# not.
+def _is_rows(t, dtype, shape, index):
+    return (t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0 and
+            (t.stride(1) == 1 or shape[0] == 0 or shape[1] == 1))
+
+
+def _is_flat(t, dtype, numel, index):
+    return (t.dtype is dtype and t.numel() == numel and t.get_device() == index >= 0 and
+            t.is_contiguous())
+
+
+def _is_table(t, numel, index):
+    return t is None or _is_flat(t, torch.int32, numel, index)
+
+
+def _slot_call(name, dev, index, stream, fn, *args):
+    """Runs a serving entry point on device `index` (`dev`; it need not be the
+    current one) and the given stream, or the device's current one."""
+    if index < 0:
         raise ValueError("libgdn takes device tensors only; got a host tensor")
-    if stream is not None and stream.device != dev:
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream(stream))
     else:
-        st = fn(*args, _stream(stream))
-    _ok(name, st)
+        raw = stream.cuda_stream
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            st = fn(*args, raw)
+    else:
+        st = fn(*args, raw)
+    if st != 0:
+        _ok(name, st)
 
 
 def _on(dev, *named):
@@ -592,7 +617,6 @@ def _cache_ok(shape, cache):
     if cache.heads != (shape.hv, shape.dv):
         raise ValueError(f"the cache's states are of {cache.heads[0]} heads of {cache.heads[1]}, the "
                          f"shape's of {shape.hv} of {shape.dv}")
-    return cache.device
 
 
 def _ptr(t):
@@ -609,17 +633,26 @@ def gdn_recurrent_fwd(shape, q, k, v, g, beta, scale, cache, slot_in, slot_out, 
                       cu_seqlens, o, stream=None):
     """cache: make_cache(S).  slot_in, slot_out [n_seq] and slot_tok [T]:
     int32 device tables, each may be None; see libgdn.h."""
-    dev = _cache_ok(shape, cache)
-    _chunk_qk(shape, q, k)
-    _rows("v", v, _tdt(shape), shape.total_tokens, shape.hv * shape.dv)
-    _per_token("g", shape, g)
-    _per_token("beta", shape, beta)
-    _heads("o", shape, o)
-    _slot_tables(shape, dev, cu_seqlens, slot_in, slot_out, slot_tok)
-    _on(dev, ("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("o", o))
-    _slot_call("gdn_recurrent_fwd", dev, stream, load().gdn_recurrent_fwd, byref(shape), _ptr(q),
-               _ptr(k), _ptr(v), _row_ld(q), _row_ld(k), _row_ld(v), _ptr(g), _ptr(beta), scale, byref(cache),
-               _ptr(slot_in), _ptr(slot_out), _ptr(slot_tok), _ptr(cu_seqlens), _ptr(o))
+    i, dt, T, N, hv, d = (cache.index, _TDT[shape.dtype], shape.total_tokens, shape.n_seq, shape.hv,
+                          shape.dv)
+    qk, f32 = (T, shape.hk * d), torch.float32
+    if not (cache.heads == (hv, d) and _is_rows(q, dt, qk, i) and _is_rows(k, dt, qk, i) and
+            _is_rows(v, dt, (T, hv * d), i) and _is_flat(g, f32, T * hv, i) and
+            _is_flat(beta, f32, T * hv, i) and _is_flat(o, dt, T * hv * d, i) and
+            _is_flat(cu_seqlens, torch.int32, N + 1, i) and _is_table(slot_in, N, i) and
+            _is_table(slot_out, N, i) and _is_table(slot_tok, T, i)):
+        _cache_ok(shape, cache)
+        _chunk_qk(shape, q, k)
+        _rows("v", v, dt, T, hv * d)
+        _per_token("g", shape, g)
+        _per_token("beta", shape, beta)
+        _heads("o", shape, o)
+        _slot_tables(shape, cache.device, cu_seqlens, slot_in, slot_out, slot_tok)
+        _on(cache.device, ("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("o", o))
+    _slot_call("gdn_recurrent_fwd", cache.device, i, stream, load().gdn_recurrent_fwd, byref(shape),
+               q.data_ptr(), k.data_ptr(), v.data_ptr(), _row_ld(q), _row_ld(k), _row_ld(v),
+               g.data_ptr(), beta.data_ptr(), scale, byref(cache), _ptr(slot_in), _ptr(slot_out),
+               _ptr(slot_tok), cu_seqlens.data_ptr(), o.data_ptr())
 
 
 def gdn_step_fwd(shape, x, w_conv, a, b, A_log, dt_bias, z, w_norm, scale, cache, slot_in,
@@ -627,25 +660,35 @@ def gdn_step_fwd(shape, x, w_conv, a, b, A_log, dt_bias, z, w_norm, scale, cache
                  act=GDN_ACT_SILU, stream=None):
     """x [T, C], a, b [T, hv] and z [T, hv*d]: rows may be strided.  cache:
     make_cache(S, conv); slot tables as gdn_recurrent_fwd."""
-    dev = _cache_ok(shape, cache)
-    dt, T = _tdt(shape), shape.total_tokens
-    C = _conv_ok(shape, x, w_conv, cu_seqlens)
-    if cache.conv is None or cache.conv.dtype != dt or cache.conv.shape[2] != C:
-        raise ValueError(f"the cache needs conv rows [n_slots, 3, {C}] of {dt}")
-    _rows("a", a, dt, T, shape.hv)
-    _rows("b", b, dt, T, shape.hv)
-    _need("A_log", A_log, torch.float32, shape.hv)
-    _need("dt_bias", dt_bias, torch.float32, shape.hv)
-    _rows("z", z, dt, T, shape.hv * shape.dv)
-    _need("w_norm", w_norm, torch.float32, shape.dv)
-    _heads("out", shape, out)
-    _slot_tables(shape, dev, cu_seqlens, slot_in, slot_out, slot_tok)
-    _on(dev, ("x", x), ("w_conv", w_conv), ("a", a), ("b", b), ("A_log", A_log),
-        ("dt_bias", dt_bias), ("z", z), ("w_norm", w_norm), ("out", out))
-    _slot_call("gdn_step_fwd", dev, stream, load().gdn_step_fwd, byref(shape), _ptr(x), _row_ld(x),
-               _ptr(w_conv), _ptr(a), _row_ld(a), _ptr(b), _row_ld(b), _ptr(A_log), _ptr(dt_bias), _ptr(z),
-               _row_ld(z), _ptr(w_norm), scale, l2_eps, norm_eps, act, byref(cache), _ptr(slot_in),
-               _ptr(slot_out), _ptr(slot_tok), _ptr(cu_seqlens), _ptr(out))
+    i, dt, T, N, hv, d = (cache.index, _TDT[shape.dtype], shape.total_tokens, shape.n_seq, shape.hv,
+                          shape.dv)
+    C, f32 = 2 * shape.hk * d + hv * d, torch.float32
+    if not (cache.heads == (hv, d) and cache.conv_rows == (dt, C) and _is_rows(x, dt, (T, C), i) and
+            _is_flat(w_conv, f32, C * 4, i) and _is_rows(a, dt, (T, hv), i) and
+            _is_rows(b, dt, (T, hv), i) and _is_flat(A_log, f32, hv, i) and
+            _is_flat(dt_bias, f32, hv, i) and _is_rows(z, dt, (T, hv * d), i) and
+            _is_flat(w_norm, f32, d, i) and _is_flat(out, dt, T * hv * d, i) and
+            _is_flat(cu_seqlens, torch.int32, N + 1, i) and _is_table(slot_in, N, i) and
+            _is_table(slot_out, N, i) and _is_table(slot_tok, T, i)):
+        _cache_ok(shape, cache)
+        _conv_ok(shape, x, w_conv, cu_seqlens)
+        if cache.conv_rows != (dt, C):
+            raise ValueError(f"the cache needs conv rows [n_slots, 3, {C}] of {dt}")
+        _rows("a", a, dt, T, hv)
+        _rows("b", b, dt, T, hv)
+        _need("A_log", A_log, f32, hv)
+        _need("dt_bias", dt_bias, f32, hv)
+        _rows("z", z, dt, T, hv * d)
+        _need("w_norm", w_norm, f32, d)
+        _heads("out", shape, out)
+        _slot_tables(shape, cache.device, cu_seqlens, slot_in, slot_out, slot_tok)
+        _on(cache.device, ("x", x), ("w_conv", w_conv), ("a", a), ("b", b), ("A_log", A_log),
+            ("dt_bias", dt_bias), ("z", z), ("w_norm", w_norm), ("out", out))
+    _slot_call("gdn_step_fwd", cache.device, i, stream, load().gdn_step_fwd, byref(shape),
+               x.data_ptr(), _row_ld(x), w_conv.data_ptr(), a.data_ptr(), _row_ld(a), b.data_ptr(),
+               _row_ld(b), A_log.data_ptr(), dt_bias.data_ptr(), z.data_ptr(), _row_ld(z),
+               w_norm.data_ptr(), scale, l2_eps, norm_eps, act, byref(cache), _ptr(slot_in),
+               _ptr(slot_out), _ptr(slot_tok), cu_seqlens.data_ptr(), out.data_ptr())
 
 
 SLOT_RANGE, SLOT_WRITTEN_TWICE, SLOT_WRITTEN_AND_READ = 1, 2, 4
@@ -659,7 +702,7 @@ def gdn_check_slots(shape, n_slots, slot_in, slot_out, slot_tok, cu_seqlens, vio
     _slot_tables(shape, dev, cu_seqlens, slot_in, slot_out, slot_tok)
     _need("violations", violations, torch.int32, 1)
     _on(dev, ("violations", violations))
-    _slot_call("gdn_check_slots", dev, stream, load().gdn_check_slots, byref(shape), n_slots,
+    _slot_call("gdn_check_slots", dev, cu_seqlens.get_device(), stream, load().gdn_check_slots, byref(shape), n_slots,
                _ptr(slot_in), _ptr(slot_out), _ptr(slot_tok), _ptr(cu_seqlens), _ptr(violations))
 
 
@@ -672,9 +715,10 @@ def _slot_rows(name, t):
     return t.shape[0], size, t.stride(0) * t.element_size() if t.shape[0] > 1 else size
 
 
-def _indexes(name, dev, t, n=None):
-    _need(name, t, torch.int32, n)
-    _on(dev, (name, t))
+def _indexes(name, like, t, n=None):
+    if t is None or not _is_flat(t, torch.int32, t.numel() if n is None else n, like.get_device()):
+        _need(name, t, torch.int32, n)
+        _on(like.device, (name, t))
     return t.numel()
 
 
@@ -685,20 +729,19 @@ def gdn_cache_copy(src, dst, src_idx=None, dst_idx=None, stream=None):
     n_dst, dsize, ds = _slot_rows("dst", dst)
     if src.dtype != dst.dtype or size != dsize:
         raise ValueError(f"slots of {size} bytes of {src.dtype} into slots of {dsize} of {dst.dtype}")
-    dev = src.device
-    _on(dev, ("dst", dst))
+    _on(src.device, ("dst", dst))
     n = min(n_src, n_dst)
     if src_idx is not None:
-        n = _indexes("src_idx", dev, src_idx)
+        n = _indexes("src_idx", src, src_idx)
         if dst_idx is None and n > n_dst:
             raise ValueError(f"{n} slots into {n_dst}")
     if dst_idx is not None:
-        n = _indexes("dst_idx", dev, dst_idx, n if src_idx is not None else None)
+        n = _indexes("dst_idx", src, dst_idx, n if src_idx is not None else None)
         if src_idx is None and n > n_src:
             raise ValueError(f"{n} slots out of {n_src}")
     if src_idx is None and dst_idx is None and n_src != n_dst:
         raise ValueError(f"{n_src} slots into {n_dst} without indexes")
-    _slot_call("gdn_cache_copy", dev, stream, load().gdn_cache_copy, _ptr(src), ss, n_src,
+    _slot_call("gdn_cache_copy", src.device, src.get_device(), stream, load().gdn_cache_copy, _ptr(src), ss, n_src,
                _ptr(src_idx), _ptr(dst), ds, n_dst, _ptr(dst_idx), size, n)
 
 
@@ -709,27 +752,35 @@ def gdn_cache_workspace(n_slots):
 def _cache_buf(buf, refs):
     if buf.dim() != 2 or not buf.is_contiguous():
         raise ValueError("the cache must be a contiguous [n_slots, slot] tensor")
-    _indexes("refs", buf.device, refs, buf.shape[0])
-    return buf.shape[0], buf.shape[1] * buf.element_size(), buf.device
+    n_slots, size = buf.shape
+    _indexes("refs", buf, refs, n_slots)
+    return n_slots, size * buf.element_size()
+
+
+def _cache_ws(buf, ws):
+    if ws is None:
+        return None, 0
+    if not _is_flat(ws, torch.uint8, ws.numel(), buf.get_device()):
+        _ws(ws)
+        _on(buf.device, ("workspace", ws))
+    return ws.data_ptr(), ws.numel()
 
 
 def gdn_cache_fork(buf, refs, src, dst, ws, stream=None):
     """Takes a free slot of buf [n_slots, slot] for every request in src and
     fills it; the slots go to dst (int32, as long as src)."""
-    n_slots, size, dev = _cache_buf(buf, refs)
-    n = _indexes("src", dev, src)
-    _indexes("dst", dev, dst, n)
-    _ws(ws)
-    _on(dev, ("workspace", ws))
-    _slot_call("gdn_cache_fork", dev, stream, load().gdn_cache_fork, _ptr(buf), size, n_slots,
-               _ptr(refs), _ptr(src), n, _ptr(dst), _ptr(ws), ws.numel() if ws is not None else 0)
+    n_slots, size = _cache_buf(buf, refs)
+    n = _indexes("src", buf, src)
+    _indexes("dst", buf, dst, n)
+    _slot_call("gdn_cache_fork", buf.device, buf.get_device(), stream, load().gdn_cache_fork, _ptr(buf),
+               size, n_slots, _ptr(refs), _ptr(src), n, _ptr(dst), *_cache_ws(buf, ws))
 
 
 def _count(name, refs, slots, stream):
-    dev = refs.device
-    n_slots = _indexes("refs", dev, refs)
-    n = _indexes("slots", dev, slots)
-    _slot_call(name, dev, stream, getattr(load(), name), _ptr(refs), n_slots, _ptr(slots), n)
+    n_slots = _indexes("refs", refs, refs)
+    n = _indexes("slots", refs, slots)
+    _slot_call(name, refs.device, refs.get_device(), stream, getattr(load(), name), _ptr(refs), n_slots,
+               _ptr(slots), n)
 
 
 def gdn_cache_retain(refs, slots, stream=None):
@@ -743,11 +794,8 @@ def gdn_cache_release(refs, slots, stream=None):
 def gdn_cache_compact(buf, refs, remap, table, ws, stream=None):
     """Moves the live slots of buf to its front; remap [n_slots] receives
     where each went, and table (int32, or None) is rewritten by it."""
-    n_slots, size, dev = _cache_buf(buf, refs)
-    _indexes("remap", dev, remap, n_slots)
-    n = 0 if table is None else _indexes("table", dev, table)
-    _ws(ws)
-    _on(dev, ("workspace", ws))
-    _slot_call("gdn_cache_compact", dev, stream, load().gdn_cache_compact, _ptr(buf), size, n_slots,
-               _ptr(refs), _ptr(remap), _ptr(table), n, _ptr(ws),
-               ws.numel() if ws is not None else 0)
+    n_slots, size = _cache_buf(buf, refs)
+    _indexes("remap", buf, remap, n_slots)
+    n = 0 if table is None else _indexes("table", buf, table)
+    _slot_call("gdn_cache_compact", buf.device, buf.get_device(), stream, load().gdn_cache_compact,
+               _ptr(buf), size, n_slots, _ptr(refs), _ptr(remap), _ptr(table), n, *_cache_ws(buf, ws))

@@ -68,6 +68,7 @@ class GDNCore:
         self.device = torch.device(device)
         self._ws = None        # conv / gate / norm scratch
         self._ws_chunk = None  # chunk scratch of calls that do not save states
+        self._last_shape = None
         L.load()
 
     def shape(self, T: int, n_seq: int) -> L.Shape:
@@ -149,6 +150,15 @@ class GDNCore:
         return saved
 
     # ------------------------------------------------------------ serving
+    def _step_shape(self, T, n_seq):
+        """shape(), the last one kept: a serving loop repeats its batch's."""
+        c = self.cfg
+        key = (T, n_seq, c.hk, c.hv, c.d, c.dtype)
+        last = self._last_shape
+        if last is None or last[0] != key:
+            last = self._last_shape = key, self.shape(T, n_seq)
+        return last[1]
+
     def step(self, x, w_conv, a, b, A_log, dt_bias, z, w_norm, cu_seqlens, cache, slot_in,
              slot_out=None, slot_tok=None, layer=0):
         """The core for the next tokens of cached sequences (usually one each):
@@ -162,7 +172,7 @@ class GDNCore:
         the rule and the norm.  No workspace, nothing synchronises."""
         c = self.cfg
         T = x.shape[0]
-        sh = self.shape(T, cu_seqlens.numel() - 1)
+        sh = self._step_shape(T, cu_seqlens.numel() - 1)
         slot_out = slot_in if slot_out is None else slot_out
         if c.check_slots:
             self.check_slots(sh, cache, slot_in, slot_out, slot_tok, cu_seqlens)
@@ -179,7 +189,7 @@ class GDNCore:
         [T, hv] -> o [T, hv, d]; the slots as in step()."""
         c = self.cfg
         T = q.shape[0]
-        sh = self.shape(T, cu_seqlens.numel() - 1)
+        sh = self._step_shape(T, cu_seqlens.numel() - 1)
         slot_out = slot_in if slot_out is None else slot_out
         if c.check_slots:
             self.check_slots(sh, cache, slot_in, slot_out, slot_tok, cu_seqlens)
