@@ -4,7 +4,8 @@
 //
 // One workgroup owns one sequence and some value heads of one key head: the
 // step all of them (so that it alone reads and writes their conv rows), HW at
-// a time, the rule one.  A head's state S (D x D, fp32) stays in registers
+// a time, the rule one or a quarter of one's rows (the rows of S need nothing
+// from each other but k and q).  A head's state S (D x D, fp32) stays in registers
 // from its load to its store, so a call reads and writes each state once
 // however many tokens a sequence has:
 //   s = S_{t-1} k,  r = S_{t-1} q   (both from the old state, reduced together)
@@ -48,38 +49,42 @@ template <int N> __device__ __forceinline__ float lanes_sum(float x) {
 }
 
 // Thread layout of the state: LPR lanes share a row of D columns; a lane
-// holds the columns 4 l + 4 LPR c + (0..3), c = 0..3, of R rows.
-template <int D, int HW> struct StepGeo {
+// holds the columns 4 l + 4 LPR c + (0..3), c = 0..3, of R rows.  SPLIT
+// workgroups share a head, VC value rows each.
+template <int D, int HW, int SPLIT> struct StepGeo {
   static constexpr int LPR = D / 16;
-  static constexpr int R = D == 128 ? 4 : 1;
+  static constexpr int R = D == 128 ? 4 / SPLIT : 1;
   static constexpr int RPW = 64 / LPR;              // rows per wave and row slot
-  static constexpr int WAVES = D / (RPW * R);       // state waves of a head
+  static constexpr int VC = D / SPLIT;
+  static constexpr int WAVES = VC / (RPW * R);      // state waves of a head
   // helper lanes: 8 channels each of q, k and HW times v, then a gate each
-  static constexpr int CONV_LANES = (2 + HW) * D / 8, HELPERS = (CONV_LANES + HW * STEP_TB + 63) / 64;
+  static constexpr int CONV_LANES = (2 * D + HW * VC) / 8, HELPERS = (CONV_LANES + HW * STEP_TB + 63) / 64;
   static constexpr int THREADS = 64 * (HW * WAVES + HELPERS);
 };
 
-template <int D, int HW> struct StepLds {
-  float q[2][STEP_TB][D], k[2][STEP_TB][D], v[2][HW][STEP_TB][D];   // v, then o in its place
+template <int D, int HW, int SPLIT> struct StepLds {
+  float q[2][STEP_TB][D], k[2][STEP_TB][D];
+  float v[2][HW][STEP_TB][D / SPLIT];                               // v, then o in its place
   float eg[2][HW][STEP_TB], beta[2][HW][STEP_TB];
   int tok[2][STEP_TB];                                              // slot_tok, -1: none
 };
 
 // What a workgroup works on: value heads h0 .. h1 - 1 of key head kh, HW at a
 // time (a round), each round in nb blocks of STEP_TB tokens; item i = (round
-// i / nb, block i % nb).
+// i / nb, block i % nb).  v0: the first value row of those that share a head.
 struct StepSpan {
-  int t0, t1, s_in, s_out, h0, h1, kh, nb, items;
+  int t0, t1, s_in, s_out, h0, h1, kh, nb, items, v0;
 };
 
 // A head's state: its load, its tokens, its store.
-template <int D> struct StepState {
-  typedef StepGeo<D, 1> G;
+template <int D, int SPLIT> struct StepState {
+  typedef StepGeo<D, 1, SPLIT> G;
   floatx4 S[G::R][4];
-  uint32_t row0, col0, at;   // first row, first column, and the byte they are at
+  uint32_t row0, col0, at;   // first row of the workgroup's, first column, and their byte in S
 
-  __device__ __forceinline__ StepState(int wave, int lane)
-      : row0(wave * (G::RPW * G::R) + lane / G::LPR), col0(4 * (lane % G::LPR)), at(4 * (row0 * D + col0)) {}
+  __device__ __forceinline__ StepState(int wave, int lane, int v0)
+      : row0(wave * (G::RPW * G::R) + lane / G::LPR), col0(4 * (lane % G::LPR)),
+        at(4 * ((v0 + row0) * D + col0)) {}
 
   // Each state passes through once, in whole lines: non-temporal both ways (the
   // rule, 200 sequences x 48 heads, bf16: 251 us with plain accesses, 245 us
@@ -171,12 +176,12 @@ template <int D> struct StepState {
   }
 };
 
-template <int D, int HW>
+template <int D, int HW, int SPLIT>
 __device__ __forceinline__ void step_state_wave(const StepArgs& p, const StepSpan& w,
-                                                StepLds<D, HW>& lds, int wave, int lane) {
-  constexpr int WAVES = StepGeo<D, HW>::WAVES;
+                                                StepLds<D, HW, SPLIT>& lds, int wave, int lane) {
+  constexpr int WAVES = StepGeo<D, HW, SPLIT>::WAVES;
   const int hw = wave / WAVES;                    // which of the round's heads
-  StepState<D> st(wave % WAVES, lane);
+  StepState<D, SPLIT> st(wave % WAVES, lane, w.v0);
   int h = w.h0 + hw, blk = 0;
   if (h < w.h1) st.load(p, w.s_in, h);
   for (int i = 0; i < w.items; ++i) {
@@ -205,15 +210,17 @@ __device__ __forceinline__ void step_state_wave(const StepArgs& p, const StepSpa
 // The helper waves; `lane` counts through them.  A conv lane forms 8 channels
 // of q, k or one head's v of every token, with the conv's window in
 // registers; the lanes behind them form the gate of one token and head each.
-template <typename T, int D, int HW, bool STEP>
+template <typename T, int D, int HW, int SPLIT, bool STEP>
 __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSpan& w,
-                                                 StepLds<D, HW>& lds, int hk, int hv, int lane) {
-  typedef StepGeo<D, HW> G;
-  constexpr int G8 = D / 8, NL = 64 * G::HELPERS, NP = (HW * STEP_TB * G8 + NL - 1) / NL;
+                                                 StepLds<D, HW, SPLIT>& lds, int hk, int hv, int lane) {
+  typedef StepGeo<D, HW, SPLIT> G;
+  constexpr int G8 = D / 8, V8 = G::VC / 8;      // lanes of a q or k row, of a v row
+  constexpr int NL = 64 * G::HELPERS, NP = (HW * STEP_TB * V8 + NL - 1) / NL;
   constexpr int AHEAD = (sizeof(T) == 2 ? 4 : 2) / (HW == 3 ? 2 : 1);   // rows of x in flight (registers)
   const int C = 2 * hk * D + hv * D;
-  const int part = lane / G8, e = lane % G8 * 8; // part: 0 q, 1 k, 2 + i v of the round's head i
-  const int vh = part < 2 ? 0 : part - 2;
+  // part: 0 q, 1 k, 2 + i v of the round's head i; e: the first of 8 channels
+  const int part = SPLIT == 1 || lane < 2 * G8 ? lane / G8 : 2 + (lane - 2 * G8) / V8;
+  const int vh = part < 2 ? 0 : part - 2, e = (part < 2 ? lane % G8 : lane % V8) * 8;
   const int gh = (lane - G::CONV_LANES) / STEP_TB, gt = (lane - G::CONV_LANES) % STEP_TB;   // the gate's
   T* out = (T*)p.out;
   // rule: this lane's tensor and its row stride
@@ -233,8 +240,9 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
       const int h = hr + vh;
       if (part >= 2 && h >= w.h1) return;
       // this lane's channel: of x, or of q, k or v
-      const int ch = (STEP ? part == 0 ? w.kh : part == 1 ? hk + w.kh : 2 * hk + h : part < 2 ? w.kh : h) * D + e;
-      float(*dst)[D] = part == 0 ? lds.q[buf] : part == 1 ? lds.k[buf] : lds.v[buf][vh];
+      const int ch = (STEP ? part == 0 ? w.kh : part == 1 ? hk + w.kh : 2 * hk + h : part < 2 ? w.kh : h) * D + (part < 2 ? 0 : w.v0) + e;
+      float* dst = (part == 0 ? lds.q[buf][0] : part == 1 ? lds.k[buf][0] : lds.v[buf][vh][0]) + e;
+      const int dst_ld = part < 2 ? D : G::VC;
       if constexpr (STEP) {
         if (tb == w.t0) {
           const T* rows = (const T*)p.cache.conv + (int64_t)w.s_in * p.cache.conv_stride + ch;
@@ -284,7 +292,7 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
               const float r = part >= 2 ? 1.f : rsqrtf(ss + p.l2_eps) * (part == 0 ? p.scale : 1.f);
 #pragma unroll
               for (int m = 0; m < 8; ++m) y.v[m] *= r;
-              store8(&dst[j0 + j][e], y);
+              store8(dst + (j0 + j) * dst_ld, y);
               x3 = x2;
               x2 = x1;
               x1 = x0;
@@ -307,7 +315,7 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
             f8 y = raw_f8(raw[j]);
 #pragma unroll
             for (int m = 0; m < 8; ++m) y.v[m] *= r;
-            store8(&dst[j][e], y);
+            store8(dst + j * dst_ld, y);
           }
       }
     } else if (gh < HW && gt < nt && hr + gh < w.h1) {
@@ -332,12 +340,12 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
     const int tb = w.t0 + i % w.nb * STEP_TB;
 #pragma unroll
     for (int s = 0; s < NP; ++s) {
-      const int job = (s * NL + lane) / G8, hi = job / STEP_TB, j = job % STEP_TB;
+      const int job = (s * NL + lane) / V8, hi = job / STEP_TB, j = job % STEP_TB;
       const int h = w.h0 + i / w.nb * HW + hi;
       if (hi < HW && h < w.h1 && tb + j < w.t1) f(s, hi, j, (int64_t)(tb + j), h);
     }
   };
-  const int oe = lane % G8 * 8;
+  const int oe = lane % V8 * 8;
   auto load_z = [&](int i) __attribute__((always_inline)) {
     if constexpr (STEP)
       each_out(i, [&](int s, int hi, int j, int64_t t, int h) __attribute__((always_inline)) {
@@ -360,7 +368,7 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
           o.v[m] *= rho * (1.f + wn.v[m]) * (p.act == 0 ? zv.v[m] * sg : sg);
         }
       }
-      store8(out + t * hv * D + h * D + oe, o);
+      store8(out + t * hv * D + h * D + w.v0 + oe, o);
     });
   };
 
@@ -376,15 +384,17 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
   finish(w.items - 1);
 }
 
-template <typename T, int D, int HW, bool STEP>
-__global__ void __launch_bounds__((StepGeo<D, HW>::THREADS), 4) step_kernel(StepArgs p, int hk, int hv,
-                                                                          int T_tok) {
-  typedef StepGeo<D, HW> G;
-  __shared__ StepLds<D, HW> lds;
+template <typename T, int D, int HW, int SPLIT, bool STEP>
+__global__ void __launch_bounds__((StepGeo<D, HW, SPLIT>::THREADS), 4) step_kernel(StepArgs p, int hk, int hv,
+                                                                                 int T_tok) {
+  static_assert(SPLIT == 1 || (!STEP && HW == 1), "the norm needs whole rows");
+  typedef StepGeo<D, HW, SPLIT> G;
+  __shared__ StepLds<D, HW, SPLIT> lds;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int heads = STEP ? hv / hk : 1, per = hv / heads, n = blockIdx.x / per;
+  const int heads = STEP ? hv / hk : 1, per = hv / heads * SPLIT, n = blockIdx.x / per;
   StepSpan w;
-  w.h0 = blockIdx.x % per * heads;
+  w.h0 = blockIdx.x % per / SPLIT * heads;
+  w.v0 = blockIdx.x % SPLIT * G::VC;
   w.h1 = w.h0 + heads;
   w.kh = w.h0 / (hv / hk);
   token_range(p.cu, n, T_tok, w.t0, w.t1);
@@ -392,15 +402,15 @@ __global__ void __launch_bounds__((StepGeo<D, HW>::THREADS), 4) step_kernel(Step
   w.s_out = slot_of(p.slot_out, n);
   if (w.s_in >= p.cache.n_slots || w.s_out >= p.cache.n_slots) {   // a bad slot: NaN rows, no state
     T* out = (T*)p.out;
-    const int64_t width = (int64_t)heads * D;
+    const int64_t width = (int64_t)heads * G::VC;
     for (int64_t i = tid; i < (w.t1 - w.t0) * width; i += G::THREADS)
-      out[(w.t0 + i / width) * hv * D + (int64_t)w.h0 * D + i % width] = from_f<T>(__builtin_nanf(""));
+      out[(w.t0 + i / width) * hv * D + (int64_t)w.h0 * D + w.v0 + i % width] = from_f<T>(__builtin_nanf(""));
     return;
   }
   if (w.t0 == w.t1) {   // no tokens: the state passes through
     if (w.s_out < 0 || w.s_out == w.s_in) return;
     if (wave < HW * G::WAVES) {
-      StepState<D> st(wave % G::WAVES, lane);
+      StepState<D, SPLIT> st(wave % G::WAVES, lane, w.v0);
       for (int h = w.h0 + wave / G::WAVES; h < w.h1; h += HW) {
         st.load(p, w.s_in, h);
         st.store(p, w.s_out, h);
@@ -419,30 +429,37 @@ __global__ void __launch_bounds__((StepGeo<D, HW>::THREADS), 4) step_kernel(Step
   }
   w.nb = (w.t1 - w.t0 - 1) / STEP_TB + 1;
   w.items = (heads + HW - 1) / HW * w.nb;
-  if (wave < HW * G::WAVES) step_state_wave<D, HW>(p, w, lds, wave, lane);
-  else step_helper_wave<T, D, HW, STEP>(p, w, lds, hk, hv, tid - 64 * HW * G::WAVES);
+  if (wave < HW * G::WAVES) step_state_wave<D, HW, SPLIT>(p, w, lds, wave, lane);
+  else step_helper_wave<T, D, HW, SPLIT, STEP>(p, w, lds, hk, hv, tid - 64 * HW * G::WAVES);
+}
+
+template <typename T, int D, int HW, int SPLIT, bool STEP>
+static void launch_step_k(const gdn_shape& s, const StepArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((step_kernel<T, D, HW, SPLIT, STEP>),
+                     dim3((unsigned)s.n_seq * (unsigned)(STEP ? s.hk : s.hv) * SPLIT),
+                     dim3(StepGeo<D, HW, SPLIT>::THREADS), 0, st, a, s.hk, s.hv, (int)s.total_tokens);
 }
 
 template <typename T, int D, bool STEP>
 static void launch_step_d(const gdn_shape& s, const StepArgs& a, hipStream_t st) {
-  const int group = s.hv / s.hk;
-  const dim3 grid((unsigned)s.n_seq * (unsigned)(STEP ? s.hk : s.hv));
-  // Value heads at a time.  With few workgroups all of a key head's together
-  // (one sequence, 48 heads over 16: 9.4 us against 13.6 us one by one; 64
-  // sequences 77 against 88 us); with many, one by one in smaller workgroups
-  // overlap better (256 sequences 294 against 302 us, 32 heads 198 against
-  // 211 us).  They meet at about 2000 workgroups.
-  const int64_t groups = (int64_t)s.n_seq * s.hk;
-  const int hw = !STEP || group == 1 || groups >= 2048 ? 1 : group == 2 || group == 4 ? 2 : 3;
-#define GDN_STEP(HW)                                                                              \
-  hipLaunchKernelGGL((step_kernel<T, D, HW, STEP>), grid, dim3(StepGeo<D, HW>::THREADS), 0, st, a, \
-                     s.hk, s.hv, (int)s.total_tokens)
   if constexpr (STEP) {
-    if (hw == 3) { GDN_STEP(3); return; }
-    if (hw == 2) { GDN_STEP(2); return; }
+    // Value heads at a time.  With few workgroups all of a key head's together
+    // (one sequence, 48 heads over 16: 9.4 us against 13.6 us one by one; 64
+    // sequences 77 against 88 us); with many, one by one in smaller workgroups
+    // overlap better (256 sequences 294 against 302 us, 32 heads 198 against
+    // 211 us).  They meet at about 2000 workgroups.
+    const int group = s.hv / s.hk;
+    if (group == 1 || (int64_t)s.n_seq * s.hk >= 2048) launch_step_k<T, D, 1, 1, STEP>(s, a, st);
+    else if (group == 2 || group == 4) launch_step_k<T, D, 2, 1, STEP>(s, a, st);
+    else launch_step_k<T, D, 3, 1, STEP>(s, a, st);
+  } else {
+    // A head over four workgroups while that still fills the chip's 256 CUs:
+    // 8 heads 4.2 us against 5.0 us for one token, 13.8 against 28.0 us for
+    // 32; 192 heads 25.0 against 32.0 us; 384 heads 46.3 against 45.1 us.
+    if constexpr (D == 128)
+      if ((int64_t)s.n_seq * s.hv <= 256) return launch_step_k<T, D, 1, 4, STEP>(s, a, st);
+    launch_step_k<T, D, 1, 1, STEP>(s, a, st);
   }
-  GDN_STEP(1);
-#undef GDN_STEP
 }
 
 template <bool STEP>
