@@ -124,6 +124,7 @@ struct StepArgs {
   const float *w_conv, *A_log, *dt_bias, *w_norm;
   float scale, l2_eps, norm_eps;
   int act;
+  int through;                                  // set by the launcher: write states through
   gdn_cache cache;
   const int32_t *slot_in, *slot_out, *slot_tok, *cu;
   void* out;

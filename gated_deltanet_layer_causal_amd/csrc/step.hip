@@ -63,9 +63,12 @@ template <int D, int HW, int SPLIT> struct StepGeo {
 };
 
 template <int D, int HW, int SPLIT> struct StepLds {
+  // One helper wave takes o out of v's buffer before it puts the block after
+  // next there; of several, one could be a step ahead: a third buffer.
+  static constexpr int NV = StepGeo<D, HW, SPLIT>::HELPERS > 1 ? 3 : 2;
   float q[2][STEP_TB][D], k[2][STEP_TB][D];
-  float v[2][HW][STEP_TB][D / SPLIT];                               // v, then o in its place
-  float eg[2][HW][STEP_TB], beta[2][HW][STEP_TB];
+  float v[NV][HW][STEP_TB][D / SPLIT];                              // v, then o in its place
+  float eg[2][HW][STEP_TB], beta[2][HW][STEP_TB], kq[2][STEP_TB];   // kq: k . q
   int tok[2][STEP_TB];                                              // slot_tok, -1: none
 };
 
@@ -74,6 +77,7 @@ template <int D, int HW, int SPLIT> struct StepLds {
 // i / nb, block i % nb).  v0: the first value row of those that share a head.
 struct StepSpan {
   int t0, t1, s_in, s_out, h0, h1, kh, nb, items, v0;
+  bool all;   // all heads of kh are here
 };
 
 // A head's state: its load, its tokens, its store.
@@ -122,15 +126,15 @@ template <int D, int SPLIT> struct StepState {
   }
   __device__ __forceinline__ void store(const StepArgs& p, int slot, int h) const {
     const auto rs = head(p, slot, h);
-    if (gridDim.x >= STEP_THROUGH) store_as<CACHE_NT | CACHE_SC1>(rs);
+    if (p.through) store_as<CACHE_NT | CACHE_SC1>(rs);
     else store_as<CACHE_NT>(rs);
   }
   // One token; its outputs take the place of v.  k and q pass through
   // registers 4 columns at a time, and k again for the update: 16 columns of
   // both would not fit beside the state.
-  __device__ __forceinline__ void token(const float* sq, const float* sk, float* sv, float eg,
-                                        float beta, int lane) {
-    float kq = 0.f, s[G::R], r[G::R], v[G::R];
+  __device__ __forceinline__ void token(const float* sq, const float* sk, float* sv, float kq,
+                                        float eg, float beta, int lane) {
+    float s[G::R], r[G::R], v[G::R];
 #pragma unroll
     for (int j = 0; j < G::R; ++j) {
       s[j] = r[j] = 0.f;
@@ -141,16 +145,13 @@ template <int D, int SPLIT> struct StepState {
       const floatx4 k = *reinterpret_cast<const floatx4*>(sk + col0 + 4 * G::LPR * c);
       const floatx4 q = *reinterpret_cast<const floatx4*>(sq + col0 + 4 * G::LPR * c);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        kq = fmaf(k[m], q[m], kq);
+      for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int j = 0; j < G::R; ++j) {
           s[j] = fmaf(S[j][c][m], k[m], s[j]);
           r[j] = fmaf(S[j][c][m], q[m], r[j]);
         }
-      }
     }
-    kq = lanes_sum<G::LPR>(kq);
 #pragma unroll
     for (int j = 0; j < G::R; ++j) {
       s[j] = lanes_sum<G::LPR>(s[j]);
@@ -185,12 +186,12 @@ __device__ __forceinline__ void step_state_wave(const StepArgs& p, const StepSpa
   int h = w.h0 + hw, blk = 0;
   if (h < w.h1) st.load(p, w.s_in, h);
   for (int i = 0; i < w.items; ++i) {
-    const int buf = i & 1;
+    const int buf = i & 1, vb = i % StepLds<D, HW, SPLIT>::NV;
     const int left = w.t1 - w.t0 - blk * STEP_TB;
     const int nt = h >= w.h1 ? 0 : left < STEP_TB ? left : STEP_TB;
     __syncthreads();   // q, k, v of item i are in LDS
     for (int j = 0; j < nt; ++j) {
-      st.token(lds.q[buf][j], lds.k[buf][j], lds.v[buf][hw][j], lds.eg[buf][hw][j],
+      st.token(lds.q[buf][j], lds.k[buf][j], lds.v[vb][hw][j], lds.kq[buf][j], lds.eg[buf][hw][j],
                lds.beta[buf][hw][j], lane);
       if (p.slot_tok) {
         const int slot = __builtin_amdgcn_readfirstlane(lds.tok[buf][j]);
@@ -207,6 +208,11 @@ __device__ __forceinline__ void step_state_wave(const StepArgs& p, const StepSpa
   __syncthreads();     // the last outputs are in LDS
 }
 
+template <typename T> __device__ __forceinline__ void st_raw8(T* p, const Raw8<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = r.v[i];
+}
+
 // The helper waves; `lane` counts through them.  A conv lane forms 8 channels
 // of q, k or one head's v of every token, with the conv's window in
 // registers; the lanes behind them form the gate of one token and head each.
@@ -215,8 +221,9 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
                                                  StepLds<D, HW, SPLIT>& lds, int hk, int hv, int lane) {
   typedef StepGeo<D, HW, SPLIT> G;
   constexpr int G8 = D / 8, V8 = G::VC / 8;      // lanes of a q or k row, of a v row
+  constexpr int NV = StepLds<D, HW, SPLIT>::NV;
   constexpr int NL = 64 * G::HELPERS, NP = (HW * STEP_TB * V8 + NL - 1) / NL;
-  constexpr int AHEAD = (sizeof(T) == 2 ? 4 : 2) / (HW == 3 ? 2 : 1);   // rows of x in flight (registers)
+  constexpr int AHEAD = (sizeof(T) == 2 ? 4 : 2) / (HW == 3 || (HW == 2 && sizeof(T) == 4) ? 2 : 1);   // rows of x in flight (registers)
   const int C = 2 * hk * D + hv * D;
   // part: 0 q, 1 k, 2 + i v of the round's head i; e: the first of 8 channels
   const int part = SPLIT == 1 || lane < 2 * G8 ? lane / G8 : 2 + (lane - 2 * G8) / V8;
@@ -224,35 +231,47 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
   const int gh = (lane - G::CONV_LANES) / STEP_TB, gt = (lane - G::CONV_LANES) % STEP_TB;   // the gate's
   T* out = (T*)p.out;
   // rule: this lane's tensor and its row stride
-  const T* lane_src = (const T*)p.q;
-  int64_t lane_ld = p.ldq;
-  if (part == 1) { lane_src = (const T*)p.k; lane_ld = p.ldk; }
-  if (part >= 2) { lane_src = (const T*)p.v; lane_ld = p.ldv; }
+  const T* lane_src = STEP ? nullptr : (const T*)p.q;
+  int64_t lane_ld = STEP ? 0 : p.ldq;
+  if (!STEP && part == 1) { lane_src = (const T*)p.k; lane_ld = p.ldk; }
+  if (!STEP && part >= 2) { lane_src = (const T*)p.v; lane_ld = p.ldv; }
+  struct Item { int hr, tb; };                   // an item's first head and first token
   float wr[8][4];
-  f8 x3, x2, x1;                                 // the window: x[t-3], x[t-2], x[t-1]
+  Raw8<T> x3, x2, x1;                            // the window: x[t-3], x[t-2], x[t-1]
+  constexpr bool Z_AHEAD = sizeof(T) == 2;       // z's rows a block ahead (registers)
   Raw8<T> z[NP];
+  Raw8<T> raw[AHEAD];                            // rows of x on their way
 
-  auto prep = [&](int i) __attribute__((always_inline)) {
-    const int buf = i & 1, hr = w.h0 + i / w.nb * HW;   // the round's first head
-    const int tb = w.t0 + i % w.nb * STEP_TB;
+  // Requests the rows of x of an item's tokens j0 .. (past the last token: that one again).
+  auto fetch = [&](const Item& at, int j0) __attribute__((always_inline)) {
+    if constexpr (STEP) {
+      const int h = at.hr + vh, t = at.tb + j0;
+      if (lane < G::CONV_LANES && (part < 2 || h < w.h1)) {
+        const T* x = (const T*)p.x + (part == 0 ? w.kh : part == 1 ? hk + w.kh : 2 * hk + h) * D + e;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) raw[j] = ld_raw8(x + (t + j < w.t1 ? t + j : w.t1 - 1) * p.ldx);
+      }
+    }
+  };
+  auto prep = [&](int i, const Item& at) __attribute__((always_inline)) {
+    const int buf = i & 1, vb = i % NV, hr = at.hr, tb = at.tb;
     const int nt = w.t1 - tb < STEP_TB ? w.t1 - tb : STEP_TB;
     if (lane < G::CONV_LANES) {
       const int h = hr + vh;
       if (part >= 2 && h >= w.h1) return;
       // this lane's channel: of x, or of q, k or v
       const int ch = (STEP ? part == 0 ? w.kh : part == 1 ? hk + w.kh : 2 * hk + h : part < 2 ? w.kh : h) * D + (part < 2 ? 0 : w.v0) + e;
-      float* dst = (part == 0 ? lds.q[buf][0] : part == 1 ? lds.k[buf][0] : lds.v[buf][vh][0]) + e;
+      float* dst = (part == 0 ? lds.q[buf][0] : part == 1 ? lds.k[buf][0] : lds.v[vb][vh][0]) + e;
       const int dst_ld = part < 2 ? D : G::VC;
       if constexpr (STEP) {
         if (tb == w.t0) {
           const T* rows = (const T*)p.cache.conv + (int64_t)w.s_in * p.cache.conv_stride + ch;
           if (w.s_in >= 0) {
-            x3 = load8(rows);
-            x2 = load8(rows + C);
-            x1 = load8(rows + 2 * C);
+            x3 = ld_raw8(rows);
+            x2 = ld_raw8(rows + C);
+            x1 = ld_raw8(rows + 2 * C);
           } else {
-#pragma unroll
-            for (int m = 0; m < 8; ++m) x3.v[m] = x2.v[m] = x1.v[m] = 0.f;
+            x3 = x2 = x1 = zero_raw8<T>();
           }
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
@@ -261,31 +280,32 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
           }
         }
         // the rows of v's channels have served when their head has; those of
-        // q and k are read again in the next round
-        const bool put_rows = part >= 2 || hr + HW >= w.h1;
+        // q and k are read again in the next round, or by other workgroups
+        const bool put_rows = part >= 2 || (w.all && hr + HW >= w.h1);
         auto put = [&](int slot) __attribute__((always_inline)) {
           T* rows = (T*)p.cache.conv + (int64_t)slot * p.cache.conv_stride + ch;
-          store8(rows, x3);
-          store8(rows + C, x2);
-          store8(rows + 2 * C, x1);
+          st_raw8(rows, x3);
+          st_raw8(rows + C, x2);
+          st_raw8(rows + 2 * C, x1);
         };
         for (int j0 = 0; j0 < nt; j0 += AHEAD) {
-          Raw8<T> raw[AHEAD];
-#pragma unroll
-          for (int j = 0; j < AHEAD; ++j) {        // rows past the last token: that one again
-            const int t = tb + j0 + j < w.t1 ? tb + j0 + j : w.t1 - 1;
-            raw[j] = ld_raw8((const T*)p.x + t * p.ldx + ch);
-          }
+          if (j0 > 0) fetch(at, j0);
 #pragma unroll
           for (int j = 0; j < AHEAD; ++j) {
             if (j0 + j < nt) {
-              const f8 x0 = raw_f8(raw[j]);
-              f8 y;
+              f8 y{};
+              auto tap = [&](int i, const f8& xr) __attribute__((always_inline)) {
+#pragma unroll
+                for (int m = 0; m < 8; ++m) y.v[m] = fmaf(wr[m][i], xr.v[m], y.v[m]);
+              };
+              tap(0, raw_f8(x3));
+              tap(1, raw_f8(x2));
+              tap(2, raw_f8(x1));
+              tap(3, raw_f8(raw[j]));
               float ss = 0.f;
 #pragma unroll
               for (int m = 0; m < 8; ++m) {
-                const float u = wr[m][0] * x3.v[m] + wr[m][1] * x2.v[m] + wr[m][2] * x1.v[m] + wr[m][3] * x0.v[m];
-                y.v[m] = u * sigmoidf_(u);
+                y.v[m] *= sigmoidf_(y.v[m]);
                 ss += y.v[m] * y.v[m];
               }
               ss = lane_group_sum<G8>(ss);
@@ -295,7 +315,7 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
               store8(dst + (j0 + j) * dst_ld, y);
               x3 = x2;
               x2 = x1;
-              x1 = x0;
+              x1 = raw[j];
               if (put_rows && p.slot_tok) {
                 const int slot = p.slot_tok[tb + j0 + j];
                 if (slot >= 0 && slot < p.cache.n_slots) put(slot);
@@ -318,6 +338,16 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
             store8(dst + j * dst_ld, y);
           }
       }
+      if (part == 1)   // k . q, when q's lanes, of the same wave, have put theirs
+#pragma unroll 2
+        for (int j = 0; j < nt; ++j) {
+          const f8 k = load8(&lds.k[buf][j][e]), q = load8(&lds.q[buf][j][e]);
+          float kq = 0.f;
+#pragma unroll
+          for (int m = 0; m < 8; ++m) kq = fmaf(k.v[m], q.v[m], kq);
+          kq = lane_group_sum<G8>(kq);
+          if (e == 0) lds.kq[buf][j] = kq;
+        }
     } else if (gh < HW && gt < nt && hr + gh < w.h1) {
       const int h = hr + gh;
       const int64_t t = tb + gt;
@@ -336,67 +366,80 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
     }
   };
   // outputs: lane = (head, token, 8 channels)
-  auto each_out = [&](int i, auto&& f) __attribute__((always_inline)) {
-    const int tb = w.t0 + i % w.nb * STEP_TB;
+  auto each_out = [&](const Item& at, auto&& f) __attribute__((always_inline)) {
+    const int tb = at.tb;
 #pragma unroll
     for (int s = 0; s < NP; ++s) {
       const int job = (s * NL + lane) / V8, hi = job / STEP_TB, j = job % STEP_TB;
-      const int h = w.h0 + i / w.nb * HW + hi;
+      const int h = at.hr + hi;
       if (hi < HW && h < w.h1 && tb + j < w.t1) f(s, hi, j, (int64_t)(tb + j), h);
     }
   };
   const int oe = lane % V8 * 8;
-  auto load_z = [&](int i) __attribute__((always_inline)) {
-    if constexpr (STEP)
-      each_out(i, [&](int s, int hi, int j, int64_t t, int h) __attribute__((always_inline)) {
+  f8 wn{};                                       // the norm's 1 + w
+  if constexpr (STEP) {
+    wn = load8(p.w_norm + oe);
+#pragma unroll
+    for (int m = 0; m < 8; ++m) wn.v[m] += 1.f;
+  }
+  auto load_z = [&](const Item& at) __attribute__((always_inline)) {
+    if constexpr (STEP && Z_AHEAD)
+      each_out(at, [&](int s, int hi, int j, int64_t t, int h) __attribute__((always_inline)) {
         z[s] = ld_raw8((const T*)p.z + t * p.ldz + h * D + oe);
       });
   };
-  auto finish = [&](int i) __attribute__((always_inline)) {
-    each_out(i, [&](int s, int hi, int j, int64_t t, int h) __attribute__((always_inline)) {
-      f8 o = load8(&lds.v[i & 1][hi][j][oe]);
+  auto finish = [&](int i, const Item& at) __attribute__((always_inline)) {
+    each_out(at, [&](int s, int hi, int j, int64_t t, int h) __attribute__((always_inline)) {
+      f8 o = load8(&lds.v[i % NV][hi][j][oe]);
       if constexpr (STEP) {
         float ss = 0.f;
 #pragma unroll
         for (int m = 0; m < 8; ++m) ss += o.v[m] * o.v[m];
         ss = lane_group_sum<G8>(ss);
         const float rho = rsqrtf(ss * (1.f / D) + p.norm_eps);
-        const f8 wn = load8(p.w_norm + oe), zv = raw_f8(z[s]);
+        const f8 zv = Z_AHEAD ? raw_f8(z[s]) : load8((const T*)p.z + t * p.ldz + h * D + oe);
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
           const float sg = sigmoidf_(zv.v[m]);
-          o.v[m] *= rho * (1.f + wn.v[m]) * (p.act == 0 ? zv.v[m] * sg : sg);
+          o.v[m] *= rho * wn.v[m] * (p.act == 0 ? zv.v[m] * sg : sg);
         }
       }
       store8(out + t * hv * D + h * D + w.v0 + oe, o);
     });
   };
 
-  if (w.items == 0) return;
-  prep(0);
+  Item prev{}, cur{}, next{w.h0, w.t0};          // items i - 1, i, i + 1
+  fetch(next, 0);
+  prep(0, next);
   for (int i = 0; i < w.items; ++i) {
+    prev = cur;
+    cur = next;
+    next.tb += STEP_TB;
+    if (next.tb >= w.t1) next = {cur.hr + HW, w.t0};
     __syncthreads();
-    if (i > 0) finish(i - 1);
-    load_z(i);
-    if (i + 1 < w.items) prep(i + 1);
+    if (i + 1 < w.items) fetch(next, 0);
+    if (i > 0) finish(i - 1, prev);
+    load_z(cur);
+    if (i + 1 < w.items) prep(i + 1, next);
   }
   __syncthreads();
-  finish(w.items - 1);
+  finish(w.items - 1, cur);
 }
 
 template <typename T, int D, int HW, int SPLIT, bool STEP>
 __global__ void __launch_bounds__((StepGeo<D, HW, SPLIT>::THREADS), 4) step_kernel(StepArgs p, int hk, int hv,
-                                                                                 int T_tok) {
+                                                                                 int heads, int T_tok) {
   static_assert(SPLIT == 1 || (!STEP && HW == 1), "the norm needs whole rows");
   typedef StepGeo<D, HW, SPLIT> G;
   __shared__ StepLds<D, HW, SPLIT> lds;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int heads = STEP ? hv / hk : 1, per = hv / heads * SPLIT, n = blockIdx.x / per;
+  const int per = hv / heads * SPLIT, n = blockIdx.x / per;
   StepSpan w;
   w.h0 = blockIdx.x % per / SPLIT * heads;
   w.v0 = blockIdx.x % SPLIT * G::VC;
   w.h1 = w.h0 + heads;
   w.kh = w.h0 / (hv / hk);
+  w.all = heads == hv / hk;
   token_range(p.cu, n, T_tok, w.t0, w.t1);
   w.s_in = slot_of(p.slot_in, n);
   w.s_out = slot_of(p.slot_out, n);
@@ -416,9 +459,9 @@ __global__ void __launch_bounds__((StepGeo<D, HW, SPLIT>::THREADS), 4) step_kern
         st.store(p, w.s_out, h);
       }
     } else if constexpr (STEP) {
-      const int C = 2 * hk * D + hv * D, n_grp = (2 + heads) * D / 8;
+      const int C = 2 * hk * D + hv * D, first = w.all ? 0 : 2, n_grp = (2 - first + heads) * D / 8;
       for (int g = tid - 64 * HW * G::WAVES; g < n_grp * 3; g += 64 * G::HELPERS) {
-        const int e = g % n_grp * 8, hd = e / D;
+        const int e = g % n_grp * 8, hd = first + e / D;
         const int64_t ch = (hd == 0 ? w.kh : hd == 1 ? hk + w.kh : 2 * hk + w.h0 + hd - 2) * D + e % D +
                            (int64_t)(g / n_grp) * C;
         store8((T*)p.cache.conv + (int64_t)w.s_out * p.cache.conv_stride + ch,
@@ -433,32 +476,85 @@ __global__ void __launch_bounds__((StepGeo<D, HW, SPLIT>::THREADS), 4) step_kern
   else step_helper_wave<T, D, HW, SPLIT, STEP>(p, w, lds, hk, hv, tid - 64 * HW * G::WAVES);
 }
 
+// The conv rows of q's and k's channels, where a key head's value heads were
+// in several workgroups and none of them could write what the others read:
+// after token t the last three input rows are x[t-2], x[t-1], x[t], reaching
+// back into the rows of slot_in.  A thread owns 8 channels of one sequence
+// and reads the rows it needs before it writes any.
+template <typename T>
+__global__ void __launch_bounds__(256) step_rows_kernel(StepArgs p, int n_grp, int C, int T_tok) {
+  const int n = blockIdx.y, grp = blockIdx.x * 256 + threadIdx.x;
+  if (grp >= n_grp) return;
+  int t0, t1;
+  token_range(p.cu, n, T_tok, t0, t1);
+  const int s_in = slot_of(p.slot_in, n), s_out = slot_of(p.slot_out, n);
+  if (s_in >= p.cache.n_slots || s_out >= p.cache.n_slots) return;
+  const T* x = (const T*)p.x + grp * 8;
+  T* rows = (T*)p.cache.conv + grp * 8;
+  Raw8<T> w[3];
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+    w[j] = s_in >= 0 ? ld_raw8(rows + (int64_t)s_in * p.cache.conv_stride + j * C) : zero_raw8<T>();
+  auto put = [&](int slot) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) st_raw8(rows + (int64_t)slot * p.cache.conv_stride + j * C, w[j]);
+  };
+  // without slots for single tokens only the last three rows matter
+  for (int t = p.slot_tok || t1 - t0 < 3 ? t0 : t1 - 3; t < t1; ++t) {
+    w[0] = w[1];
+    w[1] = w[2];
+    w[2] = ld_raw8(x + (int64_t)t * p.ldx);
+    if (p.slot_tok) {
+      const int st = p.slot_tok[t];
+      if (st >= 0 && st < p.cache.n_slots) put(st);
+    }
+  }
+  if (s_out >= 0 && (t1 > t0 || s_out != s_in)) put(s_out);
+}
+
 template <typename T, int D, int HW, int SPLIT, bool STEP>
-static void launch_step_k(const gdn_shape& s, const StepArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((step_kernel<T, D, HW, SPLIT, STEP>),
-                     dim3((unsigned)s.n_seq * (unsigned)(STEP ? s.hk : s.hv) * SPLIT),
-                     dim3(StepGeo<D, HW, SPLIT>::THREADS), 0, st, a, s.hk, s.hv, (int)s.total_tokens);
+static void launch_step_k(const gdn_shape& s, StepArgs a, int heads, hipStream_t st) {
+  const unsigned grid = (unsigned)s.n_seq * (unsigned)(s.hv / heads) * SPLIT;
+  a.through = grid >= STEP_THROUGH;
+  hipLaunchKernelGGL((step_kernel<T, D, HW, SPLIT, STEP>), dim3(grid),
+                     dim3(StepGeo<D, HW, SPLIT>::THREADS), 0, st, a, s.hk, s.hv, heads,
+                     (int)s.total_tokens);
 }
 
 template <typename T, int D, bool STEP>
 static void launch_step_d(const gdn_shape& s, const StepArgs& a, hipStream_t st) {
   if constexpr (STEP) {
+    const int group = s.hv / s.hk;
+    const int64_t groups = (int64_t)s.n_seq * s.hk;
+    // A workgroup's tokens take about 1 us each and head: where they are many
+    // and workgroups few, three or more heads of a group go apart, which costs
+    // the second launch (4 sequences, 48 heads over 16: 8 tokens 23.5 us
+    // against 25.7 us together, 48 tokens 68 against 99 us; 8 heads over 2:
+    // 61 against 133 us; 256 key heads, 16 tokens: 61 against 45 us).
+    const bool apart = group >= 3 && groups <= 128 && s.total_tokens >= 8 * (int64_t)s.n_seq;
+    if (apart) {
+      launch_step_k<T, D, 1, 1, STEP>(s, a, 1, st);
+      const int C = 2 * s.hk * D + s.hv * D, n_grp = 2 * s.hk * D / 8;
+      if (a.slot_out || a.slot_tok)
+        hipLaunchKernelGGL((step_rows_kernel<T>), dim3((n_grp + 255) / 256, s.n_seq), dim3(256), 0, st, a,
+                           n_grp, C, (int)s.total_tokens);
+      return;
+    }
     // Value heads at a time.  With few workgroups all of a key head's together
     // (one sequence, 48 heads over 16: 9.4 us against 13.6 us one by one; 64
     // sequences 77 against 88 us); with many, one by one in smaller workgroups
     // overlap better (256 sequences 294 against 302 us, 32 heads 198 against
     // 211 us).  They meet at about 2000 workgroups.
-    const int group = s.hv / s.hk;
-    if (group == 1 || (int64_t)s.n_seq * s.hk >= 2048) launch_step_k<T, D, 1, 1, STEP>(s, a, st);
-    else if (group == 2 || group == 4) launch_step_k<T, D, 2, 1, STEP>(s, a, st);
-    else launch_step_k<T, D, 3, 1, STEP>(s, a, st);
+    if (group == 1 || groups >= 2048) launch_step_k<T, D, 1, 1, STEP>(s, a, group, st);
+    else if (group == 2 || group == 4 || D == 32) launch_step_k<T, D, 2, 1, STEP>(s, a, group, st);
+    else if constexpr (D == 128) launch_step_k<T, D, 3, 1, STEP>(s, a, group, st);
   } else {
     // A head over four workgroups while that still fills the chip's 256 CUs:
     // 8 heads 4.2 us against 5.0 us for one token, 13.8 against 28.0 us for
     // 32; 192 heads 25.0 against 32.0 us; 384 heads 46.3 against 45.1 us.
     if constexpr (D == 128)
-      if ((int64_t)s.n_seq * s.hv <= 256) return launch_step_k<T, D, 1, 4, STEP>(s, a, st);
-    launch_step_k<T, D, 1, 1, STEP>(s, a, st);
+      if ((int64_t)s.n_seq * s.hv <= 256) return launch_step_k<T, D, 1, 4, STEP>(s, a, 1, st);
+    launch_step_k<T, D, 1, 1, STEP>(s, a, 1, st);
   }
 }
 

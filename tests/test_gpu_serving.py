@@ -136,6 +136,13 @@ CASES = {
     "small_bf16_strided": dict(dtype="bf16", hk=3, hv=9, d=32, lens=[1] * 7, strided=True),
     "small_fp16_sigmoid": dict(dtype="fp16", hk=1, hv=8, d=32, lens=[2, 65, 1], act=1),
     "one_head_bf16_sigmoid": dict(dtype="bf16", hk=1, hv=1, d=128, lens=[4], act=1),
+    # heads of a group in several rounds, the last not full; long enough to go apart, or not
+    "five_of_a_group_bf16": dict(dtype="bf16", hk=1, hv=5, d=128, lens=[9, 1, 20, 3]),
+    "four_of_a_group_fp32": dict(dtype="fp32", hk=2, hv=8, d=128, lens=[5, 11, 2, 7, 8, 1]),
+    "seven_of_a_group_fp16_strided": dict(dtype="fp16", hk=1, hv=7, d=32, lens=[17, 0, 1], strided=True),
+    "three_of_a_group_fp32_short": dict(dtype="fp32", hk=3, hv=9, d=128, lens=[1, 6, 0, 2]),
+    # so many groups that their heads go one by one
+    "many_bf16": dict(dtype="bf16", hk=2, hv=4, d=32, lens=[1] * 1000 + [2] * 40),
 }
 
 
@@ -164,11 +171,16 @@ def test_step_matches_the_oracle(name, mode):
     c.check(got, c.ref(slot_in, slot_out, slot_tok))
 
 
-@pytest.mark.parametrize("name", ["decode_bf16", "ragged_fp16", "ragged_fp32", "small_fp32", "small_bf16_strided"])
+CASES_RULE = dict(CASES, many_heads_bf16=dict(dtype="bf16", hk=1, hv=64, d=128, lens=[1, 3, 9, 0, 1]),
+                  many_heads_fp32=dict(dtype="fp32", hk=64, hv=64, d=128, lens=[2, 1, 1, 1, 10]))
+
+
+@pytest.mark.parametrize("name", ["decode_bf16", "ragged_fp16", "ragged_fp32", "small_fp32", "small_bf16_strided",
+                                  "many_heads_bf16", "many_heads_fp32"])
 @pytest.mark.parametrize("drafts", [False, True])
 def test_recurrent_matches_the_oracle(name, drafts):
     """The rule alone, q, k, v as columns of one tensor."""
-    kw = CASES[name]
+    kw = CASES_RULE[name]
     dtype, hk, hv, d, lens = (kw[x] for x in ("dtype", "hk", "hv", "d", "lens"))
     N, T = len(lens), sum(lens)
     rng = np.random.default_rng(7)
@@ -206,7 +218,7 @@ def test_recurrent_matches_the_oracle(name, drafts):
     assert_close("S", host(cache.S()), S_ref, FP32)
 
 
-@pytest.mark.parametrize("dtype,hk,hv,d", [("bf16", 2, 6, 128), ("fp32", 1, 3, 32)])
+@pytest.mark.parametrize("dtype,hk,hv,d", [("bf16", 2, 6, 128), ("fp32", 1, 3, 32), ("fp16", 1, 4, 128)])
 def test_tokens_one_by_one_equal_one_call(dtype, hk, hv, d):
     """A token's arithmetic does not depend on how the tokens are cut into
     calls: outputs, states and conv rows agree bit by bit."""
@@ -228,6 +240,31 @@ def test_tokens_one_by_one_equal_one_call(dtype, hk, hv, d):
     assert torch.equal(c.cache.S(), after[:, :c.cache.S()[0].numel() * 4].view(torch.float32)
                        .view_as(c.cache.S()))
     assert torch.equal(c.cache.buffer, after)
+
+
+@pytest.mark.parametrize("hk,hv,d,N", [(4, 16, 128, 40), (2, 6, 128, 100), (1, 5, 32, 300), (16, 32, 128, 160)])
+def test_runs_repeat_bit_by_bit(hk, hv, d, N):
+    """The same call on the same states, again and again: helper and state
+    waves meet at their barriers whichever is ahead."""
+    torch.manual_seed(N)
+    core = GDNCore(CoreConfig(hk, hv, d), DEV)
+    cache = GDNStateCache(core.cfg, N, device=DEV)
+    lens = [1 + (7 * n) % 20 for n in range(N)]
+    T, C, bf = sum(lens), core.cfg.channels, torch.bfloat16
+    r = lambda *s: torch.randn(*s, device=DEV)  # noqa: E731
+    args = (r(T, C).to(bf), 0.25 * r(C, 4), r(T, hv).to(bf), r(T, hv).to(bf), -r(hv).abs(), r(hv), r(T, hv, d).to(bf),
+            0.1 * r(d), ints(np.concatenate([[0], np.cumsum(lens)])))
+    cache.buffer.zero_()
+    cache.S().normal_()
+    cache.conv().normal_()
+    start, slots = cache.buffer.clone(), ints(np.random.default_rng(0).permutation(N))
+    want = core.step(*args, cache, slots)
+    after = cache.buffer.clone()
+    assert bool(torch.isfinite(want).all())
+    for k in range(25):
+        cache.buffer.copy_(start)
+        got = core.step(*args, cache, slots)
+        assert torch.equal(got, want) and torch.equal(cache.buffer, after), k
 
 
 def test_no_tokens_pass_states_through():
