@@ -68,7 +68,7 @@ template <int D, int HW, int SPLIT> struct StepLds {
   static constexpr int NV = StepGeo<D, HW, SPLIT>::HELPERS > 1 ? 3 : 2;
   float q[2][STEP_TB][D], k[2][STEP_TB][D];
   float v[NV][HW][STEP_TB][D / SPLIT];                              // v, then o in its place
-  float eg[2][HW][STEP_TB], beta[2][HW][STEP_TB], kq[2][STEP_TB];   // kq: k . q
+  float eg[2][HW][STEP_TB], beta[2][HW][STEP_TB];
   int tok[2][STEP_TB];                                              // slot_tok, -1: none
 };
 
@@ -132,9 +132,9 @@ template <int D, int SPLIT> struct StepState {
   // One token; its outputs take the place of v.  k and q pass through
   // registers 4 columns at a time, and k again for the update: 16 columns of
   // both would not fit beside the state.
-  __device__ __forceinline__ void token(const float* sq, const float* sk, float* sv, float kq,
-                                        float eg, float beta, int lane) {
-    float s[G::R], r[G::R], v[G::R];
+  __device__ __forceinline__ void token(const float* sq, const float* sk, float* sv, float eg,
+                                        float beta, int lane) {
+    float kq = 0.f, s[G::R], r[G::R], v[G::R];
 #pragma unroll
     for (int j = 0; j < G::R; ++j) {
       s[j] = r[j] = 0.f;
@@ -145,13 +145,16 @@ template <int D, int SPLIT> struct StepState {
       const floatx4 k = *reinterpret_cast<const floatx4*>(sk + col0 + 4 * G::LPR * c);
       const floatx4 q = *reinterpret_cast<const floatx4*>(sq + col0 + 4 * G::LPR * c);
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
+      for (int m = 0; m < 4; ++m) {
+        kq = fmaf(k[m], q[m], kq);
 #pragma unroll
         for (int j = 0; j < G::R; ++j) {
           s[j] = fmaf(S[j][c][m], k[m], s[j]);
           r[j] = fmaf(S[j][c][m], q[m], r[j]);
         }
+      }
     }
+    kq = lanes_sum<G::LPR>(kq);
 #pragma unroll
     for (int j = 0; j < G::R; ++j) {
       s[j] = lanes_sum<G::LPR>(s[j]);
@@ -191,7 +194,7 @@ __device__ __forceinline__ void step_state_wave(const StepArgs& p, const StepSpa
     const int nt = h >= w.h1 ? 0 : left < STEP_TB ? left : STEP_TB;
     __syncthreads();   // q, k, v of item i are in LDS
     for (int j = 0; j < nt; ++j) {
-      st.token(lds.q[buf][j], lds.k[buf][j], lds.v[vb][hw][j], lds.kq[buf][j], lds.eg[buf][hw][j],
+      st.token(lds.q[buf][j], lds.k[buf][j], lds.v[vb][hw][j], lds.eg[buf][hw][j],
                lds.beta[buf][hw][j], lane);
       if (p.slot_tok) {
         const int slot = __builtin_amdgcn_readfirstlane(lds.tok[buf][j]);
@@ -223,14 +226,15 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
   constexpr int G8 = D / 8, V8 = G::VC / 8;      // lanes of a q or k row, of a v row
   constexpr int NV = StepLds<D, HW, SPLIT>::NV;
   constexpr int NL = 64 * G::HELPERS, NP = (HW * STEP_TB * V8 + NL - 1) / NL;
-  constexpr int AHEAD = (sizeof(T) == 2 ? 4 : 2) / (HW == 3 || (HW == 2 && sizeof(T) == 4) ? 2 : 1);   // rows of x in flight (registers)
+  // the step: rows of x on their way while the norm runs, as many as registers allow
+  constexpr int AHEAD = (sizeof(T) == 2 ? 4 : 2) / (HW == 3 || (HW == 2 && sizeof(T) == 4) ? 2 : 1);
   const int C = 2 * hk * D + hv * D;
   // part: 0 q, 1 k, 2 + i v of the round's head i; e: the first of 8 channels
   const int part = SPLIT == 1 || lane < 2 * G8 ? lane / G8 : 2 + (lane - 2 * G8) / V8;
   const int vh = part < 2 ? 0 : part - 2, e = (part < 2 ? lane % G8 : lane % V8) * 8;
   const int gh = (lane - G::CONV_LANES) / STEP_TB, gt = (lane - G::CONV_LANES) % STEP_TB;   // the gate's
   T* out = (T*)p.out;
-  // rule: this lane's tensor and its row stride
+  // the rule: this lane's tensor and its row stride
   const T* lane_src = STEP ? nullptr : (const T*)p.q;
   int64_t lane_ld = STEP ? 0 : p.ldq;
   if (!STEP && part == 1) { lane_src = (const T*)p.k; lane_ld = p.ldk; }
@@ -240,7 +244,7 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
   Raw8<T> x3, x2, x1;                            // the window: x[t-3], x[t-2], x[t-1]
   constexpr bool Z_AHEAD = sizeof(T) == 2;       // z's rows a block ahead (registers)
   Raw8<T> z[NP];
-  Raw8<T> raw[AHEAD];                            // rows of x on their way
+  Raw8<T> raw[AHEAD];
 
   // Requests the rows of x of an item's tokens j0 .. (past the last token: that one again).
   auto fetch = [&](const Item& at, int j0) __attribute__((always_inline)) {
@@ -259,8 +263,8 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
     if (lane < G::CONV_LANES) {
       const int h = hr + vh;
       if (part >= 2 && h >= w.h1) return;
-      // this lane's channel: of x, or of q, k or v
-      const int ch = (STEP ? part == 0 ? w.kh : part == 1 ? hk + w.kh : 2 * hk + h : part < 2 ? w.kh : h) * D + (part < 2 ? 0 : w.v0) + e;
+      // the step: this lane's channel of x
+      const int ch = (part == 0 ? w.kh : part == 1 ? hk + w.kh : 2 * hk + h) * D + e;
       float* dst = (part == 0 ? lds.q[buf][0] : part == 1 ? lds.k[buf][0] : lds.v[vb][vh][0]) + e;
       const int dst_ld = part < 2 ? D : G::VC;
       if constexpr (STEP) {
@@ -326,28 +330,19 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
         if (put_rows && w.s_out >= 0 && tb + nt == w.t1) put(w.s_out);
       } else {
         const float r = part == 0 ? p.scale : 1.f;
-        Raw8<T> raw[STEP_TB];                    // rows past the last token: that one again
+        const T* src = lane_src + (part < 2 ? w.kh * D : h * D + w.v0) + e;
+        Raw8<T> rows[STEP_TB];                   // rows past the last token: that one again
 #pragma unroll
-        for (int j = 0; j < STEP_TB; ++j) raw[j] = ld_raw8(lane_src + (tb + j < w.t1 ? tb + j : w.t1 - 1) * lane_ld + ch);
+        for (int j = 0; j < STEP_TB; ++j) rows[j] = ld_raw8(src + (tb + j < w.t1 ? tb + j : w.t1 - 1) * lane_ld);
 #pragma unroll
         for (int j = 0; j < STEP_TB; ++j)
           if (j < nt) {
-            f8 y = raw_f8(raw[j]);
+            f8 y = raw_f8(rows[j]);
 #pragma unroll
             for (int m = 0; m < 8; ++m) y.v[m] *= r;
             store8(dst + j * dst_ld, y);
           }
       }
-      if (part == 1)   // k . q, when q's lanes, of the same wave, have put theirs
-#pragma unroll 2
-        for (int j = 0; j < nt; ++j) {
-          const f8 k = load8(&lds.k[buf][j][e]), q = load8(&lds.q[buf][j][e]);
-          float kq = 0.f;
-#pragma unroll
-          for (int m = 0; m < 8; ++m) kq = fmaf(k.v[m], q.v[m], kq);
-          kq = lane_group_sum<G8>(kq);
-          if (e == 0) lds.kq[buf][j] = kq;
-        }
     } else if (gh < HW && gt < nt && hr + gh < w.h1) {
       const int h = hr + gh;
       const int64_t t = tb + gt;
