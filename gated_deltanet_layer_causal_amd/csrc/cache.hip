@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) compact_plan_kernel(
 // throughout.  One 16-byte word a thread in workgroups that follow each other
 // through memory, non-temporal and written through: the fewer bytes are under
 // way at once, the more of them share DRAM pages (49 slots of 9.6 MB: 171 us
-// with 64 bytes a thread and plain accesses, 156 us non-temporal and 16).
+// with 64 bytes a thread and plain accesses, 156 us with 16 and non-temporal,
+// 151 us written through as well).
 __device__ __forceinline__ void copy_piece(const char* src, uint32_t fill, char* dst, int64_t at,
                                            int64_t bytes) {
   const uint32_t left = bytes - at < PIECE ? (uint32_t)(bytes - at) : PIECE, o = threadIdx.x * 16;
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(256) cache_count_kernel(int32_t* refs, int n_s
   const int s = slots[i];
   if (s < 0 || s >= n_slots) return;
   int32_t have = refs[s];
-  while (have > 0) {
+  while (have > 0 && !(delta > 0 && have == 0x7fffffff)) {   // free slots, and a full count, stay
     const int32_t was = atomicCAS(&refs[s], have, have + delta);
     if (was == have) break;
     have = was;

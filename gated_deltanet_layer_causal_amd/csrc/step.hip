@@ -2,12 +2,13 @@
 // rule token by token (gdn_recurrent_fwd), and the whole core for the next
 // tokens of every sequence (gdn_step_fwd).
 //
-// One workgroup owns one sequence and some value heads of one key head: the
-// step all of them (so that it alone reads and writes their conv rows), HW at
-// a time, the rule one or a quarter of one's rows (the rows of S need nothing
-// from each other but k and q).  A head's state S (D x D, fp32) stays in registers
-// from its load to its store, so a call reads and writes each state once
-// however many tokens a sequence has:
+// One workgroup owns one sequence and some value heads of one key head.  The
+// step takes all of them, HW at a time, so that it alone reads and writes
+// their conv rows (or one, and a second launch writes the rows of q and k).
+// The rule takes one, or a quarter of one's rows: the rows of S share nothing
+// but k and q.  A head's state S (D x D, fp32) stays in registers from its
+// load to its store, so a call reads and writes each state once however many
+// tokens a sequence has:
 //   s = S_{t-1} k,  r = S_{t-1} q   (both from the old state, reduced together)
 //   delta = beta (v - e^g s)
 //   o = e^g r + delta (k . q),  S_t = e^g S_{t-1} + delta k^T
@@ -25,7 +26,8 @@
 namespace gdn {
 
 constexpr int STEP_TB = 8;             // tokens per block
-constexpr unsigned STEP_THROUGH = 128; // workgroups from which states are written through
+constexpr unsigned STEP_THROUGH = 128; // workgroups from which states are written through:
+                                       // even at 148 (11.5 us against 11.7 us without)
 
 // Tokens of sequence n, clamped so that no table can lead outside [0, T].
 __device__ __forceinline__ void token_range(const int32_t* cu, int n, int T, int& t0, int& t1) {

@@ -200,12 +200,16 @@ class GDNCore:
 
     def prefill(self, x, w_conv, a, b, A_log, dt_bias, z, w_norm, cu_seqlens, cache, slot_in,
                 slot_out=None, layer=0):
-        """step() for long pieces: the chunked forward from and into slots
-        (contiguous a, b, z as forward(); cu_seqlens[-1] = T).  A slot_in
+        """step() for long pieces (faster from about 100 tokens a sequence):
+        the chunked forward from and into slots (contiguous a, b, z as
+        forward(); cu_seqlens[-1] = T; dtypes and head dims of the chunked form).  A slot_in
         outside the cache gives NaN, a slot_out outside it is not written."""
         c = self.cfg
         n_seq = cu_seqlens.numel() - 1
         slot_out = slot_in if slot_out is None else slot_out
+        if slot_in.numel() != n_seq or slot_out.numel() != n_seq:
+            raise ValueError(f"{n_seq} sequences, {slot_in.numel()} slots to read and "
+                             f"{slot_out.numel()} to write")
         if c.check_slots:
             self.check_slots(self.shape(x.shape[0], n_seq), cache, slot_in, slot_out, None, cu_seqlens)
         S, conv = cache.S(layer), cache.conv(layer)

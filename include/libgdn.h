@@ -349,8 +349,9 @@ typedef struct {
  *   o_t = S_t (scale * q_t)
  * in fp32 whatever the storage type, with no limit on the range of the data.
  * q, k, v, g, beta and o as gdn_chunk_fwd; every dtype at dk = dv = 32 and 128.
- * For single tokens up to short pieces; gdn_chunk_fwd is faster for long ones
- * (its state goes in and out of a cache by gdn_cache_copy). */
+ * For single tokens up to pieces of about 100 tokens a sequence; gdn_chunk_fwd
+ * is faster for longer ones (its states go in and out of a cache by
+ * gdn_cache_copy). */
 gdn_status gdn_recurrent_fwd(const gdn_shape* shape, const void* q, const void* k, const void* v,
                              int64_t ldq, int64_t ldk, int64_t ldv, const float* g,
                              const float* beta, float scale, const gdn_cache* cache,
@@ -408,7 +409,7 @@ gdn_status gdn_cache_fork(void* base, int64_t stride, int32_t n_slots, int32_t* 
 /* One more (retain) or one less (release) user of each slot in slots [n]; a
  * slot named twice counts twice.  Entries outside [0, n_slots) and free slots
  * are left alone, so a count never falls below 0 and retaining a free slot
- * does not take it. */
+ * does not take it; a count of 2^31 - 1 stays there when retained. */
 gdn_status gdn_cache_retain(int32_t* refs, int32_t n_slots, const int32_t* slots, int32_t n,
                             void* stream);
 gdn_status gdn_cache_release(int32_t* refs, int32_t n_slots, const int32_t* slots, int32_t n,

@@ -115,6 +115,9 @@ def test_counts():
     assert many.tolist() == [100001]
     L.gdn_cache_retain(many, ints([]))
     assert many.tolist() == [100001]
+    full = ints([2**31 - 2])
+    L.gdn_cache_retain(full, ints([0] * 70))
+    assert full.tolist() == [2**31 - 1]
 
 
 @pytest.mark.parametrize("words", [4, 12, 1020, 4096, 4100, 50000])

@@ -212,6 +212,18 @@ def test_state_cache_layout():
             GDNStateCache(cfg, n, k, "cpu")
 
 
+def test_prefill_wants_a_slot_for_every_sequence():
+    core = GDNCore(CoreConfig(1, 2, 32, torch.bfloat16), "cpu")
+    c = GDNStateCache(core.cfg, 4, device="cpu")
+    bf = torch.bfloat16
+    x, h, z = torch.zeros(3, 128, dtype=bf), torch.zeros(3, 2, dtype=bf), torch.zeros(3, 2, 32, dtype=bf)
+    cu = torch.tensor([0, 1, 3], dtype=torch.int32)
+    two, one = torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    for si, so in ((one, two), (two, one), (one, None)):
+        with pytest.raises(ValueError, match="2 sequences"):
+            core.prefill(x, torch.zeros(128, 4), h, h, torch.zeros(2), torch.zeros(2), z, torch.zeros(32), cu, c, si, so)
+
+
 def test_core_step_refuses_host_tensors():
     core = GDNCore(CoreConfig(1, 2, 32, torch.bfloat16), "cpu")
     c = GDNStateCache(core.cfg, 2, device="cpu")
