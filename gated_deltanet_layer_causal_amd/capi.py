@@ -561,21 +561,12 @@ def make_cache(S, conv=None) -> Cache:
 
 
 # Serving calls are as short as a few microseconds, so their wrappers ask first
-# whether every tensor is as it should be, as cheaply as Python can (dtype,
-# shape, layout and device index), and look for what is wrong only if one is
-# not.
-def _is_rows(t, dtype, shape, index):
-    return (t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0 and
-            (t.stride(1) == 1 or shape[0] == 0 or shape[1] == 1))
-
-
+# whether every tensor is as it should be, as cheaply as Python can (one
+# expression over dtype, shape, layout and device index), and go through the
+# checks that say what is wrong only if one is not.
 def _is_flat(t, dtype, numel, index):
     return (t.dtype is dtype and t.numel() == numel and t.get_device() == index >= 0 and
             t.is_contiguous())
-
-
-def _is_table(t, numel, index):
-    return t is None or _is_flat(t, torch.int32, numel, index)
 
 
 def _slot_call(name, dev, index, stream, fn, *args):
@@ -635,24 +626,40 @@ def gdn_recurrent_fwd(shape, q, k, v, g, beta, scale, cache, slot_in, slot_out, 
     int32 device tables, each may be None; see libgdn.h."""
     i, dt, T, N, hv, d = (cache.index, _TDT[shape.dtype], shape.total_tokens, shape.n_seq, shape.hv,
                           shape.dv)
-    qk, f32 = (T, shape.hk * d), torch.float32
-    if not (cache.heads == (hv, d) and _is_rows(q, dt, qk, i) and _is_rows(k, dt, qk, i) and
-            _is_rows(v, dt, (T, hv * d), i) and _is_flat(g, f32, T * hv, i) and
-            _is_flat(beta, f32, T * hv, i) and _is_flat(o, dt, T * hv * d, i) and
-            _is_flat(cu_seqlens, torch.int32, N + 1, i) and _is_table(slot_in, N, i) and
-            _is_table(slot_out, N, i) and _is_table(slot_tok, T, i)):
-        _cache_ok(shape, cache)
-        _chunk_qk(shape, q, k)
-        _rows("v", v, dt, T, hv * d)
-        _per_token("g", shape, g)
-        _per_token("beta", shape, beta)
-        _heads("o", shape, o)
-        _slot_tables(shape, cache.device, cu_seqlens, slot_in, slot_out, slot_tok)
-        _on(cache.device, ("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("o", o))
+    f32, i32, n = torch.float32, torch.int32, T * hv
+    try:
+        qs, ks, vs = q.stride(), k.stride(), v.stride()
+        good = (T > 0 and i >= 0 and cache.heads == (hv, d) and
+                q.dtype is dt and q.shape == (T, shape.hk * d) and qs[1] == 1 and q.get_device() == i and
+                k.dtype is dt and k.shape == q.shape and ks[1] == 1 and k.get_device() == i and
+                v.dtype is dt and v.shape == (T, hv * d) and vs[1] == 1 and v.get_device() == i and
+                g.dtype is f32 and g.numel() == n and g.is_contiguous() and g.get_device() == i and
+                beta.dtype is f32 and beta.numel() == n and beta.is_contiguous() and
+                beta.get_device() == i and
+                o.dtype is dt and o.numel() == n * d and o.is_contiguous() and o.get_device() == i and
+                _is_flat(cu_seqlens, i32, N + 1, i) and
+                (slot_in is None or _is_flat(slot_in, i32, N, i)) and
+                (slot_out is None or _is_flat(slot_out, i32, N, i)) and
+                (slot_tok is None or _is_flat(slot_tok, i32, T, i)))
+    except (AttributeError, IndexError):
+        good = False
+    if good and T > 1:
+        ldq, ldk, ldv = qs[0], ks[0], vs[0]
+    else:
+        if not good:
+            _cache_ok(shape, cache)
+            _chunk_qk(shape, q, k)
+            _rows("v", v, dt, T, hv * d)
+            _per_token("g", shape, g)
+            _per_token("beta", shape, beta)
+            _heads("o", shape, o)
+            _slot_tables(shape, cache.device, cu_seqlens, slot_in, slot_out, slot_tok)
+            _on(cache.device, ("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("o", o))
+        ldq, ldk, ldv = _row_ld(q), _row_ld(k), _row_ld(v)
     _slot_call("gdn_recurrent_fwd", cache.device, i, stream, load().gdn_recurrent_fwd, byref(shape),
-               q.data_ptr(), k.data_ptr(), v.data_ptr(), _row_ld(q), _row_ld(k), _row_ld(v),
-               g.data_ptr(), beta.data_ptr(), scale, byref(cache), _ptr(slot_in), _ptr(slot_out),
-               _ptr(slot_tok), cu_seqlens.data_ptr(), o.data_ptr())
+               q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ldk, ldv, g.data_ptr(),
+               beta.data_ptr(), scale, byref(cache), _ptr(slot_in), _ptr(slot_out), _ptr(slot_tok),
+               cu_seqlens.data_ptr(), o.data_ptr())
 
 
 def gdn_step_fwd(shape, x, w_conv, a, b, A_log, dt_bias, z, w_norm, scale, cache, slot_in,
@@ -662,33 +669,56 @@ def gdn_step_fwd(shape, x, w_conv, a, b, A_log, dt_bias, z, w_norm, scale, cache
     make_cache(S, conv); slot tables as gdn_recurrent_fwd."""
     i, dt, T, N, hv, d = (cache.index, _TDT[shape.dtype], shape.total_tokens, shape.n_seq, shape.hv,
                           shape.dv)
-    C, f32 = 2 * shape.hk * d + hv * d, torch.float32
-    if not (cache.heads == (hv, d) and cache.conv_rows == (dt, C) and _is_rows(x, dt, (T, C), i) and
-            _is_flat(w_conv, f32, C * 4, i) and _is_rows(a, dt, (T, hv), i) and
-            _is_rows(b, dt, (T, hv), i) and _is_flat(A_log, f32, hv, i) and
-            _is_flat(dt_bias, f32, hv, i) and _is_rows(z, dt, (T, hv * d), i) and
-            _is_flat(w_norm, f32, d, i) and _is_flat(out, dt, T * hv * d, i) and
-            _is_flat(cu_seqlens, torch.int32, N + 1, i) and _is_table(slot_in, N, i) and
-            _is_table(slot_out, N, i) and _is_table(slot_tok, T, i)):
-        _cache_ok(shape, cache)
-        _conv_ok(shape, x, w_conv, cu_seqlens)
-        if cache.conv_rows != (dt, C):
-            raise ValueError(f"the cache needs conv rows [n_slots, 3, {C}] of {dt}")
-        _rows("a", a, dt, T, hv)
-        _rows("b", b, dt, T, hv)
-        _need("A_log", A_log, f32, hv)
-        _need("dt_bias", dt_bias, f32, hv)
-        _rows("z", z, dt, T, hv * d)
-        _need("w_norm", w_norm, f32, d)
-        _heads("out", shape, out)
-        _slot_tables(shape, cache.device, cu_seqlens, slot_in, slot_out, slot_tok)
-        _on(cache.device, ("x", x), ("w_conv", w_conv), ("a", a), ("b", b), ("A_log", A_log),
-            ("dt_bias", dt_bias), ("z", z), ("w_norm", w_norm), ("out", out))
+    C, f32, i32 = 2 * shape.hk * d + hv * d, torch.float32, torch.int32
+    try:
+        xs, as_, bs, zs = x.stride(), a.stride(), b.stride(), z.stride()
+        good = (T > 0 and i >= 0 and cache.heads == (hv, d) and cache.conv_rows == (dt, C) and
+                x.dtype is dt and x.shape == (T, C) and xs[1] == 1 and x.get_device() == i and
+                a.dtype is dt and a.shape == (T, hv) and (as_[1] == 1 or hv == 1) and
+                a.get_device() == i and
+                b.dtype is dt and b.shape == (T, hv) and (bs[1] == 1 or hv == 1) and
+                b.get_device() == i and
+                z.dtype is dt and z.shape == (T, hv * d) and zs[1] == 1 and z.get_device() == i and
+                w_conv.dtype is f32 and w_conv.numel() == C * 4 and w_conv.is_contiguous() and
+                w_conv.get_device() == i and
+                A_log.dtype is f32 and A_log.numel() == hv and A_log.is_contiguous() and
+                A_log.get_device() == i and
+                dt_bias.dtype is f32 and dt_bias.numel() == hv and dt_bias.is_contiguous() and
+                dt_bias.get_device() == i and
+                w_norm.dtype is f32 and w_norm.numel() == d and w_norm.is_contiguous() and
+                w_norm.get_device() == i and
+                out.dtype is dt and out.numel() == T * hv * d and out.is_contiguous() and
+                out.get_device() == i and
+                _is_flat(cu_seqlens, i32, N + 1, i) and
+                (slot_in is None or _is_flat(slot_in, i32, N, i)) and
+                (slot_out is None or slot_out is slot_in or _is_flat(slot_out, i32, N, i)) and
+                (slot_tok is None or _is_flat(slot_tok, i32, T, i)))
+    except (AttributeError, IndexError):
+        good = False
+    if good and T > 1:
+        ldx, lda, ldb, ldz = xs[0], as_[0], bs[0], zs[0]
+    else:
+        if not good:
+            _cache_ok(shape, cache)
+            _conv_ok(shape, x, w_conv, cu_seqlens)
+            if cache.conv_rows != (dt, C):
+                raise ValueError(f"the cache needs conv rows [n_slots, 3, {C}] of {dt}")
+            _rows("a", a, dt, T, hv)
+            _rows("b", b, dt, T, hv)
+            _need("A_log", A_log, f32, hv)
+            _need("dt_bias", dt_bias, f32, hv)
+            _rows("z", z, dt, T, hv * d)
+            _need("w_norm", w_norm, f32, d)
+            _heads("out", shape, out)
+            _slot_tables(shape, cache.device, cu_seqlens, slot_in, slot_out, slot_tok)
+            _on(cache.device, ("x", x), ("w_conv", w_conv), ("a", a), ("b", b), ("A_log", A_log),
+                ("dt_bias", dt_bias), ("z", z), ("w_norm", w_norm), ("out", out))
+        ldx, lda, ldb, ldz = _row_ld(x), _row_ld(a), _row_ld(b), _row_ld(z)
     _slot_call("gdn_step_fwd", cache.device, i, stream, load().gdn_step_fwd, byref(shape),
-               x.data_ptr(), _row_ld(x), w_conv.data_ptr(), a.data_ptr(), _row_ld(a), b.data_ptr(),
-               _row_ld(b), A_log.data_ptr(), dt_bias.data_ptr(), z.data_ptr(), _row_ld(z),
-               w_norm.data_ptr(), scale, l2_eps, norm_eps, act, byref(cache), _ptr(slot_in),
-               _ptr(slot_out), _ptr(slot_tok), cu_seqlens.data_ptr(), out.data_ptr())
+               x.data_ptr(), ldx, w_conv.data_ptr(), a.data_ptr(), lda, b.data_ptr(), ldb,
+               A_log.data_ptr(), dt_bias.data_ptr(), z.data_ptr(), ldz, w_norm.data_ptr(), scale,
+               l2_eps, norm_eps, act, byref(cache), _ptr(slot_in), _ptr(slot_out), _ptr(slot_tok),
+               cu_seqlens.data_ptr(), out.data_ptr())
 
 
 SLOT_RANGE, SLOT_WRITTEN_TWICE, SLOT_WRITTEN_AND_READ = 1, 2, 4
@@ -749,31 +779,52 @@ def gdn_cache_workspace(n_slots):
     return int(load().gdn_cache_workspace(n_slots))
 
 
-def _cache_buf(buf, refs):
-    if buf.dim() != 2 or not buf.is_contiguous():
-        raise ValueError("the cache must be a contiguous [n_slots, slot] tensor")
-    n_slots, size = buf.shape
-    _indexes("refs", buf, refs, n_slots)
-    return n_slots, size * buf.element_size()
+class Slots:
+    """A cache's buffer [n_slots, slot], counts and workspace, checked once
+    and kept: what the calls below take instead of (buf, refs, ..., ws)."""
 
+    def __init__(self, buf, refs, ws):
+        if buf.dim() != 2 or not buf.is_contiguous():
+            raise ValueError("the cache must be a contiguous [n_slots, slot] tensor")
+        self.n_slots, self.size = buf.shape[0], buf.shape[1] * buf.element_size()
+        _indexes("refs", buf, refs, self.n_slots)
+        if ws is not None and not _is_flat(ws, torch.uint8, ws.numel(), buf.get_device()):
+            _ws(ws)
+            _on(buf.device, ("workspace", ws))
+        self.buf, self.refs, self.ws = buf, refs, ws
+        self.device, self.index = buf.device, buf.get_device()
+        self.ptrs = _ptr(buf), _ptr(refs), _ptr(ws), 0 if ws is None else ws.numel()
 
-def _cache_ws(buf, ws):
-    if ws is None:
-        return None, 0
-    if not _is_flat(ws, torch.uint8, ws.numel(), buf.get_device()):
-        _ws(ws)
-        _on(buf.device, ("workspace", ws))
-    return ws.data_ptr(), ws.numel()
+    def _table(self, name, t, n=None):
+        if t is None or not _is_flat(t, torch.int32, t.numel() if n is None else n, self.index):
+            _need(name, t, torch.int32, n)
+            _on(self.device, (name, t))
+        return t.numel()
+
+    def fork(self, src, dst, stream=None):
+        n = self._table("src", src)
+        self._table("dst", dst, n)
+        buf, refs, ws, ws_bytes = self.ptrs
+        _slot_call("gdn_cache_fork", self.device, self.index, stream, load().gdn_cache_fork, buf,
+                   self.size, self.n_slots, refs, src.data_ptr(), n, dst.data_ptr(), ws, ws_bytes)
+
+    def count(self, name, slots, stream=None):
+        n = self._table("slots", slots)
+        _slot_call(name, self.device, self.index, stream, getattr(load(), name), self.ptrs[1],
+                   self.n_slots, slots.data_ptr(), n)
+
+    def compact(self, remap, table, stream=None):
+        self._table("remap", remap, self.n_slots)
+        n = 0 if table is None else self._table("table", table)
+        buf, refs, ws, ws_bytes = self.ptrs
+        _slot_call("gdn_cache_compact", self.device, self.index, stream, load().gdn_cache_compact,
+                   buf, self.size, self.n_slots, refs, remap.data_ptr(), _ptr(table), n, ws, ws_bytes)
 
 
 def gdn_cache_fork(buf, refs, src, dst, ws, stream=None):
     """Takes a free slot of buf [n_slots, slot] for every request in src and
     fills it; the slots go to dst (int32, as long as src)."""
-    n_slots, size = _cache_buf(buf, refs)
-    n = _indexes("src", buf, src)
-    _indexes("dst", buf, dst, n)
-    _slot_call("gdn_cache_fork", buf.device, buf.get_device(), stream, load().gdn_cache_fork, _ptr(buf),
-               size, n_slots, _ptr(refs), _ptr(src), n, _ptr(dst), *_cache_ws(buf, ws))
+    Slots(buf, refs, ws).fork(src, dst, stream)
 
 
 def _count(name, refs, slots, stream):
@@ -794,8 +845,4 @@ def gdn_cache_release(refs, slots, stream=None):
 def gdn_cache_compact(buf, refs, remap, table, ws, stream=None):
     """Moves the live slots of buf to its front; remap [n_slots] receives
     where each went, and table (int32, or None) is rewritten by it."""
-    n_slots, size = _cache_buf(buf, refs)
-    _indexes("remap", buf, remap, n_slots)
-    n = 0 if table is None else _indexes("table", buf, table)
-    _slot_call("gdn_cache_compact", buf.device, buf.get_device(), stream, load().gdn_cache_compact,
-               _ptr(buf), size, n_slots, _ptr(refs), _ptr(remap), _ptr(table), n, *_cache_ws(buf, ws))
+    Slots(buf, refs, ws).compact(remap, table, stream)

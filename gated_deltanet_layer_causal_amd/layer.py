@@ -177,7 +177,8 @@ class GDNCore:
         if c.check_slots:
             self.check_slots(sh, cache, slot_in, slot_out, slot_tok, cu_seqlens)
         out = torch.empty((T, c.hv, c.d), dtype=c.dtype, device=x.device)
-        L.gdn_step_fwd(sh, x, w_conv, a, b, A_log, dt_bias, z.view(T, c.hv * c.d), w_norm, c.q_scale,
+        L.gdn_step_fwd(sh, x, w_conv, a, b, A_log, dt_bias,
+                       z if z.dim() == 2 else z.view(T, c.hv * c.d), w_norm, c.q_scale,
                        cache.layer(layer), slot_in, slot_out, slot_tok, cu_seqlens, out, c.l2_eps,
                        c.norm_eps, c.act)
         return out

@@ -44,15 +44,24 @@ class GDNStateCache:
         elif refs.dtype != torch.int32 or tuple(refs.shape) != (n_slots,) or \
                 refs.device != buffer.device or not refs.is_contiguous():
             raise ValueError(f"refs must be a contiguous int32 [{n_slots}] tensor on the buffer's device")
-        self.buffer, self.refs = buffer, refs
         self._layers = []
         for k in range(n_layers):
             at = k * layer
             S = buffer[:, at:at + s_bytes].view(torch.float32).view(n_slots, cfg.hv, cfg.d, cfg.d)
             conv = buffer[:, at + s_bytes:at + s_bytes + c_bytes].view(cfg.dtype).view(n_slots, 3, C)
             self._layers.append(L.make_cache(S, conv))
-        self._ws = torch.empty(L.gdn_cache_workspace(n_slots), dtype=torch.uint8,
-                               device=buffer.device)
+        self._slots = L.Slots(buffer, refs, torch.empty(L.gdn_cache_workspace(n_slots),
+                                                        dtype=torch.uint8, device=buffer.device))
+
+    @property
+    def buffer(self) -> torch.Tensor:
+        """All slots, uint8 [n_slots, slot_bytes]."""
+        return self._slots.buf
+
+    @property
+    def refs(self) -> torch.Tensor:
+        """The users of each slot, int32 [n_slots]."""
+        return self._slots.refs
 
     def layer(self, k: int = 0) -> L.Cache:
         """The C ABI's view of layer k."""
@@ -72,16 +81,16 @@ class GDNStateCache:
         the slots (int32); -1 where the request could not be served (no free
         slot left, or src[i] is no live slot) or src[i] < -1 (no request)."""
         dst = torch.empty_like(src)
-        L.gdn_cache_fork(self.buffer, self.refs, src, dst, self._ws)
+        self._slots.fork(src, dst)
         return dst
 
     def retain(self, slots: torch.Tensor) -> None:
         """One more user of each live slot named."""
-        L.gdn_cache_retain(self.refs, slots)
+        self._slots.count("gdn_cache_retain", slots)
 
     def release(self, slots: torch.Tensor) -> None:
         """One user less of each slot named; at 0 the slot is free."""
-        L.gdn_cache_release(self.refs, slots)
+        self._slots.count("gdn_cache_release", slots)
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor) -> None:
         """Slot dst[i] = slot src[i] (zeros where src[i] < 0), counts left alone."""
@@ -92,5 +101,5 @@ class GDNStateCache:
         slot's new place (int32 [n_slots], -1 for free ones) and rewrites
         `table` (int32, any length: the slots of the running sequences) by it."""
         remap = torch.empty_like(self.refs)
-        L.gdn_cache_compact(self.buffer, self.refs, remap, table, self._ws)
+        self._slots.compact(remap, table)
         return remap
