@@ -28,7 +28,7 @@ class GDNStateCache:
         [n_slots]): memory to use instead of new memory, taken as it is."""
         if n_slots < 1 or n_layers < 1:
             raise ValueError("a cache needs at least one slot and one layer")
-        C, E = cfg.channels, torch.empty(0, dtype=cfg.dtype).element_size()
+        C, E = cfg.channels, cfg.dtype.itemsize
         self.cfg, self.n_slots, self.n_layers = cfg, n_slots, n_layers
         s_bytes, c_bytes = cfg.hv * cfg.d * cfg.d * 4, 3 * C * E
         layer = (s_bytes + c_bytes + self.ALIGN - 1) // self.ALIGN * self.ALIGN
@@ -44,12 +44,9 @@ class GDNStateCache:
         elif refs.dtype != torch.int32 or tuple(refs.shape) != (n_slots,) or \
                 refs.device != buffer.device or not refs.is_contiguous():
             raise ValueError(f"refs must be a contiguous int32 [{n_slots}] tensor on the buffer's device")
-        self._layers = []
-        for k in range(n_layers):
-            at = k * layer
-            S = buffer[:, at:at + s_bytes].view(torch.float32).view(n_slots, cfg.hv, cfg.d, cfg.d)
-            conv = buffer[:, at + s_bytes:at + s_bytes + c_bytes].view(cfg.dtype).view(n_slots, 3, C)
-            self._layers.append(L.make_cache(S, conv))
+        self._layer_bytes, self._parts = layer, (s_bytes, c_bytes)
+        self._dims = cfg.hv, cfg.d, C, cfg.dtype
+        self._layers = [None] * n_layers     # views, made when first asked for
         self._slots = L.Slots(buffer, refs, torch.empty(L.gdn_cache_workspace(n_slots),
                                                         dtype=torch.uint8, device=buffer.device))
 
@@ -65,15 +62,23 @@ class GDNStateCache:
 
     def layer(self, k: int = 0) -> L.Cache:
         """The C ABI's view of layer k."""
-        return self._layers[k]
+        got = self._layers[k]
+        if got is None:
+            (hv, d, C, dtype), buf = self._dims, self.buffer
+            at = k % self.n_layers * self._layer_bytes
+            mid, end = at + self._parts[0], at + sum(self._parts)
+            S = buf[:, at:mid].view(torch.float32).view(self.n_slots, hv, d, d)
+            conv = buf[:, mid:end].view(dtype).view(self.n_slots, 3, C)
+            got = self._layers[k] = L.make_cache(S, conv)
+        return got
 
     def S(self, k: int = 0) -> torch.Tensor:
         """Layer k's states [n_slots, hv, d, d], a view."""
-        return self._layers[k].S
+        return self.layer(k).S
 
     def conv(self, k: int = 0) -> torch.Tensor:
         """Layer k's conv rows [n_slots, 3, C], a view."""
-        return self._layers[k].conv
+        return self.layer(k).conv
 
     def fork(self, src: torch.Tensor) -> torch.Tensor:
         """Takes a free slot for every request: filled with a copy of slot
