@@ -14,19 +14,19 @@ OK, INVALID, UNSUPPORTED, ALIGNMENT, WORKSPACE = 0, 1, 2, 3, 4
 
 
 def shape(**kw):
-    base = dict(n_seq=2, total_tokens=3, hk=2, hv=4, d=128, dtype=L.GDN_BF16)
+    base = dict(n_seq=2, total_tokens=3, hk=2, hv=6, d=128, dtype=L.GDN_BF16)
     base.update(kw)
     return L.make_shape(base["n_seq"], base["total_tokens"], base["hk"], base["hv"], base["d"], base["dtype"])
 
 
 def cache(**kw):
-    base = dict(S_ptr=256, S_stride=4 * 128 * 128, conv_ptr=256, conv_stride=3 * 1024, n_slots=5)
+    base = dict(S_ptr=256, S_stride=6 * 128 * 128, conv_ptr=256, conv_stride=3 * 1280, n_slots=5)
     base.update(kw)
     return L.Cache(*base.values())
 
 
 def rule(sh=None, c=None, **kw):
-    a = dict(q=P, k=P, v=P, ldq=256, ldk=256, ldv=512, g=P, beta=P, cu=P, o=P)
+    a = dict(q=P, k=P, v=P, ldq=256, ldk=256, ldv=768, g=P, beta=P, cu=P, o=P)
     a.update(kw)
     sh = shape() if sh is None else sh
     return L.load().gdn_recurrent_fwd(
@@ -35,7 +35,7 @@ def rule(sh=None, c=None, **kw):
 
 
 def step(sh=None, c=None, **kw):
-    a = dict(x=P, ldx=1024, w=P, a=P, lda=4, b=P, ldb=4, A=P, dt=P, z=P, ldz=512, wn=P, l2=1e-6, ne=1e-6,
+    a = dict(x=P, ldx=1280, w=P, a=P, lda=6, b=P, ldb=6, A=P, dt=P, z=P, ldz=768, wn=P, l2=1e-6, ne=1e-6,
              act=0, cu=P, out=P)
     a.update(kw)
     sh = shape() if sh is None else sh
@@ -49,10 +49,10 @@ def step(sh=None, c=None, **kw):
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(o=None), INVALID),
     (dict(g=None), INVALID), (dict(beta=None), INVALID), (dict(cu=None), INVALID),
     (dict(q=ODD), ALIGNMENT), (dict(o=ODD), ALIGNMENT), (dict(ldq=255), INVALID), (dict(ldk=260), ALIGNMENT),
-    (dict(ldv=504), INVALID), (dict(sh=shape(d=64)), UNSUPPORTED), (dict(sh=shape(hv=3)), INVALID),
+    (dict(ldv=760), INVALID), (dict(sh=shape(d=64)), UNSUPPORTED), (dict(sh=shape(hv=5)), INVALID),
     (dict(sh=shape(n_seq=0)), INVALID), (dict(sh=shape(total_tokens=-1)), INVALID),
     (dict(c=cache(S_ptr=None)), INVALID), (dict(c=cache(n_slots=0)), INVALID),
-    (dict(c=cache(S_stride=4 * 128 * 128 - 4)), INVALID), (dict(c=cache(S_stride=4 * 128 * 128 + 2)), ALIGNMENT),
+    (dict(c=cache(S_stride=6 * 128 * 128 - 4)), INVALID), (dict(c=cache(S_stride=6 * 128 * 128 + 2)), ALIGNMENT),
     (dict(c=cache(S_ptr=260)), ALIGNMENT)])
 def test_rule_refusals(kw, status):
     assert rule(**kw) == status
@@ -62,11 +62,11 @@ def test_rule_refusals(kw, status):
     (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(a=None), INVALID), (dict(b=None), INVALID),
     (dict(A=None), INVALID), (dict(dt=None), INVALID), (dict(z=None), INVALID), (dict(wn=None), INVALID),
     (dict(cu=None), INVALID), (dict(out=None), INVALID), (dict(x=ODD), ALIGNMENT), (dict(z=ODD), ALIGNMENT),
-    (dict(ldx=1016), INVALID), (dict(ldx=1028), ALIGNMENT), (dict(ldz=504), INVALID), (dict(ldz=516), ALIGNMENT),
-    (dict(lda=3), INVALID), (dict(ldb=3), INVALID), (dict(l2=-1.0), INVALID), (dict(ne=-1.0), INVALID),
+    (dict(ldx=1272), INVALID), (dict(ldx=1284), ALIGNMENT), (dict(ldz=760), INVALID), (dict(ldz=772), ALIGNMENT),
+    (dict(lda=5), INVALID), (dict(ldb=5), INVALID), (dict(l2=-1.0), INVALID), (dict(ne=-1.0), INVALID),
     (dict(ne=float("nan")), INVALID), (dict(act=2), INVALID), (dict(sh=shape(d=64)), UNSUPPORTED),
-    (dict(c=cache(conv_ptr=None)), INVALID), (dict(c=cache(conv_stride=3 * 1024 - 8)), INVALID),
-    (dict(c=cache(conv_ptr=264)), ALIGNMENT), (dict(c=cache(conv_stride=3 * 1024 + 4)), ALIGNMENT),
+    (dict(c=cache(conv_ptr=None)), INVALID), (dict(c=cache(conv_stride=3 * 1280 - 8)), INVALID),
+    (dict(c=cache(conv_ptr=264)), ALIGNMENT), (dict(c=cache(conv_stride=3 * 1280 + 4)), ALIGNMENT),
     (dict(c=cache(S_ptr=None)), INVALID)])
 def test_step_refusals(kw, status):
     assert step(**kw) == status
@@ -74,7 +74,7 @@ def test_step_refusals(kw, status):
 
 def test_null_cache_is_refused():
     lib, sh = L.load(), shape()
-    assert lib.gdn_recurrent_fwd(ctypes.byref(sh), P, P, P, 256, 256, 512, P, P, 0.1, None, None, None, None, P,
+    assert lib.gdn_recurrent_fwd(ctypes.byref(sh), P, P, P, 256, 256, 768, P, P, 0.1, None, None, None, None, P,
                                  P, None) == INVALID
 
 
