@@ -143,6 +143,7 @@ CASES = {
     "three_of_a_group_fp32_short": dict(dtype="fp32", hk=3, hv=9, d=128, lens=[1, 6, 0, 2]),
     # so many groups that their heads go one by one
     "many_bf16": dict(dtype="bf16", hk=2, hv=4, d=32, lens=[1] * 1000 + [2] * 40),
+    "most_heads_bf16": dict(dtype="bf16", hk=1, hv=256, d=32, lens=[1, 2]),
 }
 
 
@@ -388,6 +389,73 @@ def test_another_layer_of_the_slots():
     for k in (0, 2):
         n = c.cache.slot_bytes // 3
         assert torch.equal(c.cache.buffer[:, k * n:(k + 1) * n], before[:, k * n:(k + 1) * n])
+
+
+@pytest.mark.parametrize("hk,hv,lens", [(1, 6, [3, 1, 2]), (1, 5, [20, 13]), (2, 4, [1, 9])])
+def test_a_state_kept_in_the_slot_it_came_from(hk, hv, lens):
+    """A single token's state may go to the slot that the sequence began from
+    (its last goes elsewhere), heads together, in rounds and apart."""
+    N, T = len(lens), sum(lens)
+    c = Case("bf16", hk, hv, 128, lens, 2 * N, seed=8)
+    slot_in, slot_out, tok = list(range(N)), list(range(N, 2 * N)), [-1] * T
+    for n in range(N):
+        tok[int(c.cu[n])] = n                       # after its first token
+    got = c.step(slot_in, slot_out, tok)
+    c.check(got, c.ref(slot_in, slot_out, tok))
+
+
+def test_no_tables_at_all():
+    """Without tables every sequence is new and no state is kept."""
+    c = Case("bf16", 2, 4, 128, [2, 1, 5], 2)
+    before = c.cache.buffer.clone()
+    got = c.core.step(*c.args(), c.cache, None)
+    c.check(got, c.ref([-1] * 3, [-1] * 3))
+    q, k, v = (torch.randn(8, n, device=DEV).bfloat16() for n in (256, 256, 512))
+    g, beta = -torch.rand(8, 4, device=DEV), torch.rand(8, 4, device=DEV)
+    a = c.core.recurrent(q, k, v, g, beta, ints(c.cu), c.cache, None)
+    b = c.core.recurrent(q, k, v, g, beta, ints(c.cu), c.cache, ints([-1] * 3), ints([-1] * 3), ints([-1] * 8))
+    assert torch.equal(a, b) and torch.equal(c.cache.buffer, before)
+
+
+def test_lengths_outside_the_tokens_are_clamped():
+    c = Case("bf16", 1, 3, 128, [2, 2, 0, 0], 4)
+    x, w, a, b, A, dt, z, wn, _ = c.args()
+    slots = ints([3, 1, 0, 2])
+    got = c.core.step(x, w, a, b, A, dt, z, wn, ints([-9, 2, 1 << 30, 1, -(1 << 31)]), c.cache, slots)
+    c.check(got, c.ref([3, 1, 0, 2]))
+
+
+def test_as_many_sequences_as_a_call_takes():
+    """65535 sequences of one token, against the formula in elementary torch."""
+    N, d = 65535, 32
+    torch.manual_seed(3)
+    core = GDNCore(CoreConfig(1, 1, d, torch.float32, scale=1.0), DEV)
+    cache = GDNStateCache(core.cfg, N, device=DEV)
+    cache.S().normal_()
+    q, k, v = (torch.randn(N, d, device=DEV) for _ in range(3))
+    k /= k.norm(dim=1, keepdim=True)
+    g, beta = -torch.rand(N, 1, device=DEV), torch.rand(N, 1, device=DEV)
+    S = cache.S()[:, 0].double() * torch.exp(g.double())[..., None]
+    delta = beta.double() * (v.double() - (S * k.double()[:, None]).sum(2))
+    S = S + delta[..., None] * k.double()[:, None]
+    want = (S * q.double()[:, None]).sum(2)
+    slots = torch.arange(N, dtype=torch.int32, device=DEV)
+    o = core.recurrent(q, k, v, g, beta, torch.arange(N + 1, dtype=torch.int32, device=DEV), cache, slots)
+    assert_close("o", host(o[:, 0]), host(want), FP32)
+    assert_close("S", host(cache.S()[:, 0]), host(S), FP32)
+
+
+def test_on_a_given_stream():
+    c = Case("bf16", 2, 4, 128, [1, 3], 2)
+    want = c.ref([1, 0])
+    x, w, a, b, A, dt, z, wn, cu = c.args()
+    out, slots = torch.empty(4, 4, 128, dtype=torch.bfloat16, device=DEV), ints([1, 0])
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    L.gdn_step_fwd(c.core.shape(4, 2), x, w, a, b, A, dt, z.view(4, -1), wn, 128 ** -0.5, c.cache.layer(), slots,
+                   slots, None, cu, out, stream=st)
+    st.synchronize()
+    c.check(out, want)
 
 
 def test_on_another_stream():
