@@ -569,22 +569,30 @@ def _is_flat(t, dtype, numel, index):
             t.is_contiguous())
 
 
-def _slot_call(name, dev, index, stream, fn, *args):
-    """Runs a serving entry point on device `index` (`dev`; it need not be the
-    current one) and the given stream, or the device's current one."""
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(dev, index, stream):
+    """The hipStream_t of `stream`, or of device `index`'s current one."""
     if index < 0:
         raise ValueError("libgdn takes device tensors only; got a host tensor")
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)
-    elif stream.device != dev:
+        return _get_stream(index)
+    if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return stream.cuda_stream
+
+
+def _run(name, index, args):
+    """Runs a serving entry point on device `index`, which need not be the
+    current one."""
+    fn = getattr(_lib or load(), name)
+    if index == _get_device():
+        st = fn(*args)
     else:
-        raw = stream.cuda_stream
-    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
-            st = fn(*args, raw)
-    else:
-        st = fn(*args, raw)
+            st = fn(*args)
     if st != 0:
         _ok(name, st)
 
@@ -656,17 +664,17 @@ def gdn_recurrent_fwd(shape, q, k, v, g, beta, scale, cache, slot_in, slot_out, 
             _slot_tables(shape, cache.device, cu_seqlens, slot_in, slot_out, slot_tok)
             _on(cache.device, ("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("o", o))
         ldq, ldk, ldv = _row_ld(q), _row_ld(k), _row_ld(v)
-    _slot_call("gdn_recurrent_fwd", cache.device, i, stream, load().gdn_recurrent_fwd, byref(shape),
-               q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ldk, ldv, g.data_ptr(),
-               beta.data_ptr(), scale, byref(cache), _ptr(slot_in), _ptr(slot_out), _ptr(slot_tok),
-               cu_seqlens.data_ptr(), o.data_ptr())
+    _run("gdn_recurrent_fwd", i, (
+        byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ldk, ldv, g.data_ptr(),
+        beta.data_ptr(), scale, byref(cache), _ptr(slot_in), _ptr(slot_out), _ptr(slot_tok),
+        cu_seqlens.data_ptr(), o.data_ptr(), _raw_stream(cache.device, i, stream)))
 
 
 def gdn_step_fwd(shape, x, w_conv, a, b, A_log, dt_bias, z, w_norm, scale, cache, slot_in,
                  slot_out, slot_tok, cu_seqlens, out, l2_eps=1e-6, norm_eps=1e-6,
                  act=GDN_ACT_SILU, stream=None):
-    """x [T, C], a, b [T, hv] and z [T, hv*d]: rows may be strided.  cache:
-    make_cache(S, conv); slot tables as gdn_recurrent_fwd."""
+    """x [T, C], a, b [T, hv] and z [T, hv*d] or [T, hv, d]: rows may be
+    strided.  cache: make_cache(S, conv); slot tables as gdn_recurrent_fwd."""
     i, dt, T, N, hv, d = (cache.index, _TDT[shape.dtype], shape.total_tokens, shape.n_seq, shape.hv,
                           shape.dv)
     C, f32, i32 = 2 * shape.hk * d + hv * d, torch.float32, torch.int32
@@ -678,7 +686,9 @@ def gdn_step_fwd(shape, x, w_conv, a, b, A_log, dt_bias, z, w_norm, scale, cache
                 a.get_device() == i and
                 b.dtype is dt and b.shape == (T, hv) and (bs[1] == 1 or hv == 1) and
                 b.get_device() == i and
-                z.dtype is dt and z.shape == (T, hv * d) and zs[1] == 1 and z.get_device() == i and
+                z.dtype is dt and z.get_device() == i and
+                (z.shape == (T, hv, d) and zs[2] == 1 and zs[1] == d or
+                 z.shape == (T, hv * d) and zs[1] == 1) and
                 w_conv.dtype is f32 and w_conv.numel() == C * 4 and w_conv.is_contiguous() and
                 w_conv.get_device() == i and
                 A_log.dtype is f32 and A_log.numel() == hv and A_log.is_contiguous() and
@@ -699,6 +709,8 @@ def gdn_step_fwd(shape, x, w_conv, a, b, A_log, dt_bias, z, w_norm, scale, cache
         ldx, lda, ldb, ldz = xs[0], as_[0], bs[0], zs[0]
     else:
         if not good:
+            if z is not None and z.dim() == 3:
+                z = z.view(z.shape[0], z.shape[1] * z.shape[2])
             _cache_ok(shape, cache)
             _conv_ok(shape, x, w_conv, cu_seqlens)
             if cache.conv_rows != (dt, C):
@@ -713,12 +725,12 @@ def gdn_step_fwd(shape, x, w_conv, a, b, A_log, dt_bias, z, w_norm, scale, cache
             _slot_tables(shape, cache.device, cu_seqlens, slot_in, slot_out, slot_tok)
             _on(cache.device, ("x", x), ("w_conv", w_conv), ("a", a), ("b", b), ("A_log", A_log),
                 ("dt_bias", dt_bias), ("z", z), ("w_norm", w_norm), ("out", out))
-        ldx, lda, ldb, ldz = _row_ld(x), _row_ld(a), _row_ld(b), _row_ld(z)
-    _slot_call("gdn_step_fwd", cache.device, i, stream, load().gdn_step_fwd, byref(shape),
-               x.data_ptr(), ldx, w_conv.data_ptr(), a.data_ptr(), lda, b.data_ptr(), ldb,
-               A_log.data_ptr(), dt_bias.data_ptr(), z.data_ptr(), ldz, w_norm.data_ptr(), scale,
-               l2_eps, norm_eps, act, byref(cache), _ptr(slot_in), _ptr(slot_out), _ptr(slot_tok),
-               cu_seqlens.data_ptr(), out.data_ptr())
+        ldx, lda, ldb, ldz = C if good else _row_ld(x), _row_ld(a), _row_ld(b), hv * d if good else _row_ld(z)
+    _run("gdn_step_fwd", i, (
+        byref(shape), x.data_ptr(), ldx, w_conv.data_ptr(), a.data_ptr(), lda, b.data_ptr(), ldb,
+        A_log.data_ptr(), dt_bias.data_ptr(), z.data_ptr(), ldz, w_norm.data_ptr(), scale, l2_eps,
+        norm_eps, act, byref(cache), _ptr(slot_in), _ptr(slot_out), _ptr(slot_tok),
+        cu_seqlens.data_ptr(), out.data_ptr(), _raw_stream(cache.device, i, stream)))
 
 
 SLOT_RANGE, SLOT_WRITTEN_TWICE, SLOT_WRITTEN_AND_READ = 1, 2, 4
@@ -732,8 +744,10 @@ def gdn_check_slots(shape, n_slots, slot_in, slot_out, slot_tok, cu_seqlens, vio
     _slot_tables(shape, dev, cu_seqlens, slot_in, slot_out, slot_tok)
     _need("violations", violations, torch.int32, 1)
     _on(dev, ("violations", violations))
-    _slot_call("gdn_check_slots", dev, cu_seqlens.get_device(), stream, load().gdn_check_slots, byref(shape), n_slots,
-               _ptr(slot_in), _ptr(slot_out), _ptr(slot_tok), _ptr(cu_seqlens), _ptr(violations))
+    i = cu_seqlens.get_device()
+    _run("gdn_check_slots", i, (
+        byref(shape), n_slots, _ptr(slot_in), _ptr(slot_out), _ptr(slot_tok), _ptr(cu_seqlens),
+        _ptr(violations), _raw_stream(dev, i, stream)))
 
 
 def _slot_rows(name, t):
@@ -771,8 +785,10 @@ def gdn_cache_copy(src, dst, src_idx=None, dst_idx=None, stream=None):
             raise ValueError(f"{n} slots out of {n_src}")
     if src_idx is None and dst_idx is None and n_src != n_dst:
         raise ValueError(f"{n_src} slots into {n_dst} without indexes")
-    _slot_call("gdn_cache_copy", src.device, src.get_device(), stream, load().gdn_cache_copy, _ptr(src), ss, n_src,
-               _ptr(src_idx), _ptr(dst), ds, n_dst, _ptr(dst_idx), size, n)
+    i = src.get_device()
+    _run("gdn_cache_copy", i, (
+        _ptr(src), ss, n_src, _ptr(src_idx), _ptr(dst), ds, n_dst, _ptr(dst_idx), size, n,
+        _raw_stream(src.device, i, stream)))
 
 
 def gdn_cache_workspace(n_slots):
@@ -805,20 +821,22 @@ class Slots:
         n = self._table("src", src)
         self._table("dst", dst, n)
         buf, refs, ws, ws_bytes = self.ptrs
-        _slot_call("gdn_cache_fork", self.device, self.index, stream, load().gdn_cache_fork, buf,
-                   self.size, self.n_slots, refs, src.data_ptr(), n, dst.data_ptr(), ws, ws_bytes)
+        _run("gdn_cache_fork", self.index, (
+            buf, self.size, self.n_slots, refs, src.data_ptr(), n, dst.data_ptr(), ws, ws_bytes,
+            _raw_stream(self.device, self.index, stream)))
 
     def count(self, name, slots, stream=None):
         n = self._table("slots", slots)
-        _slot_call(name, self.device, self.index, stream, getattr(load(), name), self.ptrs[1],
-                   self.n_slots, slots.data_ptr(), n)
+        _run(name, self.index, (self.ptrs[1], self.n_slots, slots.data_ptr(), n,
+                                _raw_stream(self.device, self.index, stream)))
 
     def compact(self, remap, table, stream=None):
         self._table("remap", remap, self.n_slots)
         n = 0 if table is None else self._table("table", table)
         buf, refs, ws, ws_bytes = self.ptrs
-        _slot_call("gdn_cache_compact", self.device, self.index, stream, load().gdn_cache_compact,
-                   buf, self.size, self.n_slots, refs, remap.data_ptr(), _ptr(table), n, ws, ws_bytes)
+        _run("gdn_cache_compact", self.index, (
+            buf, self.size, self.n_slots, refs, remap.data_ptr(), _ptr(table), n, ws, ws_bytes,
+            _raw_stream(self.device, self.index, stream)))
 
 
 def gdn_cache_fork(buf, refs, src, dst, ws, stream=None):
@@ -830,8 +848,8 @@ def gdn_cache_fork(buf, refs, src, dst, ws, stream=None):
 def _count(name, refs, slots, stream):
     n_slots = _indexes("refs", refs, refs)
     n = _indexes("slots", refs, slots)
-    _slot_call(name, refs.device, refs.get_device(), stream, getattr(load(), name), _ptr(refs), n_slots,
-               _ptr(slots), n)
+    i = refs.get_device()
+    _run(name, i, (_ptr(refs), n_slots, _ptr(slots), n, _raw_stream(refs.device, i, stream)))
 
 
 def gdn_cache_retain(refs, slots, stream=None):

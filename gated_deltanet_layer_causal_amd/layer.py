@@ -176,9 +176,8 @@ class GDNCore:
         slot_out = slot_in if slot_out is None else slot_out
         if c.check_slots:
             self.check_slots(sh, cache, slot_in, slot_out, slot_tok, cu_seqlens)
-        out = torch.empty((T, c.hv, c.d), dtype=c.dtype, device=x.device)
-        L.gdn_step_fwd(sh, x, w_conv, a, b, A_log, dt_bias,
-                       z if z.dim() == 2 else z.view(T, c.hv * c.d), w_norm, c.q_scale,
+        out = x.new_empty((T, c.hv, c.d))
+        L.gdn_step_fwd(sh, x, w_conv, a, b, A_log, dt_bias, z, w_norm, c.q_scale,
                        cache.layer(layer), slot_in, slot_out, slot_tok, cu_seqlens, out, c.l2_eps,
                        c.norm_eps, c.act)
         return out
@@ -194,7 +193,7 @@ class GDNCore:
         slot_out = slot_in if slot_out is None else slot_out
         if c.check_slots:
             self.check_slots(sh, cache, slot_in, slot_out, slot_tok, cu_seqlens)
-        o = torch.empty((T, c.hv, c.d), dtype=c.dtype, device=q.device)
+        o = q.new_empty((T, c.hv, c.d))
         L.gdn_recurrent_fwd(sh, q, k, v, g, beta, c.q_scale, cache.layer(layer), slot_in, slot_out,
                             slot_tok, cu_seqlens, o)
         return o
