@@ -404,6 +404,49 @@ def test_a_state_kept_in_the_slot_it_came_from(hk, hv, lens):
     c.check(got, c.ref(slot_in, slot_out, tok))
 
 
+@pytest.mark.parametrize("dtype,hk,hv,d,lens", [("bf16", 2, 6, 128, [1, 3, 9, 0]), ("fp32", 1, 4, 32, [5, 1, 1, 2]),
+                                                ("fp16", 1, 5, 128, [17, 20, 1, 0])])
+def test_nothing_is_written_outside(dtype, hk, hv, d, lens):
+    """Bands of a known pattern around the cache, its workspace, the outputs
+    and the tables stay as they were, through every serving call."""
+    tdt, N, T = torch_dtype(dtype), len(lens), sum(lens)
+    bands = []
+
+    def banded(n, kind=torch.uint8):
+        n *= torch.empty(0, dtype=kind).element_size()
+        whole = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device=DEV)
+        bands.append(whole)
+        return whole[4096:4096 + n].view(kind)
+
+    c = Case(dtype, hk, hv, d, lens, 6)
+    size, cfg = c.cache.slot_bytes, c.core.cfg
+    refs = banded(6, torch.int32)
+    refs.copy_(ints([1, 1, 2, 1, 0, 0]))
+    cache = GDNStateCache(cfg, 6, device=DEV, buffer=banded(6 * size).view(6, size), refs=refs)
+    cache.buffer.copy_(c.cache.buffer)
+    x, w, a, b, A, dt, z, wn, cu = c.args()
+    out = banded(T * hv * d, tdt)
+    slots, tok, table, dst, remap = (banded(n, torch.int32) for n in (N, T, 9, 3, 6))
+    slots.copy_(ints([0, 1, 2, 3]))
+    tok.copy_(ints([4, 5] + [-1] * (T - 2)))
+    sh = c.core.shape(T, N)
+    L.gdn_step_fwd(sh, x, w, a, b, A, dt, z, wn, 1.0, cache.layer(), slots, slots, tok, cu, out)
+    q, k, v = c.core.split(x)
+    g, beta = -torch.rand(T, hv, device=DEV), torch.rand(T, hv, device=DEV)
+    L.gdn_recurrent_fwd(sh, q, k, v, g, beta, 1.0, cache.layer(), slots, slots, tok, cu, out)
+    ws = banded(L.gdn_cache_workspace(6))
+    L.gdn_cache_fork(cache.buffer, refs, ints([2, -1, 0]), dst, ws)
+    assert dst.tolist() == [4, 5, -1]
+    cache.release(ints([0, 2, 5]))
+    table.copy_(ints([0, 1, 2, 3, 4, 5, -1, 6, 3]))
+    L.gdn_cache_compact(cache.buffer, refs, remap, table, ws)
+    assert remap.tolist() == [-1, 1, 2, 3, 0, -1] and table.tolist() == [-1, 1, 2, 3, 0, -1, -1, 6, 3]
+    cache.copy(ints([3, -1]), ints([4, 5]))
+    torch.cuda.synchronize()
+    for i, whole in enumerate(bands):
+        assert bool((whole[:4096] == 0xA5).all()) and bool((whole[-4096:] == 0xA5).all()), i
+
+
 def test_no_tables_at_all():
     """Without tables every sequence is new and no state is kept."""
     c = Case("bf16", 2, 4, 128, [2, 1, 5], 2)
