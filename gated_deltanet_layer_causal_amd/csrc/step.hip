@@ -44,18 +44,15 @@ __device__ __forceinline__ float softplus_full(float x) {
   return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
 }
 
-// Sum over aligned groups of N lanes (2 for D = 32, 8 for D = 128).
-template <int N> __device__ __forceinline__ float lanes_sum(float x) {
-  if constexpr (N == 2) return x + dpp_f<0xB1>(x);
-  else return lane_group_sum<N>(x);
-}
-
 // Thread layout of the state: LPR lanes share a row of D columns; a lane
-// holds the columns 4 l + 4 LPR c + (0..3), c = 0..3, of R rows.  SPLIT
+// holds the columns 4 l + 4 LPR c + (0..3), c = 0 .. NC - 1, of R rows, so
+// that the lanes of a row touch whole 128-byte lines at a time (with two
+// lanes a row at D = 32, 32 bytes of each line, the rule took 125 us instead
+// of 32 us for 254 sequences x 48 heads with every state kept twice).  SPLIT
 // workgroups share a head, VC value rows each.
 template <int D, int HW, int SPLIT> struct StepGeo {
-  static constexpr int LPR = D / 16;
-  static constexpr int R = D == 128 ? 4 / SPLIT : 1;
+  static constexpr int LPR = 8, NC = D / (4 * LPR);
+  static constexpr int R = 4 / SPLIT;
   static constexpr int RPW = 64 / LPR;              // rows per wave and row slot
   static constexpr int VC = D / SPLIT;
   static constexpr int WAVES = VC / (RPW * R);      // state waves of a head
@@ -85,7 +82,7 @@ struct StepSpan {
 // A head's state: its load, its tokens, its store.
 template <int D, int SPLIT> struct StepState {
   typedef StepGeo<D, 1, SPLIT> G;
-  floatx4 S[G::R][4];
+  floatx4 S[G::R][G::NC];
   uint32_t row0, col0, at;   // first row of the workgroup's, first column, and their byte in S
 
   __device__ __forceinline__ StepState(int wave, int lane, int v0)
@@ -107,14 +104,14 @@ template <int D, int SPLIT> struct StepState {
 #pragma unroll
       for (int j = 0; j < G::R; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < G::NC; ++c)
           S[j][c] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(
               rs, at + 16 * G::LPR * c, 4 * j * G::RPW * D, CACHE_NT));
     } else {
 #pragma unroll
       for (int j = 0; j < G::R; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) S[j][c] = zero4();
+        for (int c = 0; c < G::NC; ++c) S[j][c] = zero4();
     }
   }
   template <int AUX>
@@ -122,7 +119,7 @@ template <int D, int SPLIT> struct StepState {
 #pragma unroll
     for (int j = 0; j < G::R; ++j)
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < G::NC; ++c)
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[j][c]), rs, at + 16 * G::LPR * c,
                                                4 * j * G::RPW * D, AUX);
   }
@@ -143,7 +140,7 @@ template <int D, int SPLIT> struct StepState {
       v[j] = sv[row0 + j * G::RPW];
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < G::NC; ++c) {
       const floatx4 k = *reinterpret_cast<const floatx4*>(sk + col0 + 4 * G::LPR * c);
       const floatx4 q = *reinterpret_cast<const floatx4*>(sq + col0 + 4 * G::LPR * c);
 #pragma unroll
@@ -156,11 +153,11 @@ template <int D, int SPLIT> struct StepState {
         }
       }
     }
-    kq = lanes_sum<G::LPR>(kq);
+    kq = lane_group_sum<G::LPR>(kq);
 #pragma unroll
     for (int j = 0; j < G::R; ++j) {
-      s[j] = lanes_sum<G::LPR>(s[j]);
-      r[j] = lanes_sum<G::LPR>(r[j]);
+      s[j] = lane_group_sum<G::LPR>(s[j]);
+      r[j] = lane_group_sum<G::LPR>(r[j]);
     }
 #pragma unroll
     for (int j = 0; j < G::R; ++j) {
@@ -172,7 +169,7 @@ template <int D, int SPLIT> struct StepState {
       for (int j = 0; j < G::R; ++j) sv[row0 + j * G::RPW] = r[j];
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < G::NC; ++c) {
       const floatx4 k = *reinterpret_cast<const floatx4*>(sk + col0 + 4 * G::LPR * c);
 #pragma unroll
       for (int j = 0; j < G::R; ++j)
