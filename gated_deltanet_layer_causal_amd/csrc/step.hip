@@ -226,7 +226,8 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
   constexpr int NV = StepLds<D, HW, SPLIT>::NV;
   constexpr int NL = 64 * G::HELPERS, NP = (HW * STEP_TB * V8 + NL - 1) / NL;
   // the step: rows of x on their way while the norm runs, as many as registers allow
-  constexpr int AHEAD = (sizeof(T) == 2 ? 4 : 2) / (HW == 3 || (HW == 2 && sizeof(T) == 4) ? 2 : 1);
+  constexpr int AHEAD = HW == 3 && D == 32 ? 1
+      : (sizeof(T) == 2 ? 4 : 2) / (HW == 3 || (HW == 2 && sizeof(T) == 4) ? 2 : 1);
   const int C = 2 * hk * D + hv * D;
   // part: 0 q, 1 k, 2 + i v of the round's head i; e: the first of 8 channels
   const int part = SPLIT == 1 || lane < 2 * G8 ? lane / G8 : 2 + (lane - 2 * G8) / V8;
@@ -538,10 +539,13 @@ static void launch_step_d(const gdn_shape& s, const StepArgs& a, hipStream_t st)
     // (one sequence, 48 heads over 16: 9.4 us against 13.6 us one by one; 64
     // sequences 77 against 88 us); with many, one by one in smaller workgroups
     // overlap better (256 sequences 294 against 302 us, 32 heads 198 against
-    // 211 us).  They meet at about 2000 workgroups.
-    if (group == 1 || groups >= 2048) launch_step_k<T, D, 1, 1, STEP>(s, a, group, st);
-    else if (group == 2 || group == 4 || D == 32) launch_step_k<T, D, 2, 1, STEP>(s, a, group, st);
-    else if constexpr (D == 128) launch_step_k<T, D, 3, 1, STEP>(s, a, group, st);
+    // 211 us).  They meet at about 2000 workgroups.  Heads of 32 columns have
+    // little to overlap and stay together (380 sequences of two tokens, 48
+    // heads over 16: three together 49.5 us, two 54.2 us, one by one 56.0 us;
+    // 32 heads over 8: two together 33.2 us, four 43.5 us, one by one 42.1 us).
+    if (group == 1 || (D == 128 && groups >= 2048)) launch_step_k<T, D, 1, 1, STEP>(s, a, group, st);
+    else if (group == 2 || group == 4) launch_step_k<T, D, 2, 1, STEP>(s, a, group, st);
+    else launch_step_k<T, D, 3, 1, STEP>(s, a, group, st);
   } else {
     // A head over four workgroups while that still fills the chip's 256 CUs:
     // 8 heads 4.2 us against 5.0 us for one token, 13.8 against 28.0 us for

@@ -141,8 +141,11 @@ CASES = {
     "four_of_a_group_fp32": dict(dtype="fp32", hk=2, hv=8, d=128, lens=[5, 11, 2, 7, 8, 1]),
     "seven_of_a_group_fp16_strided": dict(dtype="fp16", hk=1, hv=7, d=32, lens=[17, 0, 1], strided=True),
     "three_of_a_group_fp32_short": dict(dtype="fp32", hk=3, hv=9, d=128, lens=[1, 6, 0, 2]),
-    # so many groups that their heads go one by one
+    # a few thousand groups
     "many_bf16": dict(dtype="bf16", hk=2, hv=4, d=32, lens=[1] * 1000 + [2] * 40),
+    "three_together_fp16": dict(dtype="fp16", hk=2, hv=6, d=32, lens=[1, 9, 0, 2, 7]),
+    "five_of_a_group_fp32_strided": dict(dtype="fp32", hk=2, hv=10, d=32, lens=[3, 8, 1, 0], strided=True),
+    "many_of_three_bf16": dict(dtype="bf16", hk=4, hv=12, d=32, lens=[1] * 520 + [0] * 5 + [3] * 4),
     "most_heads_bf16": dict(dtype="bf16", hk=1, hv=256, d=32, lens=[1, 2]),
 }
 
