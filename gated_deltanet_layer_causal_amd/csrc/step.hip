@@ -579,8 +579,8 @@ static void launch_step_d(const gdn_shape& s, const StepArgs& a, hipStream_t st)
     else launch_step_k<T, D, 3, 1, STEP>(s, a, group, st);
   } else {
     // A head over four workgroups while that still fills the chip's 256 CUs:
-    // 8 heads 4.2 us against 5.0 us for one token, 13.8 against 28.0 us for
-    // 32; 192 heads 25.0 against 32.0 us; 384 heads 46.3 against 45.1 us.
+    // 8 heads 3.8 us against 4.4 us for one token, 12.4 against 26.4 us for
+    // 32; 192 heads 23.3 against 30.7 us; 384 heads 41.1 against 40.3 us.
     if constexpr (D == 128)
       if ((int64_t)s.n_seq * s.hv <= 256) return launch_step_k<T, D, 1, 4, STEP>(s, a, 1, st);
     launch_step_k<T, D, 1, 1, STEP>(s, a, 1, st);
