@@ -53,10 +53,11 @@ __device__ __forceinline__ float lane_of(float x, int l) {
 // that the lanes of a row touch whole 128-byte lines at a time (with two
 // lanes a row at D = 32, 32 bytes of each line, the rule took 125 us instead
 // of 32 us for 254 sequences x 48 heads with every state kept twice).  SPLIT
-// workgroups share a head, VC value rows each.
-template <int D, int HW, int SPLIT> struct StepGeo {
+// workgroups share a head, VC value rows each; R < 4 / SPLIT spreads them over
+// more waves.
+template <int D, int HW, int SPLIT, int R_ = 4 / SPLIT> struct StepGeo {
   static constexpr int LPR = 8, NC = D / (4 * LPR);
-  static constexpr int R = 4 / SPLIT;
+  static constexpr int R = R_;
   static constexpr int RPW = 64 / LPR;              // rows per wave and row slot
   static constexpr int VC = D / SPLIT;
   static constexpr int WAVES = VC / (RPW * R);      // state waves of a head
@@ -84,8 +85,8 @@ struct StepSpan {
 };
 
 // A head's state: its load, its tokens, its store.
-template <int D, int SPLIT> struct StepState {
-  typedef StepGeo<D, 1, SPLIT> G;
+template <int D, int SPLIT, int R> struct StepState {
+  typedef StepGeo<D, 1, SPLIT, R> G;
   floatx4 S[G::R][G::NC];
   uint32_t row0, col0, at;   // first row of the workgroup's, first column, and their byte in S
 
@@ -134,7 +135,7 @@ template <int D, int SPLIT> struct StepState {
   }
   // k . q of a whole block, token lane / 8 in each lane, instead of each
   // token's in every group of lanes; summed in the same order.  The rule takes
-  // it so: 512 tokens of 48 heads 145 us against 157 us, 7 sequences of up to
+  // it so, and the step of long pieces with eight waves a head: 512 tokens of 48 heads 145 us against 157 us, 7 sequences of up to
   // 97 tokens x 32 heads 38 us against 40 us.  In the step's short calls it
   // would only stand between a barrier and the first token (64 sequences 81.4
   // against 80.5 us, 384 sequences 428 against 426.5 us).
@@ -208,12 +209,12 @@ template <int D, int SPLIT> struct StepState {
   }
 };
 
-template <int D, int HW, int SPLIT, bool STEP>
+template <int D, int HW, int SPLIT, bool BLOCK_KQ, int R>
 __device__ __forceinline__ void step_state_wave(const StepArgs& p, const StepSpan& w,
                                                 StepLds<D, HW, SPLIT>& lds, int wave, int lane) {
-  constexpr int WAVES = StepGeo<D, HW, SPLIT>::WAVES;
+  constexpr int WAVES = StepGeo<D, HW, SPLIT, R>::WAVES;
   const int hw = wave / WAVES;                    // which of the round's heads
-  StepState<D, SPLIT> st(wave % WAVES, lane, w.v0);
+  StepState<D, SPLIT, R> st(wave % WAVES, lane, w.v0);
   int h = w.h0 + hw, blk = 0;
   if (h < w.h1) st.load(p, w.s_in, h);
   for (int i = 0; i < w.items; ++i) {
@@ -221,11 +222,11 @@ __device__ __forceinline__ void step_state_wave(const StepArgs& p, const StepSpa
     const int left = w.t1 - w.t0 - blk * STEP_TB;
     const int nt = h >= w.h1 ? 0 : left < STEP_TB ? left : STEP_TB;
     __syncthreads();   // q, k, v of item i are in LDS
-    const float kq = STEP ? 0.f : StepState<D, SPLIT>::block_kq(lds.q[buf], lds.k[buf], lane);
+    const float kq = !BLOCK_KQ ? 0.f : StepState<D, SPLIT, R>::block_kq(lds.q[buf], lds.k[buf], lane);
     for (int j = 0; j < nt; ++j) {
-      st.template token<!STEP>(lds.q[buf][j], lds.k[buf][j], lds.v[vb][hw][j], lds.eg[buf][hw][j],
+      st.template token<BLOCK_KQ>(lds.q[buf][j], lds.k[buf][j], lds.v[vb][hw][j], lds.eg[buf][hw][j],
                                lds.beta[buf][hw][j],
-                               STEP ? 0.f : lane_of(kq, j * StepGeo<D, HW, SPLIT>::LPR), lane);
+                               !BLOCK_KQ ? 0.f : lane_of(kq, j * StepGeo<D, HW, SPLIT>::LPR), lane);
       if (p.slot_tok) {
         const int slot = __builtin_amdgcn_readfirstlane(lds.tok[buf][j]);
         if (slot >= 0) st.store(p, slot, h);
@@ -452,11 +453,11 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
   finish(w.items - 1, cur);
 }
 
-template <typename T, int D, int HW, int SPLIT, bool STEP>
-__global__ void __launch_bounds__((StepGeo<D, HW, SPLIT>::THREADS), 4) step_kernel(StepArgs p, int hk, int hv,
+template <typename T, int D, int HW, int SPLIT, bool STEP, int R>
+__global__ void __launch_bounds__((StepGeo<D, HW, SPLIT, R>::THREADS), 4) step_kernel(StepArgs p, int hk, int hv,
                                                                                  int heads, int T_tok) {
   static_assert(SPLIT == 1 || (!STEP && HW == 1), "the norm needs whole rows");
-  typedef StepGeo<D, HW, SPLIT> G;
+  typedef StepGeo<D, HW, SPLIT, R> G;
   __shared__ StepLds<D, HW, SPLIT> lds;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int per = hv / heads * SPLIT, n = blockIdx.x / per;
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__((StepGeo<D, HW, SPLIT>::THREADS), 4) step_kern
   if (w.t0 == w.t1) {   // no tokens: the state passes through
     if (w.s_out < 0 || w.s_out == w.s_in) return;
     if (wave < HW * G::WAVES) {
-      StepState<D, SPLIT> st(wave % G::WAVES, lane, w.v0);
+      StepState<D, SPLIT, R> st(wave % G::WAVES, lane, w.v0);
       for (int h = w.h0 + wave / G::WAVES; h < w.h1; h += HW) {
         st.load(p, w.s_in, h);
         st.store(p, w.s_out, h);
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__((StepGeo<D, HW, SPLIT>::THREADS), 4) step_kern
   }
   w.nb = (w.t1 - w.t0 - 1) / STEP_TB + 1;
   w.items = (heads + HW - 1) / HW * w.nb;
-  if (wave < HW * G::WAVES) step_state_wave<D, HW, SPLIT, STEP>(p, w, lds, wave, lane);
+  if (wave < HW * G::WAVES) step_state_wave<D, HW, SPLIT, !STEP || R == 2, R>(p, w, lds, wave, lane);
   else step_helper_wave<T, D, HW, SPLIT, STEP>(p, w, lds, hk, hv, tid - 64 * HW * G::WAVES);
 }
 
@@ -538,12 +539,12 @@ __global__ void __launch_bounds__(256) step_rows_kernel(StepArgs p, int n_grp, i
   if (s_out >= 0 && (t1 > t0 || s_out != s_in)) put(s_out);
 }
 
-template <typename T, int D, int HW, int SPLIT, bool STEP>
+template <typename T, int D, int HW, int SPLIT, bool STEP, int R = 4 / SPLIT>
 static void launch_step_k(const gdn_shape& s, StepArgs a, int heads, hipStream_t st) {
   const unsigned grid = (unsigned)s.n_seq * (unsigned)(s.hv / heads) * SPLIT;
   a.through = grid >= STEP_THROUGH;
-  hipLaunchKernelGGL((step_kernel<T, D, HW, SPLIT, STEP>), dim3(grid),
-                     dim3(StepGeo<D, HW, SPLIT>::THREADS), 0, st, a, s.hk, s.hv, heads,
+  hipLaunchKernelGGL((step_kernel<T, D, HW, SPLIT, STEP, R>), dim3(grid),
+                     dim3(StepGeo<D, HW, SPLIT, R>::THREADS), 0, st, a, s.hk, s.hv, heads,
                      (int)s.total_tokens);
 }
 
@@ -556,10 +557,16 @@ static void launch_step_d(const gdn_shape& s, const StepArgs& a, hipStream_t st)
     // and workgroups few, three or more heads of a group go apart, which costs
     // the second launch (4 sequences, 48 heads over 16: 8 tokens 23.5 us
     // against 25.7 us together, 48 tokens 68 against 99 us; 8 heads over 2:
-    // 61 against 133 us; 256 key heads, 16 tokens: 61 against 45 us).
+    // 61 against 133 us; 256 key heads, 16 tokens: 61 against 45 us; all with
+    // four waves a head).
     const bool apart = group >= 3 && groups <= 128 && s.total_tokens >= 8 * (int64_t)s.n_seq;
     if (apart) {
-      launch_step_k<T, D, 1, 1, STEP>(s, a, 1, st);
+      // While each has a CU to itself, a head's rows go over eight waves
+      // instead of four (4 sequences, 48 heads: 8 tokens 16.7 against 19.1 us,
+      // 48 tokens 53.7 against 55.9 us; two on a CU have no room for that: 6
+      // sequences, 48 tokens 102 against 80 us).
+      if (D == 128 && (int64_t)s.n_seq * s.hv <= 256) launch_step_k<T, D, 1, 1, STEP, D == 128 ? 2 : 4>(s, a, 1, st);
+      else launch_step_k<T, D, 1, 1, STEP>(s, a, 1, st);
       const int C = 2 * s.hk * D + s.hv * D, n_grp = 2 * s.hk * D / 8;
       if (a.slot_out || a.slot_tok)
         hipLaunchKernelGGL((step_rows_kernel<T>), dim3((n_grp + 255) / 256, s.n_seq), dim3(256), 0, st, a,
