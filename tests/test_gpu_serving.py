@@ -141,6 +141,10 @@ CASES = {
     "four_of_a_group_fp32": dict(dtype="fp32", hk=2, hv=8, d=128, lens=[5, 11, 2, 7, 8, 1]),
     "seven_of_a_group_fp16_strided": dict(dtype="fp16", hk=1, hv=7, d=32, lens=[17, 0, 1], strided=True),
     "three_of_a_group_fp32_short": dict(dtype="fp32", hk=3, hv=9, d=128, lens=[1, 6, 0, 2]),
+    # apart, with a head over eight waves, and (over 256 heads) over four
+    "apart_fp32": dict(dtype="fp32", hk=1, hv=3, d=128, lens=[9, 17, 8]),
+    "apart_fp16_strided": dict(dtype="fp16", hk=2, hv=8, d=128, lens=[12, 0, 15, 25], strided=True),
+    "apart_many_heads_bf16": dict(dtype="bf16", hk=2, hv=16, d=128, lens=[8] * 19 + [12]),
     # a few thousand groups
     "many_bf16": dict(dtype="bf16", hk=2, hv=4, d=32, lens=[1] * 1000 + [2] * 40),
     "three_together_fp16": dict(dtype="fp16", hk=2, hv=6, d=32, lens=[1, 9, 0, 2, 7]),
