@@ -559,19 +559,29 @@ static void launch_step_d(const gdn_shape& s, const StepArgs& a, hipStream_t st)
   if constexpr (STEP) {
     const int group = s.hv / s.hk;
     const int64_t groups = (int64_t)s.n_seq * s.hk;
-    // A workgroup's tokens take about 1 us each and head: where they are many
-    // and workgroups few, three or more heads of a group go apart, which costs
-    // the second launch (4 sequences, 48 heads over 16: 8 tokens 23.5 us
-    // against 25.7 us together, 48 tokens 68 against 99 us; 8 heads over 2:
-    // 61 against 133 us; 256 key heads, 16 tokens: 61 against 45 us; all with
-    // four waves a head).
-    const bool apart = group >= 3 && groups <= 128 && s.total_tokens >= 8 * (int64_t)s.n_seq;
+    // While there are no more than 128 groups, heads of a group can go apart,
+    // each into a workgroup of its own, at the price of the second launch.
+    // Four or more would otherwise take turns two or three at a time (d = 128:
+    // 8 sequences of one token, 16 heads over 2: 9.4 us against 21.0 us, of
+    // four tokens 11.7 against 29.3 us; 32 over 8: 12.0 against 13.4 us;
+    // d = 32: 7.5 against 10.6 us; with 192 groups of four 25.0 against 23.2
+    // us).  Two or three go side by side otherwise, so that only pieces of
+    // several tokens gain (one sequence, 48 heads over 16: four tokens 10.9
+    // against 13.7 us, four sequences 13.2 against 14.6 us, of two 11.3
+    // against 10.9 us; 8 heads over 4, eight tokens 14.3 against 15.9 us, four
+    // 10.4 both), more heads than CUs later (7 sequences, 48 heads: four 17.1
+    // against 16.4 us, eight 23.6 us both), and those of 32 columns never (8
+    // tokens: 14.1 against 11.5 us).
+    const bool few = D == 128 && (int64_t)s.n_seq * s.hv <= 256;
+    const int64_t pieces = group == 2 ? few ? 8 : 0 : few ? 4 : 8;   // tokens a sequence; 0: never
+    const bool apart = groups <= 128 &&
+        (group >= 4 || (D == 128 && group > 1 && pieces > 0 && s.total_tokens >= pieces * s.n_seq));
     if (apart) {
-      // While each has a CU to itself, a head's rows go over eight waves
-      // instead of four (4 sequences, 48 heads: 8 tokens 16.7 against 19.1 us,
-      // 48 tokens 53.7 against 55.9 us; two on a CU have no room for that: 6
-      // sequences, 48 tokens 102 against 80 us).
-      if (D == 128 && (int64_t)s.n_seq * s.hv <= 256) launch_step_k<T, D, 1, 1, STEP, D == 128 ? 2 : 4>(s, a, 1, st);
+      // With a CU to each, a head's rows go over eight waves instead of four (4
+      // sequences, 48 heads: 8 tokens 16.7 against 19.1 us, 48 tokens 53.7
+      // against 55.9 us; two on a CU have no room for that: 6 sequences, 48
+      // tokens 102 against 80 us).
+      if (few) launch_step_k<T, D, 1, 1, STEP, D == 128 ? 2 : 4>(s, a, 1, st);
       else launch_step_k<T, D, 1, 1, STEP>(s, a, 1, st);
       const int C = 2 * s.hk * D + s.hv * D, n_grp = 2 * s.hk * D / 8;
       if (a.slot_out || a.slot_tok)
