@@ -145,6 +145,12 @@ CASES = {
     "apart_fp32": dict(dtype="fp32", hk=1, hv=3, d=128, lens=[9, 17, 8]),
     "apart_fp16_strided": dict(dtype="fp16", hk=2, hv=8, d=128, lens=[12, 0, 15, 25], strided=True),
     "apart_many_heads_bf16": dict(dtype="bf16", hk=2, hv=16, d=128, lens=[8] * 19 + [12]),
+    # too many groups for that: in rounds of two and of three
+    "rounds_of_two_bf16": dict(dtype="bf16", hk=4, hv=16, d=128, lens=[1, 2, 0, 9] + [1] * 30),
+    "rounds_of_two_fp32": dict(dtype="fp32", hk=4, hv=16, d=32, lens=[3, 10, 0, 1] + [1] * 30, strided=True),
+    "rounds_of_three_fp16": dict(dtype="fp16", hk=2, hv=10, d=128, lens=[17, 0, 2] + [1] * 63),
+    "rounds_of_three_fp32": dict(dtype="fp32", hk=2, hv=10, d=128, lens=[9, 0, 2] + [1] * 63, act=1),
+    "rounds_of_three_bf16": dict(dtype="bf16", hk=4, hv=20, d=32, lens=[2, 0, 17] + [1] * 31, strided=True),
     # a few thousand groups
     "many_bf16": dict(dtype="bf16", hk=2, hv=4, d=32, lens=[1] * 1000 + [2] * 40),
     "three_together_fp16": dict(dtype="fp16", hk=2, hv=6, d=32, lens=[1, 9, 0, 2, 7]),
