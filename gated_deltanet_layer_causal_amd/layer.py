@@ -99,20 +99,27 @@ class GDNCore:
 
     def forward(self, x, w_conv, a, b, A_log, dt_bias, z, w_norm, cu_seqlens, S0=None,
                 want_final=False, timer=None, save_states=True, conv_state=None,
-                want_conv_state=False):
+                want_conv_state=False, ws_chunk=None):
         """conv_state [n_seq, 3, C] (optional): the carried conv state, the
         three input rows before each sequence; with want_conv_state the
         returned dict holds the final one under "conv_state_out" (the last
         three input rows of each sequence), so that a later call continues
-        the sequences (feed S_final and conv_state_out back in)."""
+        the sequences (feed S_final and conv_state_out back in).  ws_chunk
+        (optional, with save_states=False only): chunk scratch of at least
+        gdn_chunk_fwd_workspace bytes; no scratch of the core is used then."""
         c = self.cfg
         T = x.shape[0]
         n_seq = cu_seqlens.numel() - 1
         sh = self.shape(T, n_seq)
         if c.check_cu_seqlens:
             self.check_cu_seqlens(sh, cu_seqlens)
-        ws = self.workspace(sh, T * c.hv)
-        wc = self.chunk_workspace(sh, fresh=save_states)
+        if ws_chunk is not None:
+            if save_states:
+                raise ValueError("ws_chunk is scratch; saved states need a workspace that stays")
+            wc = ws_chunk
+        else:
+            ws = self.workspace(sh, T * c.hv)
+            wc = self.chunk_workspace(sh, fresh=save_states)
         dev, dt = x.device, c.dtype
         y = torch.empty((T, c.channels), dtype=dt, device=dev)
         cs_out = (torch.empty((n_seq, 3, c.channels), dtype=dt, device=dev) if want_conv_state
@@ -203,22 +210,27 @@ class GDNCore:
         """step() for long pieces (faster from about 100 tokens a sequence):
         the chunked forward from and into slots (contiguous a, b, z as
         forward(); cu_seqlens[-1] = T; dtypes and head dims of the chunked form).  A slot_in
-        outside the cache gives NaN, a slot_out outside it is not written."""
+        outside the cache gives NaN, a slot_out outside it is not written.
+        Every call has scratch of its own, so that one core may prefill
+        several caches on several streams, and a captured call keeps its."""
         c = self.cfg
         n_seq = cu_seqlens.numel() - 1
         slot_out = slot_in if slot_out is None else slot_out
         if slot_in.numel() != n_seq or slot_out.numel() != n_seq:
             raise ValueError(f"{n_seq} sequences, {slot_in.numel()} slots to read and "
                              f"{slot_out.numel()} to write")
+        sh = self.shape(x.shape[0], n_seq)
         if c.check_slots:
-            self.check_slots(self.shape(x.shape[0], n_seq), cache, slot_in, slot_out, None, cu_seqlens)
+            self.check_slots(sh, cache, slot_in, slot_out, None, cu_seqlens)
         S, conv = cache.S(layer), cache.conv(layer)
         S0 = torch.empty((n_seq,) + S.shape[1:], dtype=S.dtype, device=S.device)
         rows = torch.empty((n_seq,) + conv.shape[1:], dtype=conv.dtype, device=S.device)
         L.gdn_cache_copy(S, S0, src_idx=slot_in)
         L.gdn_cache_copy(conv, rows, src_idx=slot_in)
+        ws = torch.empty(L.gdn_chunk_fwd_workspace(sh), dtype=torch.uint8, device=S.device)
         f = self.forward(x, w_conv, a, b, A_log, dt_bias, z, w_norm, cu_seqlens, S0=S0,
-                         want_final=True, save_states=False, conv_state=rows, want_conv_state=True)
+                         want_final=True, save_states=False, conv_state=rows, want_conv_state=True,
+                         ws_chunk=ws)
         L.gdn_cache_copy(f["S_final"], S, dst_idx=slot_out)
         L.gdn_cache_copy(f["conv_state_out"], conv, dst_idx=slot_out)
         return f["out"]
