@@ -14,6 +14,7 @@ than an out-of-bounds device access.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from ctypes import POINTER, byref, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
@@ -601,6 +602,18 @@ def _on(dev, *named):
     for nm, t in named:
         if t is not None and t.device != dev:
             raise ValueError(f"{nm} is on {t.device}, the cache on {dev}")
+
+
+def same_device(dev, **named):
+    """ValueError naming the first tensor that is not on `dev`."""
+    _on(dev, *named.items())
+
+
+def current_device(dev):
+    """A context with `dev` as the current device, for the entry points that
+    run on the current device's stream (nothing for the host, whose tensors
+    they refuse)."""
+    return torch.cuda.device(dev) if dev.type == "cuda" else contextlib.nullcontext()
 
 
 def _slot_tables(shape, dev, cu, slot_in, slot_out, slot_tok):

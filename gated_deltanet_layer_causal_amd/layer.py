@@ -223,16 +223,20 @@ class GDNCore:
         if c.check_slots:
             self.check_slots(sh, cache, slot_in, slot_out, None, cu_seqlens)
         S, conv = cache.S(layer), cache.conv(layer)
-        S0 = torch.empty((n_seq,) + S.shape[1:], dtype=S.dtype, device=S.device)
-        rows = torch.empty((n_seq,) + conv.shape[1:], dtype=conv.dtype, device=S.device)
-        L.gdn_cache_copy(S, S0, src_idx=slot_in)
-        L.gdn_cache_copy(conv, rows, src_idx=slot_in)
-        ws = torch.empty(L.gdn_chunk_fwd_workspace(sh), dtype=torch.uint8, device=S.device)
-        f = self.forward(x, w_conv, a, b, A_log, dt_bias, z, w_norm, cu_seqlens, S0=S0,
-                         want_final=True, save_states=False, conv_state=rows, want_conv_state=True,
-                         ws_chunk=ws)
-        L.gdn_cache_copy(f["S_final"], S, dst_idx=slot_out)
-        L.gdn_cache_copy(f["conv_state_out"], conv, dst_idx=slot_out)
+        dev = S.device
+        L.same_device(dev, x=x, w_conv=w_conv, a=a, b=b, A_log=A_log, dt_bias=dt_bias, z=z,
+                      w_norm=w_norm, cu_seqlens=cu_seqlens, slot_in=slot_in, slot_out=slot_out)
+        with L.current_device(dev):     # forward() runs on the current device's stream
+            S0 = torch.empty((n_seq,) + S.shape[1:], dtype=S.dtype, device=dev)
+            rows = torch.empty((n_seq,) + conv.shape[1:], dtype=conv.dtype, device=dev)
+            L.gdn_cache_copy(S, S0, src_idx=slot_in)
+            L.gdn_cache_copy(conv, rows, src_idx=slot_in)
+            ws = torch.empty(L.gdn_chunk_fwd_workspace(sh), dtype=torch.uint8, device=dev)
+            f = self.forward(x, w_conv, a, b, A_log, dt_bias, z, w_norm, cu_seqlens, S0=S0,
+                             want_final=True, save_states=False, conv_state=rows, want_conv_state=True,
+                             ws_chunk=ws)
+            L.gdn_cache_copy(f["S_final"], S, dst_idx=slot_out)
+            L.gdn_cache_copy(f["conv_state_out"], conv, dst_idx=slot_out)
         return f["out"]
 
     def check_slots(self, sh, cache, slot_in, slot_out, slot_tok, cu_seqlens):

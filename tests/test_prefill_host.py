@@ -1,5 +1,7 @@
 """GDNCore.prefill's calls on the host (no GPU): the entry points are replaced
 by recorders, so that what each is given can be looked at."""
+import contextlib
+
 import pytest
 import torch
 
@@ -19,13 +21,14 @@ def calls(monkeypatch):
     return got
 
 
-def prefill(core, cache, T, n_seq=2):
+def prefill(core, cache, T, n_seq=2, **other):
     c, bf = core.cfg, torch.bfloat16
     h = torch.zeros(T, c.hv, dtype=bf)
-    cu = torch.tensor([0] + [T] * n_seq, dtype=torch.int32)
-    slots = torch.arange(n_seq, dtype=torch.int32)
-    return core.prefill(torch.zeros(T, c.channels, dtype=bf), torch.zeros(c.channels, 4), h, h, torch.zeros(c.hv),
-                        torch.zeros(c.hv), torch.zeros(T, c.hv, c.d, dtype=bf), torch.zeros(c.d), cu, cache, slots)
+    args = dict(x=torch.zeros(T, c.channels, dtype=bf), w_conv=torch.zeros(c.channels, 4), a=h, b=h,
+                A_log=torch.zeros(c.hv), dt_bias=torch.zeros(c.hv), z=torch.zeros(T, c.hv, c.d, dtype=bf),
+                w_norm=torch.zeros(c.d), cu_seqlens=torch.tensor([0] + [T] * n_seq, dtype=torch.int32), cache=cache,
+                slot_in=torch.arange(n_seq, dtype=torch.int32))
+    return core.prefill(**dict(args, **other))
 
 
 def make():
@@ -55,3 +58,29 @@ def test_saved_states_do_not_go_into_scratch():
     z = torch.zeros(1)
     with pytest.raises(ValueError, match="ws_chunk"):
         core.forward(z.view(1, 1), z, z, z, z, z, z, z, torch.zeros(2, dtype=torch.int32), ws_chunk=z)
+
+
+def test_prefill_runs_on_the_caches_device(calls, monkeypatch):
+    """The copies from and into the cache and the chunked forward go to one
+    device's stream, whichever device is the current one."""
+    core, cache = make()
+    on = []
+
+    @contextlib.contextmanager
+    def current(dev):
+        on.append((dev, len(calls)))
+        yield
+        on.append((dev, len(calls)))
+
+    monkeypatch.setattr(L, "current_device", current, raising=False)
+    prefill(core, cache, 5)
+    assert on == [(cache.buffer.device, 0), (cache.buffer.device, len(calls))] and len(calls) == 9
+
+
+def test_prefill_refuses_tensors_on_other_devices(calls):
+    core, cache = make()
+    for name in ("x", "w_conv", "a", "b", "A_log", "dt_bias", "z", "w_norm", "cu_seqlens", "slot_in", "slot_out"):
+        t = torch.zeros(5, 128, dtype=torch.bfloat16) if name == "x" else torch.zeros(3 if name == "cu_seqlens" else 2)
+        with pytest.raises(ValueError, match=f"{name} is on meta, the cache on cpu"):
+            prefill(core, cache, 5, **{name: t.to("meta")})
+    assert not calls
