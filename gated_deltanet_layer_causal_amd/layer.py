@@ -226,6 +226,9 @@ class GDNCore:
         dev = S.device
         L.same_device(dev, x=x, w_conv=w_conv, a=a, b=b, A_log=A_log, dt_bias=dt_bias, z=z,
                       w_norm=w_norm, cu_seqlens=cu_seqlens, slot_in=slot_in, slot_out=slot_out)
+        if x.shape[0] == 0:             # the chunked entry points want a token
+            return self.step(x, w_conv, a, b, A_log, dt_bias, z, w_norm, cu_seqlens, cache, slot_in,
+                             slot_out, layer=layer)
         with L.current_device(dev):     # forward() runs on the current device's stream
             S0 = torch.empty((n_seq,) + S.shape[1:], dtype=S.dtype, device=dev)
             rows = torch.empty((n_seq,) + conv.shape[1:], dtype=conv.dtype, device=dev)

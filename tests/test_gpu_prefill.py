@@ -1,10 +1,12 @@
 """GDNCore.prefill on the GPU: several at once, captured, and at its edges.
 Values are compared with the same calls made one after the other, bit by bit
 (the chunked form's own accuracy is tested with its entry points)."""
+import numpy as np
 import pytest
 import torch
 
 from gated_deltanet_layer_causal_amd.layer import GDNStateCache
+from tests.gpu_util import host
 from tests.test_gpu_serving import Case, ints
 
 pytestmark = pytest.mark.gpu
@@ -64,3 +66,12 @@ def test_captured_and_replayed_beside_longer_calls():
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(c.cache.buffer, after), k
         assert torch.equal(lgot, lwant) and torch.equal(other.buffer, lafter), k
+
+
+def test_no_tokens_pass_states_through():
+    c = Case("bf16", 1, 2, 128, [0, 0, 0], 6)
+    got = c.core.prefill(*c.args(), c.cache, ints([0, 3, -1]), ints([1, 3, 4]))
+    assert got.shape == (0, 2, 128)
+    S, conv = c.S.copy(), c.conv.copy()
+    S[1], conv[1], S[4], conv[4] = S[0], conv[0], 0, 0
+    assert np.array_equal(host(c.cache.S()), S) and np.array_equal(host(c.cache.conv()), conv)

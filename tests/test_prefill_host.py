@@ -84,3 +84,13 @@ def test_prefill_refuses_tensors_on_other_devices(calls):
         with pytest.raises(ValueError, match=f"{name} is on meta, the cache on cpu"):
             prefill(core, cache, 5, **{name: t.to("meta")})
     assert not calls
+
+
+def test_prefill_of_no_tokens_passes_states_through(calls, monkeypatch):
+    """A batch of empty sequences: what step() does with one."""
+    core, cache = make()
+    monkeypatch.setattr(L, "gdn_step_fwd", lambda *a, **kw: calls.append(("gdn_step_fwd", a)))
+    out = prefill(core, cache, 0, slot_out=torch.tensor([2, 3], dtype=torch.int32))
+    assert [name for name, _ in calls] == ["gdn_step_fwd"] and out.shape == (0, 2, 32)
+    slot_in, slot_out = calls[0][1][11:13]
+    assert slot_in.tolist() == [0, 1] and slot_out.tolist() == [2, 3]
