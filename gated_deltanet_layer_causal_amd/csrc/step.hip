@@ -466,9 +466,9 @@ __global__ void __launch_bounds__((StepGeo<D, HW, SPLIT, R>::THREADS), 4) step_k
   typedef StepGeo<D, HW, SPLIT, R> G;
   __shared__ StepLds<D, HW, SPLIT> lds;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int per = hv / heads * SPLIT, n = blockIdx.x / per;
+  const int n = blockIdx.y;
   StepSpan w;
-  w.h0 = blockIdx.x % per / SPLIT * heads;
+  w.h0 = blockIdx.x / SPLIT * heads;
   w.v0 = blockIdx.x % SPLIT * G::VC;
   w.h1 = w.h0 + heads;
   w.kh = w.h0 / (hv / hk);
@@ -547,9 +547,10 @@ __global__ void __launch_bounds__(256) step_rows_kernel(StepArgs p, int n_grp, i
 
 template <typename T, int D, int HW, int SPLIT, bool STEP, int R = 4 / SPLIT>
 static void launch_step_k(const gdn_shape& s, StepArgs a, int heads, hipStream_t st) {
-  const unsigned grid = (unsigned)s.n_seq * (unsigned)(s.hv / heads) * SPLIT;
-  a.through = grid >= STEP_THROUGH;
-  hipLaunchKernelGGL((step_kernel<T, D, HW, SPLIT, STEP, R>), dim3(grid),
+  // heads fastest; in one dimension the threads could pass 2^32, which no launch takes
+  const dim3 grid((unsigned)(s.hv / heads) * SPLIT, (unsigned)s.n_seq);
+  a.through = grid.x * grid.y >= STEP_THROUGH;
+  hipLaunchKernelGGL((step_kernel<T, D, HW, SPLIT, STEP, R>), grid,
                      dim3(StepGeo<D, HW, SPLIT, R>::THREADS), 0, st, a, s.hk, s.hv, heads,
                      (int)s.total_tokens);
 }
