@@ -48,6 +48,14 @@ __device__ __forceinline__ float lane_of(float x, int l) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l));
 }
 
+// Between LDS reads of some lanes of a wave and writes of others to the same
+// words: a wave's LDS operations take effect in order, so only the compiler has
+// to keep them so (no instruction comes of it).
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Thread layout of the state: LPR lanes share a row of D columns; a lane
 // holds the columns 4 l + 4 LPR c + (0..3), c = 0 .. NC - 1, of R rows, so
 // that the lanes of a row touch whole 128-byte lines at a time (with two
@@ -453,6 +461,7 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
     if (i + 1 < w.items) fetch(next);
     if (i > 0) finish(i - 1, prev);
     load_z(cur);
+    if constexpr (NV == 2) wave_lds_order();   // prep puts v where other lanes read o in finish
     if (i + 1 < w.items) prep(i + 1, next);
   }
   __syncthreads();
