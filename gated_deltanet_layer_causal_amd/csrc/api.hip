@@ -476,6 +476,7 @@ gdn_status gdn_cache_fork(void* base, int64_t stride, int32_t n_slots, int32_t* 
                           const int32_t* src, int32_t n, int32_t* dst, void* ws, size_t ws_bytes,
                           void* stream) {
   if (n < 0) return GDN_ERR_INVALID_ARG;
+  if (stride < 16) return GDN_ERR_INVALID_ARG;   // slots of nothing: no move to launch
   GDN_TRY(check_slot_rows(base, stride, stride, n_slots));
   if (!refs || (n > 0 && (!src || !dst))) return GDN_ERR_INVALID_ARG;
   if (!ws || ws_bytes < cache_ws_bytes(n_slots) || !aligned16(ws)) return GDN_ERR_WORKSPACE;
@@ -499,6 +500,7 @@ gdn_status gdn_cache_compact(void* base, int64_t stride, int32_t n_slots, int32_
                              int32_t* remap, int32_t* table, int32_t n_table, void* ws,
                              size_t ws_bytes, void* stream) {
   if (n_table < 0) return GDN_ERR_INVALID_ARG;
+  if (stride < 16) return GDN_ERR_INVALID_ARG;   // slots of nothing: no move to launch
   GDN_TRY(check_slot_rows(base, stride, stride, n_slots));
   if (!refs || !remap || (n_table > 0 && !table)) return GDN_ERR_INVALID_ARG;
   if (!ws || ws_bytes < cache_ws_bytes(n_slots) || !aligned16(ws)) return GDN_ERR_WORKSPACE;

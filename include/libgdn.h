@@ -401,7 +401,8 @@ gdn_status gdn_cache_copy(const void* src, int64_t src_stride, int32_t n_src,
  * lowest slots first, and fills it: a copy of slot src[i], or zeros where
  * src[i] == -1.  dst[i] receives the slot, and its count becomes 1.  Where
  * src[i] < -1 (no request), src[i] >= n_slots, src[i] is a free slot, or no
- * free slot is left, dst[i] = -1 and nothing is taken. */
+ * free slot is left, dst[i] = -1 and nothing is taken.  stride >= 16, here
+ * and in gdn_cache_compact. */
 gdn_status gdn_cache_fork(void* base, int64_t stride, int32_t n_slots, int32_t* refs,
                           const int32_t* src, int32_t n, int32_t* dst, void* ws, size_t ws_bytes,
                           void* stream);
