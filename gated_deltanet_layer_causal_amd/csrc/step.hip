@@ -475,9 +475,9 @@ __global__ void __launch_bounds__((StepGeo<D, HW, SPLIT, R>::THREADS), 4) step_k
   typedef StepGeo<D, HW, SPLIT, R> G;
   __shared__ StepLds<D, HW, SPLIT> lds;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n = blockIdx.y;
+  const int per = hv / heads * SPLIT, n = blockIdx.x / per;
   StepSpan w;
-  w.h0 = blockIdx.x / SPLIT * heads;
+  w.h0 = blockIdx.x % per / SPLIT * heads;
   w.v0 = blockIdx.x % SPLIT * G::VC;
   w.h1 = w.h0 + heads;
   w.kh = w.h0 / (hv / hk);
@@ -556,12 +556,22 @@ __global__ void __launch_bounds__(256) step_rows_kernel(StepArgs p, int n_grp, i
 
 template <typename T, int D, int HW, int SPLIT, bool STEP, int R = 4 / SPLIT>
 static void launch_step_k(const gdn_shape& s, StepArgs a, int heads, hipStream_t st) {
-  // heads fastest; in one dimension the threads could pass 2^32, which no launch takes
-  const dim3 grid((unsigned)(s.hv / heads) * SPLIT, (unsigned)s.n_seq);
-  a.through = grid.x * grid.y >= STEP_THROUGH;
-  hipLaunchKernelGGL((step_kernel<T, D, HW, SPLIT, STEP, R>), grid,
-                     dim3(StepGeo<D, HW, SPLIT, R>::THREADS), 0, st, a, s.hk, s.hv, heads,
-                     (int)s.total_tokens);
+  constexpr unsigned THREADS = StepGeo<D, HW, SPLIT, R>::THREADS;
+  const unsigned per = (unsigned)(s.hv / heads) * SPLIT;
+  a.through = (unsigned)s.n_seq * per >= STEP_THROUGH;
+  // A launch takes fewer than 2^32 threads; 65535 sequences of 256 heads are
+  // more, and go in two.  (Sequences on a second grid dimension cost long
+  // pieces their registers: 4 sequences of 1024 tokens 1045 against 1035 us.)
+  const unsigned most = 0xffffffffu / (THREADS * per);
+  for (unsigned left = s.n_seq; left > 0;) {
+    const unsigned now = left < most ? left : most;
+    hipLaunchKernelGGL((step_kernel<T, D, HW, SPLIT, STEP, R>), dim3(now * per), dim3(THREADS), 0, st, a,
+                       s.hk, s.hv, heads, (int)s.total_tokens);
+    a.cu += now;
+    if (a.slot_in) a.slot_in += now;
+    if (a.slot_out) a.slot_out += now;
+    left -= now;
+  }
 }
 
 template <typename T, int D, bool STEP>
