@@ -611,9 +611,11 @@ def same_device(dev, **named):
 
 def current_device(dev):
     """A context with `dev` as the current device, for the entry points that
-    run on the current device's stream (nothing for the host, whose tensors
-    they refuse)."""
-    return torch.cuda.device(dev) if dev.type == "cuda" else contextlib.nullcontext()
+    run on the current device's stream (nothing to do where it is, nor for the
+    host, whose tensors they refuse)."""
+    if dev.type != "cuda" or dev.index == _get_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
 
 
 def _slot_tables(shape, dev, cu, slot_in, slot_out, slot_tok):
