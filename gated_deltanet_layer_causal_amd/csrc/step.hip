@@ -461,8 +461,10 @@ __device__ __forceinline__ void step_helper_wave(const StepArgs& p, const StepSp
     if (i + 1 < w.items) fetch(next);
     if (i > 0) finish(i - 1, prev);
     load_z(cur);
-    if constexpr (NV == 2) wave_lds_order();   // prep puts v where other lanes read o in finish
-    if (i + 1 < w.items) prep(i + 1, next);
+    if (i + 1 < w.items) {
+      if constexpr (NV == 2) wave_lds_order();   // prep puts v where other lanes read o in finish
+      prep(i + 1, next);
+    }
   }
   __syncthreads();
   finish(w.items - 1, cur);
