@@ -223,7 +223,7 @@ hipError_t launch_cache_compact(void* base, int64_t stride, int32_t n_slots, int
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || n_slots < 2) return e;
   // up to half of the slots move, usually far fewer: 60 of up to 100 slots of
-  // 12.8 MB take 120 us with 131072 workgroups, 126 us with one for every
+  // 6.4 MB take 120 us with 131072 workgroups, 126 us with one for every
   // piece that could have to move
   hipLaunchKernelGGL(cache_move_kernel, dim3(copy_grid(n_slots / 2, stride, 1 << 17)), dim3(256), 0, st,
                      (char*)base, stride, (const int32_t*)ws, room);

@@ -19,15 +19,17 @@
 // load the state or walk the block before, and norm and store the outputs of
 // the block behind them: neither their loads nor their arithmetic sit between
 // a state's load and its store.  One barrier per block joins the two; the
-// blocks of q, k, v alternate between two buffers.
+// blocks of q and k alternate between two buffers, those of v (and o, which
+// takes its place) between two or, with more than one helper wave, three.
 #include "chunk_stream.h"
 #include "launch.h"
 
 namespace gdn {
 
 constexpr int STEP_TB = 8;             // tokens per block
-constexpr unsigned STEP_THROUGH = 128; // workgroups from which states are written through:
-                                       // even at 148 (11.5 us against 11.7 us without)
+constexpr unsigned STEP_THROUGH = 128; // workgroups from which states are written through: a
+                                       // loss at 16, a gain at thousands, no difference at 148
+                                       // (11.5 against 11.7 us, the spread of one side's runs)
 
 // Tokens of sequence n, clamped so that no table can lead outside [0, T].
 __device__ __forceinline__ void token_range(const int32_t* cu, int n, int T, int& t0, int& t1) {
@@ -562,8 +564,8 @@ static void launch_step_k(const gdn_shape& s, StepArgs a, int heads, hipStream_t
   const unsigned per = (unsigned)(s.hv / heads) * SPLIT;
   a.through = (unsigned)s.n_seq * per >= STEP_THROUGH;
   // A launch takes fewer than 2^32 threads; 65535 sequences of 256 heads are
-  // more, and go in two.  (Sequences on a second grid dimension cost long
-  // pieces their registers: 4 sequences of 1024 tokens 1045 against 1035 us.)
+  // more, and go in two.  (With the sequences on a second grid dimension 4 of
+  // 1024 tokens take 1045 us instead of 1035 us.)
   const unsigned most = 0xffffffffu / (THREADS * per);
   for (unsigned left = s.n_seq; left > 0;) {
     const unsigned now = left < most ? left : most;
@@ -593,7 +595,11 @@ static void launch_step_d(const gdn_shape& s, const StepArgs& a, hipStream_t st)
     // against 10.9 us; 8 heads over 4, eight tokens 14.3 against 15.9 us, four
     // 10.4 both), more heads than CUs later (7 sequences, 48 heads: four 17.1
     // against 16.4 us, eight 23.6 us both), and those of 32 columns never (8
-    // tokens: 14.1 against 11.5 us).
+    // tokens: 14.1 against 11.5 us).  The limit of 128 is that of groups of
+    // four; larger groups gain most (80 sequences, 16 heads over one: 40
+    // against 61 us) and were not measured beyond it.  The lengths are on the
+    // device: what counts here are the rows of the call, those of a padded
+    // batch among them.
     const bool few = D == 128 && (int64_t)s.n_seq * s.hv <= 256;
     const int64_t pieces = group == 2 ? few ? 8 : 0 : few ? 4 : 8;   // tokens a sequence; 0: never
     const bool apart = groups <= 128 &&

@@ -174,9 +174,12 @@ class GDNCore:
         slot_in[n] of the GDNStateCache (-1: a new sequence) and written to
         slot_out[n] (default: in place; -1: nowhere); slot_tok [T] names slots
         for the states after single tokens (-1: none).  Rows behind
-        cu_seqlens[-1] are left alone, so a batch may be padded.  Results
-        match forward() up to rounding: nothing is rounded between the conv,
-        the rule and the norm.  No workspace, nothing synchronises."""
+        cu_seqlens[-1] are neither read nor written, so a batch may be
+        padded; out's hold what the new memory held, NaN perhaps.  A slot_in
+        or slot_out outside the cache gives NaN rows, and no state of that
+        sequence is written.  Results match forward() up to rounding: nothing
+        is rounded between the conv, the rule and the norm.  No workspace,
+        nothing synchronises."""
         c = self.cfg
         T = x.shape[0]
         sh = self._step_shape(T, cu_seqlens.numel() - 1)
@@ -207,12 +210,16 @@ class GDNCore:
 
     def prefill(self, x, w_conv, a, b, A_log, dt_bias, z, w_norm, cu_seqlens, cache, slot_in,
                 slot_out=None, layer=0):
-        """step() for long pieces (faster from about 100 tokens a sequence):
+        """step() for long pieces (faster from 100 to 150 tokens a sequence on):
         the chunked forward from and into slots (contiguous a, b, z as
-        forward(); cu_seqlens[-1] = T; dtypes and head dims of the chunked form).  A slot_in
-        outside the cache gives NaN, a slot_out outside it is not written.
-        Every call has scratch of its own, so that one core may prefill
-        several caches on several streams, and a captured call keeps its."""
+        forward(); cu_seqlens[-1] = T; dtypes and head dims of the chunked form).
+        Slots outside the cache are gathered and scattered as by
+        gdn_cache_copy, unlike step()'s: such a slot_in gives NaN rows and a
+        NaN state, which goes to slot_out (in place that slot is outside as
+        well, and nothing is written); such a slot_out gives the rows and
+        keeps no state.  check_slots in the config finds both.  Every call
+        has scratch of its own, so that one core may prefill several caches on
+        several streams, and a captured call keeps its."""
         c = self.cfg
         n_seq = cu_seqlens.numel() - 1
         slot_out = slot_in if slot_out is None else slot_out

@@ -347,7 +347,8 @@ typedef struct {
 /* The gated delta rule (as gdn_chunk_fwd), token by token:
  *   S_t = exp(g_t) S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T
  *   o_t = S_t (scale * q_t)
- * in fp32 whatever the storage type, with no limit on the range of the data.
+ * in fp32 whatever the storage type; no operand is 16-bit inside.  S k, S q and
+ * k . q are formed before the gates apply and must be finite in fp32.
  * q, k, v, g, beta and o as gdn_chunk_fwd; every dtype at dk = dv = 32 and 128.
  * For single tokens up to pieces of about 100 tokens a sequence; gdn_chunk_fwd
  * is faster for longer ones (its states go in and out of a cache by
