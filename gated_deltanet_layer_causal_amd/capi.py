@@ -36,7 +36,9 @@ EXPORTS = (
     "gdn_chunk_bwd_states", "gdn_chunk_bwd_reverse", "gdn_chunk_bwd_grads",
     "gdn_check_cu_seqlens", "gdn_recurrent_fwd", "gdn_step_fwd", "gdn_check_slots",
     "gdn_cache_copy", "gdn_cache_fork", "gdn_cache_retain", "gdn_cache_release",
-    "gdn_cache_compact", "gdn_cache_workspace",
+    "gdn_cache_compact", "gdn_cache_workspace", "gdn_add_norm_fwd", "gdn_add_norm_fwd_mx8",
+    "gdn_add_norm_bwd", "gdn_add_norm_bwd_workspace", "gdn_w4_bytes", "gdn_w4_pack",
+    "gdn_w4_arrange", "gdn_w4_unpack", "gdn_w4_fwd", "gdn_w4_fwd_mx8",
 )
 
 
@@ -120,6 +122,20 @@ def load(path: str = LIB_PATH):
     lib.gdn_cache_compact.argtypes = [V, I64, I32, V, V, V, I32, V, c_size_t, V]
     lib.gdn_cache_workspace.argtypes = [I32]
     lib.gdn_cache_workspace.restype = c_size_t
+    lib.gdn_add_norm_fwd.argtypes = [I64, I32, c_int, c_int, V, I64, V, I64, V, F, V, I64, V, I64, V]
+    lib.gdn_add_norm_fwd_mx8.argtypes = [I64, I32, c_int, c_int, V, I64, V, I64, V, F, V, I64, V, I64,
+                                         V, I64, V]
+    lib.gdn_add_norm_bwd.argtypes = [I64, I32, c_int, c_int, V, I64, V, F, V, I64, V, I64, V, I64, V,
+                                     I64, V, V, c_size_t, V]
+    lib.gdn_add_norm_bwd_workspace.argtypes = [I64, I32]
+    lib.gdn_add_norm_bwd_workspace.restype = c_size_t
+    lib.gdn_w4_bytes.argtypes = [I32, I32]
+    lib.gdn_w4_bytes.restype = c_size_t
+    lib.gdn_w4_pack.argtypes = [I32, I32, c_int, V, I64, V, c_size_t, V]
+    lib.gdn_w4_arrange.argtypes = [I32, I32, V, I64, V, I64, V, c_size_t, V]
+    lib.gdn_w4_unpack.argtypes = [I32, I32, V, c_size_t, c_int, V, I64, V]
+    lib.gdn_w4_fwd.argtypes = [I64, I32, I32, c_int, V, I64, V, c_size_t, V, I64, V]
+    lib.gdn_w4_fwd_mx8.argtypes = [I64, I32, I32, V, I64, V, I64, V, c_size_t, c_int, V, I64, V]
     for name in ("gdn_conv_bwd_workspace", "gdn_gate_bwd_workspace", "gdn_chunk_fwd_workspace",
                  "gdn_chunk_bwd_workspace"):
         getattr(lib, name).argtypes = [SP]
@@ -133,7 +149,9 @@ def load(path: str = LIB_PATH):
                  "gdn_chunk_bwd_states", "gdn_chunk_bwd_reverse",
                  "gdn_chunk_bwd_grads", "gdn_check_cu_seqlens", "gdn_recurrent_fwd", "gdn_step_fwd",
                  "gdn_check_slots", "gdn_cache_copy", "gdn_cache_fork", "gdn_cache_retain",
-                 "gdn_cache_release", "gdn_cache_compact"):
+                 "gdn_cache_release", "gdn_cache_compact", "gdn_add_norm_fwd", "gdn_add_norm_fwd_mx8",
+                 "gdn_add_norm_bwd", "gdn_w4_pack", "gdn_w4_arrange", "gdn_w4_unpack", "gdn_w4_fwd",
+                 "gdn_w4_fwd_mx8"):
         getattr(lib, name).restype = c_int
     _lib = lib
     return lib
@@ -879,3 +897,174 @@ def gdn_cache_compact(buf, refs, remap, table, ws, stream=None):
     """Moves the live slots of buf to its front; remap [n_slots] receives
     where each went, and table (int32, or None) is rewritten by it."""
     Slots(buf, refs, ws).compact(remap, table, stream)
+
+
+# ---------------------------------------------------------------- around the core
+def _width(t):
+    """The row stride that goes with _row_ld of a matrix of any width: one row
+    needs none, so its width to the next multiple of 16."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def _wide(name, t, dtype, T, cols, dev):
+    """_rows with the device; the row stride."""
+    _rows(name, t, dtype, T, cols)
+    _on(dev, (name, t))
+    return _width(t)
+
+
+def _mat(t, dtype, shape, index):
+    """Whether t is what _wide wants, in one expression."""
+    return t.dtype is dtype and t.shape == shape and t.stride(1) == 1 and t.get_device() == index
+
+
+_TYPES = {(a, b): (x, y) for a, x in _GDN_DT.items() for b, y in _GDN_DT.items()
+          if b in (a, torch.float32)}
+
+
+def _types(dtype, res_dtype):
+    got = _TYPES.get((dtype, res_dtype))
+    if got is None:
+        raise TypeError(f"rows of {dtype} with a residual stream of {res_dtype}: rows of bf16, fp16 or "
+                        "fp32, their stream in the same type or fp32")
+    return got
+
+
+def _norm_rows(x, res, w, h):
+    """The checks of the residual norm's forward: (T, n, types, ldx, ldr, ldh, index, device)."""
+    if x is None or x.dim() != 2:
+        raise ValueError("x must be a [T, n] matrix")
+    i, dev, shape = x.get_device(), x.device, x.shape
+    T, n = shape
+    rt = res.dtype if res is not None else h.dtype if h is not None else x.dtype
+    types = _types(x.dtype, rt)
+    if not (T > 1 and i >= 0 and n > 1 and x.stride(1) == 1 and
+            (res is None or _mat(res, rt, shape, i)) and (h is None or _mat(h, rt, shape, i)) and
+            _is_flat(w, torch.float32, n, i)):
+        ldx = _wide("x", x, x.dtype, T, n, dev)
+        ldr = 0 if res is None else _wide("res", res, rt, T, n, dev)
+        ldh = 0 if h is None else _wide("h", h, rt, T, n, dev)
+        _need("w", w, torch.float32, n)
+        _on(dev, ("w", w))
+        return T, n, types, ldx, ldr, ldh, i, dev
+    return (T, n, types, x.stride(0), 0 if res is None else res.stride(0),
+            0 if h is None else h.stride(0), i, dev)
+
+
+def gdn_add_norm_fwd(x, res, w, h, y, eps=1e-6, stream=None):
+    """h = x + res (None: h = x), y = h / sqrt(mean h^2 + eps) * (1 + w) over
+    the rows of [T, n] matrices (rows may be strided).  h may be None (not
+    written), res itself, or x of the same type; y may be x."""
+    T, n, (dt, rt), ldx, ldr, ldh, i, dev = _norm_rows(x, res, w, h)
+    ldy = y.stride(0) if T > 1 and _mat(y, x.dtype, x.shape, i) else _wide("y", y, x.dtype, T, n, dev)
+    _run("gdn_add_norm_fwd", i, (
+        T, n, dt, rt, x.data_ptr(), ldx, _ptr(res), ldr, w.data_ptr(), eps, _ptr(h), ldh, y.data_ptr(),
+        ldy, _raw_stream(dev, i, stream)))
+
+
+def gdn_add_norm_fwd_mx8(x, res, w, h, q, scale, eps=1e-6, stream=None):
+    """gdn_add_norm_fwd with y in 8 bits: q float8_e4m3fn [T, n] under a power
+    of two for each 32 columns, scale uint8 [T, n / 32] (2^(byte - 127))."""
+    T, n, (dt, rt), ldx, ldr, ldh, i, dev = _norm_rows(x, res, w, h)
+    ldq = _wide("q", q, torch.float8_e4m3fn, T, n, dev)
+    lds = _wide("scale", scale, torch.uint8, T, n // 32, dev)
+    _run("gdn_add_norm_fwd_mx8", i, (
+        T, n, dt, rt, x.data_ptr(), ldx, _ptr(res), ldr, w.data_ptr(), eps, _ptr(h), ldh, q.data_ptr(),
+        ldq, scale.data_ptr(), lds, _raw_stream(dev, i, stream)))
+
+
+def gdn_add_norm_bwd_workspace(rows, n):
+    return int(load().gdn_add_norm_bwd_workspace(rows, n))
+
+
+def gdn_add_norm_bwd(h, w, dy, dh, dx, dres, dw, ws, eps=1e-6, stream=None):
+    """The backward, from the forward's h: dy [T, n] in the rows' type, dh (or
+    None) in h's -> dx in dy's type, dres in h's, dw fp32 [n] (each may be
+    None; ws is needed for dw only).  dres may be dh, dx may be dy."""
+    if h is None or dy is None or h.dim() != 2:
+        raise ValueError("h and dy must be [T, n] matrices")
+    T, n = h.shape
+    i, dev, rt, xt = h.get_device(), h.device, h.dtype, dy.dtype
+    dt, rdt = _types(xt, rt)
+    ld = [_wide(nm, t, to, T, n, dev) if t is not None else 0 for nm, t, to in (
+        ("h", h, rt), ("dy", dy, xt), ("dh", dh, rt), ("dx", dx, xt), ("dres", dres, rt))]
+    _need("w", w, torch.float32, n)
+    _need("dw", dw, torch.float32, n, optional=True)
+    _ws(ws)
+    _on(dev, ("w", w), ("dw", dw), ("workspace", ws))
+    _run("gdn_add_norm_bwd", i, (
+        T, n, dt, rdt, h.data_ptr(), ld[0], w.data_ptr(), eps, dy.data_ptr(), ld[1], _ptr(dh), ld[2],
+        _ptr(dx), ld[3], _ptr(dres), ld[4], _ptr(dw), _ptr(ws), 0 if ws is None else ws.numel(),
+        _raw_stream(dev, i, stream)))
+
+
+def gdn_w4_bytes(n, k):
+    return int(load().gdn_w4_bytes(n, k))
+
+
+class W4:
+    """Packed 4-bit weights of n outputs and k inputs, checked once and kept."""
+
+    def __init__(self, packed, n, k):
+        need = gdn_w4_bytes(n, k)
+        if need == 0:
+            raise ValueError(f"no 4-bit weights of {n} outputs and {k} inputs: inputs come in groups of 32")
+        if packed.dtype != torch.uint8 or not packed.is_contiguous() or packed.numel() < need:
+            raise ValueError(f"the packed weights must be a contiguous uint8 tensor of {need} bytes")
+        self.packed, self.n, self.k = packed, n, k
+        self.device, self.index = packed.device, packed.get_device()
+        self.args = packed.data_ptr(), packed.numel()
+
+
+def gdn_w4_pack(weight, w4, stream=None):
+    """weight [n, k] in a storage type (rows may be strided) into w4."""
+    if weight.dtype not in _GDN_DT:
+        raise TypeError(f"unsupported dtype {weight.dtype}")
+    ld = _wide("weight", weight, weight.dtype, w4.n, w4.k, w4.device)
+    _run("gdn_w4_pack", w4.index, (w4.n, w4.k, _GDN_DT[weight.dtype], weight.data_ptr(), ld, *w4.args,
+                                   _raw_stream(w4.device, w4.index, stream)))
+
+
+def gdn_w4_arrange(codes, scales, w4, stream=None):
+    """codes uint8 [n, k / 2] (input 2j in the low four bits of byte j) and
+    scales uint8 [n, k / 32] (2^(byte - 127)) into w4."""
+    ldc = _wide("codes", codes, torch.uint8, w4.n, w4.k // 2, w4.device)
+    lds = _wide("scales", scales, torch.uint8, w4.n, w4.k // 32, w4.device)
+    _run("gdn_w4_arrange", w4.index, (w4.n, w4.k, codes.data_ptr(), ldc, scales.data_ptr(), lds, *w4.args,
+                                      _raw_stream(w4.device, w4.index, stream)))
+
+
+def gdn_w4_unpack(w4, weight, stream=None):
+    """The values of w4 into weight [n, k], in its storage type."""
+    if weight.dtype not in _GDN_DT:
+        raise TypeError(f"unsupported dtype {weight.dtype}")
+    ld = _wide("weight", weight, weight.dtype, w4.n, w4.k, w4.device)
+    _run("gdn_w4_unpack", w4.index, (w4.n, w4.k, *w4.args, _GDN_DT[weight.dtype], weight.data_ptr(), ld,
+                                     _raw_stream(w4.device, w4.index, stream)))
+
+
+def gdn_w4_fwd(x, w4, y, stream=None):
+    """y [T, n] = x [T, k] W^T in x's storage type, rows may be strided."""
+    i, dt, T = w4.index, x.dtype, x.shape[0]
+    if T > 1 and dt in _GDN_DT and _mat(x, dt, (T, w4.k), i) and _mat(y, dt, (T, w4.n), i):
+        ldx, ldy = x.stride(0), y.stride(0)
+    else:
+        if dt not in _GDN_DT:
+            raise TypeError(f"unsupported dtype {dt}")
+        ldx = _wide("x", x, dt, T, w4.k, w4.device)
+        ldy = _wide("y", y, dt, T, w4.n, w4.device)
+    _run("gdn_w4_fwd", i, (T, w4.n, w4.k, _GDN_DT[dt], x.data_ptr(), ldx, *w4.args, y.data_ptr(), ldy,
+                           _raw_stream(w4.device, i, stream)))
+
+
+def gdn_w4_fwd_mx8(q, scale, w4, y, stream=None):
+    """gdn_w4_fwd for rows in 8 bits as gdn_add_norm_fwd_mx8 writes them; y in
+    any storage type."""
+    i, dt, T = w4.index, y.dtype, q.shape[0]
+    if dt not in _GDN_DT:
+        raise TypeError(f"unsupported dtype {dt}")
+    ldq = _wide("q", q, torch.float8_e4m3fn, T, w4.k, w4.device)
+    lds = _wide("scale", scale, torch.uint8, T, w4.k // 32, w4.device)
+    ldy = _wide("y", y, dt, T, w4.n, w4.device)
+    _run("gdn_w4_fwd_mx8", i, (T, w4.n, w4.k, q.data_ptr(), ldq, scale.data_ptr(), lds, *w4.args,
+                               _GDN_DT[dt], y.data_ptr(), ldy, _raw_stream(w4.device, i, stream)))

@@ -508,4 +508,157 @@ gdn_status gdn_cache_compact(void* base, int64_t stride, int32_t n_slots, int32_
                                        (hipStream_t)stream));
 }
 
+// ---------------------------------------------------------------- around the core
+static gdn_status add_norm_shape(int64_t rows, int32_t n, gdn_dtype dtype, gdn_dtype res_dtype, float eps) {
+  if (rows < 0 || n < 1 || !dtype_ok(dtype) || !dtype_ok(res_dtype) || !(eps >= 0.f))
+    return GDN_ERR_INVALID_ARG;
+  if (res_dtype != dtype && res_dtype != GDN_FP32) return GDN_ERR_UNSUPPORTED;
+  if (n % 8 || n > ADD_NORM_MAX) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+// a matrix of rows that may be absent
+static gdn_status check_rows(const void* p, int64_t ld, int64_t cols) {
+  if (!p) return GDN_OK;
+  if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
+  return check_ld(ld, cols);
+}
+
+static gdn_status add_norm_fwd(int64_t rows, int32_t n, gdn_dtype dtype, gdn_dtype res_dtype, const void* x,
+                               int64_t ldx, const void* res, int64_t ldr, const float* w, float eps, void* h,
+                               int64_t ldh, void* y, int64_t ldy, uint8_t* scale, int64_t lds, void* stream) {
+  GDN_TRY(add_norm_shape(rows, n, dtype, res_dtype, eps));
+  GDN_TRY(check_ptrs({w}));
+  if (rows == 0) return GDN_OK;
+  GDN_TRY(check_ptrs({x, y}));
+  GDN_TRY(check_ld(ldx, n));
+  GDN_TRY(check_rows(res, ldr, n));
+  GDN_TRY(check_rows(h, ldh, n));
+  GDN_TRY(check_ld(ldy, n));
+  AddNormArgs a = {};
+  a.rows = rows; a.n = n; a.dtype = dtype; a.res_dtype = res_dtype; a.x = x; a.res = res; a.w = w;
+  a.eps = eps; a.h = h; a.y = y; a.scale = scale; a.ldx = ldx; a.ldr = ldr; a.ldh = ldh; a.ldy = ldy;
+  a.lds = lds;
+  return launched(launch_add_norm_fwd(a, (hipStream_t)stream));
+}
+
+gdn_status gdn_add_norm_fwd(int64_t rows, int32_t n, gdn_dtype dtype, gdn_dtype res_dtype, const void* x,
+                            int64_t ldx, const void* res, int64_t ldr, const float* w, float eps, void* h,
+                            int64_t ldh, void* y, int64_t ldy, void* stream) {
+  return add_norm_fwd(rows, n, dtype, res_dtype, x, ldx, res, ldr, w, eps, h, ldh, y, ldy, nullptr, 0, stream);
+}
+
+gdn_status gdn_add_norm_fwd_mx8(int64_t rows, int32_t n, gdn_dtype dtype, gdn_dtype res_dtype, const void* x,
+                                int64_t ldx, const void* res, int64_t ldr, const float* w, float eps, void* h,
+                                int64_t ldh, void* q, int64_t ldq, uint8_t* scale, int64_t lds, void* stream) {
+  GDN_TRY(add_norm_shape(rows, n, dtype, res_dtype, eps));
+  if (n % 32) return GDN_ERR_UNSUPPORTED;
+  if (rows > 0 && (!scale || lds < n / 32)) return GDN_ERR_INVALID_ARG;
+  if (rows > 0 && ldq % 16) return GDN_ERR_ALIGNMENT;
+  return add_norm_fwd(rows, n, dtype, res_dtype, x, ldx, res, ldr, w, eps, h, ldh, q, ldq, scale, lds, stream);
+}
+
+size_t gdn_add_norm_bwd_workspace(int64_t rows, int32_t n) {
+  if (rows < 0 || n < 1 || n > ADD_NORM_MAX) return 0;
+  return sizeof(float) * (size_t)add_norm_blocks(rows, n) * (size_t)n;
+}
+
+gdn_status gdn_add_norm_bwd(int64_t rows, int32_t n, gdn_dtype dtype, gdn_dtype res_dtype, const void* h,
+                            int64_t ldh, const float* w, float eps, const void* dy, int64_t lddy, const void* dh,
+                            int64_t lddh, void* dx, int64_t lddx, void* dres, int64_t lddr, float* dw, void* ws,
+                            size_t ws_bytes, void* stream) {
+  GDN_TRY(add_norm_shape(rows, n, dtype, res_dtype, eps));
+  GDN_TRY(check_ptrs({w}));
+  if (rows > 0) {
+    GDN_TRY(check_ptrs({h, dy}));
+    if (!dx && !dres && !dw) return GDN_ERR_INVALID_ARG;
+    GDN_TRY(check_ld(ldh, n));
+    GDN_TRY(check_ld(lddy, n));
+    GDN_TRY(check_rows(dh, lddh, n));
+    GDN_TRY(check_rows(dx, lddx, n));
+    GDN_TRY(check_rows(dres, lddr, n));
+  }
+  if (dw && !aligned16(dw)) return GDN_ERR_ALIGNMENT;
+  const size_t need = dw ? gdn_add_norm_bwd_workspace(rows, n) : 0;
+  if (need && (!ws || ws_bytes < need || !aligned16(ws))) return GDN_ERR_WORKSPACE;
+  AddNormBwdArgs a = {};
+  a.rows = rows; a.n = n; a.dtype = dtype; a.res_dtype = res_dtype; a.h = h; a.dy = dy; a.dh = dh; a.w = w;
+  a.eps = eps; a.dx = dx; a.dres = dres; a.dw = dw; a.partials = dw ? (float*)ws : nullptr;
+  a.ldh = ldh; a.lddy = lddy; a.lddh = lddh; a.lddx = lddx; a.lddr = lddr;
+  return launched(launch_add_norm_bwd(a, (hipStream_t)stream));
+}
+
+static gdn_status check_w4(int32_t n, int32_t k) {
+  if (n < 1 || k < 1) return GDN_ERR_INVALID_ARG;
+  // groups of 32 inputs; at most 2^26 tiles of 16 x 512 weights
+  if (k % 32 || n > (1 << 22) || k > (1 << 20) || (int64_t)((n + 15) / 16) * ((k + 511) / 512) >= (1LL << 26))
+    return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+static gdn_status check_packed(int32_t n, int32_t k, const void* packed, size_t bytes) {
+  GDN_TRY(check_w4(n, k));
+  GDN_TRY(check_ptrs({packed}));
+  return bytes < w4_bytes(n, k) ? GDN_ERR_INVALID_ARG : GDN_OK;
+}
+
+size_t gdn_w4_bytes(int32_t n, int32_t k) { return check_w4(n, k) == GDN_OK ? w4_bytes(n, k) : 0; }
+
+gdn_status gdn_w4_pack(int32_t n, int32_t k, gdn_dtype dtype, const void* w, int64_t ldw, void* packed,
+                       size_t bytes, void* stream) {
+  if (!dtype_ok(dtype)) return GDN_ERR_INVALID_ARG;
+  GDN_TRY(check_packed(n, k, packed, bytes));
+  GDN_TRY(check_ptrs({w}));
+  GDN_TRY(check_ld(ldw, k));
+  return launched(launch_w4_pack(dtype, w, ldw, n, k, packed, (hipStream_t)stream));
+}
+
+gdn_status gdn_w4_arrange(int32_t n, int32_t k, const uint8_t* codes, int64_t ldc, const uint8_t* scales,
+                          int64_t lds, void* packed, size_t bytes, void* stream) {
+  GDN_TRY(check_packed(n, k, packed, bytes));
+  GDN_TRY(check_ptrs({codes}));
+  if (!scales || ldc < k / 2 || lds < k / 32) return GDN_ERR_INVALID_ARG;
+  if (ldc % 16) return GDN_ERR_ALIGNMENT;
+  return launched(launch_w4_arrange(codes, ldc, scales, lds, n, k, packed, (hipStream_t)stream));
+}
+
+gdn_status gdn_w4_unpack(int32_t n, int32_t k, const void* packed, size_t bytes, gdn_dtype dtype, void* w,
+                         int64_t ldw, void* stream) {
+  if (!dtype_ok(dtype)) return GDN_ERR_INVALID_ARG;
+  GDN_TRY(check_packed(n, k, packed, bytes));
+  GDN_TRY(check_ptrs({w}));
+  GDN_TRY(check_ld(ldw, k));
+  return launched(launch_w4_unpack(dtype, packed, n, k, w, ldw, (hipStream_t)stream));
+}
+
+gdn_status gdn_w4_fwd(int64_t rows, int32_t n, int32_t k, gdn_dtype dtype, const void* x, int64_t ldx,
+                      const void* packed, size_t bytes, void* y, int64_t ldy, void* stream) {
+  if (rows < 0 || !dtype_ok(dtype)) return GDN_ERR_INVALID_ARG;
+  GDN_TRY(check_packed(n, k, packed, bytes));
+  if (rows == 0) return GDN_OK;
+  GDN_TRY(check_ptrs({x, y}));
+  GDN_TRY(check_ld(ldx, k));
+  GDN_TRY(check_ld(ldy, n));
+  W4Args a = {};
+  a.rows = rows; a.n = n; a.k = k; a.x = x; a.ldx = ldx; a.packed = packed;
+  a.scales_at = w4_scales_at(n, k); a.y = y; a.ldy = ldy;
+  return launched(launch_w4(a, dtype, (hipStream_t)stream));
+}
+
+gdn_status gdn_w4_fwd_mx8(int64_t rows, int32_t n, int32_t k, const void* q, int64_t ldq, const uint8_t* scale,
+                          int64_t lds, const void* packed, size_t bytes, gdn_dtype dtype, void* y, int64_t ldy,
+                          void* stream) {
+  if (rows < 0 || !dtype_ok(dtype)) return GDN_ERR_INVALID_ARG;
+  GDN_TRY(check_packed(n, k, packed, bytes));
+  if (rows == 0) return GDN_OK;
+  GDN_TRY(check_ptrs({q, y}));
+  if (!scale || ldq < k || lds < k / 32) return GDN_ERR_INVALID_ARG;
+  if (ldq % 16) return GDN_ERR_ALIGNMENT;
+  GDN_TRY(check_ld(ldy, n));
+  W4Args a = {};
+  a.rows = rows; a.n = n; a.k = k; a.x = q; a.ldx = ldq; a.xs = scale; a.ldxs = lds; a.packed = packed;
+  a.scales_at = w4_scales_at(n, k); a.y = y; a.ldy = ldy;
+  return launched(launch_w4(a, dtype, (hipStream_t)stream));
+}
+
 }  // extern "C"

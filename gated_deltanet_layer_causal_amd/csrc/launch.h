@@ -153,4 +153,53 @@ hipError_t launch_cache_compact(void* base, int64_t stride, int32_t n_slots, int
                                 int32_t* remap, int32_t* table, int32_t n_table, void* ws,
                                 hipStream_t st);
 
+// The residual norm (add_norm.hip).  scale != NULL: y in e4m3 with scales.
+struct AddNormArgs {
+  int64_t rows;
+  int n;
+  gdn_dtype dtype, res_dtype;
+  const void *x, *res;
+  const float* w;
+  float eps;
+  void *h, *y;
+  uint8_t* scale;
+  int64_t ldx, ldr, ldh, ldy, lds;
+};
+struct AddNormBwdArgs {
+  int64_t rows;
+  int n;
+  gdn_dtype dtype, res_dtype;
+  const void *h, *dy, *dh;
+  const float* w;
+  float eps;
+  void *dx, *dres;
+  float *dw, *partials;                          // partials: NULL where dw is
+  int64_t ldh, lddy, lddh, lddx, lddr;
+};
+constexpr int ADD_NORM_MAX = 16384;              // widest row
+constexpr int ADD_NORM_WAVE = 2560;              // widest row that one wave holds
+constexpr int64_t ADD_NORM_BLOCKS_MAX = 1024;    // blocks of the backward, each with partial sums of dw
+int64_t add_norm_blocks(int64_t rows, int32_t n);
+hipError_t launch_add_norm_fwd(const AddNormArgs& a, hipStream_t st);
+hipError_t launch_add_norm_bwd(const AddNormBwdArgs& a, hipStream_t st);
+
+// 4-bit weights (w4.hip).  xs != NULL: rows in e4m3 with scales, y in dt.
+struct W4Args {
+  int64_t rows;
+  int n, k;
+  const void* x;
+  const uint8_t* xs;
+  const void* packed;
+  int64_t scales_at;
+  void* y;
+  int64_t ldx, ldxs, ldy;
+};
+size_t w4_bytes(int n, int k);
+int64_t w4_scales_at(int n, int k);
+hipError_t launch_w4(const W4Args& a, gdn_dtype dt, hipStream_t st);
+hipError_t launch_w4_pack(gdn_dtype dt, const void* w, int64_t ldw, int n, int k, void* packed, hipStream_t st);
+hipError_t launch_w4_arrange(const void* codes, int64_t ldc, const void* scales, int64_t lds, int n, int k,
+                             void* packed, hipStream_t st);
+hipError_t launch_w4_unpack(gdn_dtype dt, const void* packed, int n, int k, void* w, int64_t ldw, hipStream_t st);
+
 }  // namespace gdn

@@ -1,0 +1,323 @@
+// Products of few rows with weights of 4 bits: y[t][n] = sum_k x[t][k] W[n][k],
+// W[n][k] = e2m1(code) * 2^(byte - 127) with a byte for each 32 inputs.
+//
+// Packed weights.  A tile is 16 outputs (lane % 16) by 512 inputs; its 16
+// blocks of 32 inputs are numbered b = 4 q + t, q = lane / 16.  Codes of a tile
+// are [t][lane][16 bytes], its scales [lane][t]: one load of 1 KB a wave for a
+// t, in the operand order of the matrix instructions, and one word a lane for
+// the four scales.  Outputs and inputs beyond the matrix have codes of 0.
+#include "common.h"
+#include "launch.h"
+
+namespace gdn {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int W4_TILE = 16 * 512 / 2;        // code bytes of a tile
+__host__ __device__ inline int w4_ktiles(int k) { return (k + 511) / 512; }
+
+// e8m0 as a float for the conversions, which read its exponent only: 0 is
+// 2^-127, 255 NaN.
+__device__ __forceinline__ float scale_f(uint32_t byte) {
+  return __uint_as_float(byte << 23 | 0x00400000u);
+}
+
+// Eight codes as bf16 (exact: two significant bits).
+__device__ __forceinline__ bf16x8 codes8(uint32_t w, float s) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Eight row values as TERMS bf16 each, whose sum they are: one for bf16, two
+// for fp16 (11 bits in 8 + 8), three for fp32 (24 bits).
+template <typename T> struct Split;
+template <> struct Split<bf16> { static constexpr int TERMS = 1; };
+template <> struct Split<fp16> { static constexpr int TERMS = 2; };
+template <> struct Split<float> { static constexpr int TERMS = 3; };
+template <typename T> __device__ __forceinline__ void split8(const T* p, bf16x8 (&out)[Split<T>::TERMS]) {
+  if constexpr (__is_same(T, bf16)) {
+    out[0] = *reinterpret_cast<const bf16x8*>(p);
+  } else {
+    f8 v = load8(p);
+#pragma unroll
+    for (int t = 0; t < Split<T>::TERMS; ++t)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bf16 hi = (bf16)v.v[j];
+        out[t][j] = hi;
+        // what is not finite stays in the first term
+        v.v[j] = __builtin_isfinite((float)hi) ? v.v[j] - (float)hi : 0.f;
+      }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void put4(T* y, int64_t n, int64_t n_all, floatx4 v) {
+  if (n + 4 <= n_all) {
+    store4(y + n, v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < n_all) y[n + i] = from_f<T>(v[i]);
+  }
+}
+
+// One wave: 16 outputs, 16 rows.  The weights are the A operand, so that a
+// lane ends with four adjacent outputs of a row.
+template <typename T>
+__global__ void __launch_bounds__(64) w4_kernel(W4Args a) {
+  const int lane = threadIdx.x, q = lane >> 4, r = lane & 15;
+  const int kt = w4_ktiles(a.k);
+  const int64_t nt = blockIdx.x;
+  const uint4* codes = (const uint4*)a.packed + nt * kt * (W4_TILE / 16) + lane;
+  const uint32_t* scales = (const uint32_t*)((const uint8_t*)a.packed + a.scales_at) + nt * kt * 64 + lane;
+  for (int64_t m0 = (int64_t)blockIdx.y * 16; m0 < a.rows; m0 += (int64_t)gridDim.y * 16) {
+    const bool live = m0 + r < a.rows;
+    const T* x = (const T*)a.x + (live ? m0 + r : 0) * a.ldx;
+    floatx4 acc = zero4();
+    for (int s = 0; s < kt; ++s) {
+      const uint32_t sc = scales[s * 64];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint4 w = codes[(s * 4 + t) * 64];
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        const float f = scale_f(sc >> (8 * t) & 255);
+        const int k = s * 512 + (4 * q + t) * 32;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          bf16x8 b[Split<T>::TERMS];
+          if (live && k < a.k) {
+            split8(x + k + 8 * d, b);
+          } else {
+#pragma unroll
+            for (int u = 0; u < Split<T>::TERMS; ++u) b[u] = bf16x8{0, 0, 0, 0, 0, 0, 0, 0};
+          }
+          const bf16x8 av = codes8(ws[d], f);
+#pragma unroll
+          for (int u = 0; u < Split<T>::TERMS; ++u)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, b[u], acc, 0, 0, 0);
+        }
+      }
+    }
+    if (live) put4((T*)a.y + (m0 + r) * a.ldy, nt * 16 + 4 * q, a.n, acc);
+  }
+}
+
+// The same for rows in e4m3 with a scale for each 32 columns: the scaled
+// matrix instruction takes codes, values and scales as they are.  Its 8-bit
+// operand holds in lane group q the columns 16 q .. 16 q + 15 and 64 + 16 q ..
+// of 128, the scale of lane group q is that of columns 32 q .. 32 q + 31.
+template <typename T>
+__global__ void __launch_bounds__(64) w4_mx8_kernel(W4Args a) {
+  const int lane = threadIdx.x, q = lane >> 4, r = lane & 15;
+  const int kt = w4_ktiles(a.k);
+  const int64_t nt = blockIdx.x;
+  const uint4* codes = (const uint4*)a.packed + nt * kt * (W4_TILE / 16) + lane;
+  const uint32_t* scales = (const uint32_t*)((const uint8_t*)a.packed + a.scales_at) + nt * kt * 64 + lane;
+  for (int64_t m0 = (int64_t)blockIdx.y * 16; m0 < a.rows; m0 += (int64_t)gridDim.y * 16) {
+    const bool live = m0 + r < a.rows;
+    const uint8_t* x = (const uint8_t*)a.x + (live ? m0 + r : 0) * a.ldx;
+    const uint8_t* xs = a.xs + (live ? m0 + r : 0) * a.ldxs;
+    floatx4 acc = zero4();
+    for (int s = 0; s < kt; ++s) {
+      const int sc = (int)scales[s * 64];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint4 w = codes[(s * 4 + t) * 64];
+        const v8i av = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+        int sx = 127;
+        const int k0 = s * 512 + (4 * (q >> 1) + t) * 32, k1 = k0 + 256, ks = s * 16 + 4 * q + t;
+        if (live && k0 < a.k) lo = *(const uint4*)(x + k0 + 16 * (q & 1));
+        if (live && k1 < a.k) hi = *(const uint4*)(x + k1 + 16 * (q & 1));
+        if (live && ks * 32 < a.k) sx = xs[ks];
+        const v8i bv = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+        switch (t) {
+          case 0: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 0, 0, sc, 0, sx); break;
+          case 1: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 0, 1, sc, 0, sx); break;
+          case 2: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 0, 2, sc, 0, sx); break;
+          default: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 0, 3, sc, 0, sx);
+        }
+      }
+    }
+    if (live) put4((T*)a.y + (m0 + r) * a.ldy, nt * 16 + 4 * q, a.n, acc);
+  }
+}
+
+// ---------------------------------------------------------------- packing
+// e2m1 code (no sign) of a >= 0, ties to the even code; 7 (6.0) from 5 on.
+__device__ __forceinline__ int e2m1(float a) {
+  const float c = a < 2.f ? rintf(2.f * a) : a < 4.f ? 4.f + rintf(a - 2.f) : 6.f + rintf(0.5f * a - 2.f);
+  return (int)fminf(c, 7.f);
+}
+__device__ __forceinline__ float e2m1_value(int c) {
+  return c < 4 ? 0.5f * c : c < 6 ? c - 2.f : 2.f * c - 8.f;
+}
+
+// One wave a tile; a lane takes the four blocks 4 q .. 4 q + 3 of its output:
+// 128 adjacent inputs.  Of the smallest scale that keeps a block within 6 =
+// 0.75 * 2^3 and the next smaller one, which cuts its largest to 6, the one
+// with the smaller squared error (sums in 64 bits, so that near ties do not
+// hang on the order of the sum; the larger scale on a tie).
+template <typename T>
+__global__ void __launch_bounds__(256) w4_pack_kernel(const T* w, int64_t ldw, int n, int k, int64_t tiles,
+                                                      uint8_t* packed, int64_t scales_at) {
+  const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+  const int kt = w4_ktiles(k);
+  const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (tile >= tiles) return;
+  const int64_t row = tile / kt * 16 + r;
+  const int k0 = (int)(tile % kt) * 512 + q * 128;
+  uint32_t sc = 0;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    uint32_t code[4] = {0, 0, 0, 0};
+    if (row < n && k0 + 32 * t < k) {
+      f8 v[4];
+      float amax = 0.f;
+      bool finite = true;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        v[d] = load8(w + row * ldw + k0 + 32 * t + 8 * d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          amax = fmaxf(amax, fabsf(v[d].v[j]));
+          finite &= __builtin_isfinite(v[d].v[j]);
+        }
+      }
+      int e = __builtin_amdgcn_frexp_expf(amax) - 3 + (__builtin_amdgcn_frexp_mantf(amax) > 0.75f);
+      e = amax == 0.f || e < -127 ? -127 : e > 125 ? 125 : e;    // 6 * 2^125 is finite, 4 * 2^126 is not
+      double wide = 0, fine = 0;       // squared errors, in units of 4^e and 4^(e - 1)
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float a = ldexpf(fabsf(v[d].v[j]), -e);
+          const double x = (double)a - e2m1_value(e2m1(a)), y = (double)(2.f * a) - e2m1_value(e2m1(2.f * a));
+          wide += x * x;
+          fine += y * y;
+        }
+      if (e > -127 && fine < 4 * wide) --e;
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float a = ldexpf(fabsf(v[d].v[j]), -e);
+          code[d] |= (uint32_t)(e2m1(a) | (v[d].v[j] < 0.f ? 8 : 0)) << (4 * j);
+        }
+      if (!finite) e = 128;
+      if (!finite) code[0] = code[1] = code[2] = code[3] = 0;
+      sc |= (uint32_t)(e + 127) << (8 * t);
+    }
+    ((uint4*)packed)[(tile * 4 + t) * 64 + lane] = make_uint4(code[0], code[1], code[2], code[3]);
+  }
+  ((uint32_t*)(packed + scales_at))[tile * 64 + lane] = sc;
+}
+
+// Codes [n][k/2] and scales [n][k/32] into the packed order.
+__global__ void __launch_bounds__(256) w4_arrange_kernel(const uint8_t* codes, int64_t ldc, const uint8_t* scales,
+                                                         int64_t lds, int n, int k, int64_t tiles, uint8_t* packed,
+                                                         int64_t scales_at) {
+  const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+  const int kt = w4_ktiles(k);
+  const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (tile >= tiles) return;
+  const int64_t row = tile / kt * 16 + r;
+  const int k0 = (int)(tile % kt) * 512 + q * 128;
+  uint32_t sc = 0;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    uint4 c = make_uint4(0, 0, 0, 0);
+    if (row < n && k0 + 32 * t < k) {
+      c = *(const uint4*)(codes + row * ldc + (k0 + 32 * t) / 2);
+      sc |= (uint32_t)scales[row * lds + (k0 + 32 * t) / 32] << (8 * t);
+    }
+    ((uint4*)packed)[(tile * 4 + t) * 64 + lane] = c;
+  }
+  ((uint32_t*)(packed + scales_at))[tile * 64 + lane] = sc;
+}
+
+// Packed weights into dense rows of a storage type.
+template <typename T>
+__global__ void __launch_bounds__(256) w4_unpack_kernel(const uint8_t* packed, int64_t scales_at, int n, int k,
+                                                        int64_t tiles, T* w, int64_t ldw) {
+  const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+  const int kt = w4_ktiles(k);
+  const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (tile >= tiles) return;
+  const int64_t row = tile / kt * 16 + r;
+  const int k0 = (int)(tile % kt) * 512 + q * 128;
+  const uint32_t sc = ((const uint32_t*)(packed + scales_at))[tile * 64 + lane];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    if (row < n && k0 + 32 * t < k) {
+      const uint4 c = ((const uint4*)packed)[(tile * 4 + t) * 64 + lane];
+      const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
+      const int b = (int)(sc >> (8 * t) & 255);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        f8 v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int code = (int)(cs[d] >> (4 * j) & 15);
+          const float m = ldexpf(e2m1_value(code & 7), b - 127);
+          v.v[j] = b == 255 ? __builtin_nanf("") : code & 8 ? -m : m;
+        }
+        store8(w + row * ldw + k0 + 32 * t + 8 * d, v);
+      }
+    }
+  }
+}
+
+static int64_t w4_tiles(int n, int k) { return (int64_t)((n + 15) / 16) * w4_ktiles(k); }
+size_t w4_bytes(int n, int k) { return (size_t)w4_tiles(n, k) * (W4_TILE + 256); }
+int64_t w4_scales_at(int n, int k) { return w4_tiles(n, k) * W4_TILE; }
+
+hipError_t launch_w4(const W4Args& a, gdn_dtype dt, hipStream_t st) {
+  if (a.rows == 0) return hipSuccess;
+  const int64_t mb = (a.rows + 15) / 16, nb = (a.n + 15) / 16;
+  const int64_t most = ((int64_t)1 << 25) / nb;      // a launch holds fewer than 2^32 threads
+  const dim3 grid((unsigned)nb, (unsigned)(mb < most ? mb : most < 1 ? 1 : most < 65535 ? most : 65535));
+  auto k = a.xs ? (dt == GDN_BF16 ? w4_mx8_kernel<bf16> : dt == GDN_FP16 ? w4_mx8_kernel<fp16> : w4_mx8_kernel<float>)
+                : (dt == GDN_BF16 ? w4_kernel<bf16> : dt == GDN_FP16 ? w4_kernel<fp16> : w4_kernel<float>);
+  hipLaunchKernelGGL(k, grid, dim3(64), 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_w4_pack(gdn_dtype dt, const void* w, int64_t ldw, int n, int k, void* packed, hipStream_t st) {
+  const int64_t tiles = w4_tiles(n, k), at = w4_scales_at(n, k);
+  const dim3 grid((unsigned)((tiles + 3) / 4));
+  if (dt == GDN_BF16)
+    hipLaunchKernelGGL(w4_pack_kernel<bf16>, grid, dim3(256), 0, st, (const bf16*)w, ldw, n, k, tiles, (uint8_t*)packed, at);
+  else if (dt == GDN_FP16)
+    hipLaunchKernelGGL(w4_pack_kernel<fp16>, grid, dim3(256), 0, st, (const fp16*)w, ldw, n, k, tiles, (uint8_t*)packed, at);
+  else
+    hipLaunchKernelGGL(w4_pack_kernel<float>, grid, dim3(256), 0, st, (const float*)w, ldw, n, k, tiles, (uint8_t*)packed, at);
+  return hipGetLastError();
+}
+
+hipError_t launch_w4_arrange(const void* codes, int64_t ldc, const void* scales, int64_t lds, int n, int k,
+                             void* packed, hipStream_t st) {
+  const int64_t tiles = w4_tiles(n, k);
+  hipLaunchKernelGGL(w4_arrange_kernel, dim3((unsigned)((tiles + 3) / 4)), dim3(256), 0, st, (const uint8_t*)codes, ldc,
+                     (const uint8_t*)scales, lds, n, k, tiles, (uint8_t*)packed, w4_scales_at(n, k));
+  return hipGetLastError();
+}
+
+hipError_t launch_w4_unpack(gdn_dtype dt, const void* packed, int n, int k, void* w, int64_t ldw, hipStream_t st) {
+  const int64_t tiles = w4_tiles(n, k), at = w4_scales_at(n, k);
+  const dim3 grid((unsigned)((tiles + 3) / 4));
+  if (dt == GDN_BF16)
+    hipLaunchKernelGGL(w4_unpack_kernel<bf16>, grid, dim3(256), 0, st, (const uint8_t*)packed, at, n, k, tiles, (bf16*)w, ldw);
+  else if (dt == GDN_FP16)
+    hipLaunchKernelGGL(w4_unpack_kernel<fp16>, grid, dim3(256), 0, st, (const uint8_t*)packed, at, n, k, tiles, (fp16*)w, ldw);
+  else
+    hipLaunchKernelGGL(w4_unpack_kernel<float>, grid, dim3(256), 0, st, (const uint8_t*)packed, at, n, k, tiles, (float*)w, ldw);
+  return hipGetLastError();
+}
+
+}  // namespace gdn

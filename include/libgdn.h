@@ -429,6 +429,96 @@ gdn_status gdn_cache_compact(void* base, int64_t stride, int32_t n_slots, int32_
 /* Workspace of gdn_cache_fork and gdn_cache_compact. */
 size_t gdn_cache_workspace(int32_t n_slots);
 
+/* ---------------------------------------------------------------------------
+ * Around the core in a model's block: the residual's addition with the
+ * zero-centred RMSNorm that precedes a layer (Megatron page,
+ * "--apply-layernorm-1p"), and projections with weights of 4 bits.
+ *
+ * gdn_add_norm_fwd, per row of n columns:
+ *   h = x + res,   y = h / sqrt(mean(h^2) + eps) * (1 + w)
+ * x, y [rows][ld] in dtype; res, h in res_dtype (dtype, or GDN_FP32 for a
+ * residual stream in fp32); w fp32 [n].  res == NULL: h = x.  h == NULL: not
+ * written.  The norm is formed from the sum in fp32, before h is rounded to
+ * res_dtype.  n a multiple of 8, at most 16384; row strides multiples of 8.
+ * Without rows (rows == 0) the tensors of rows may be NULL, in all calls here.
+ * h may be the memory of res, or of x where the types are the same, and y
+ * that of x (same row strides): other overlaps give undefined values.
+ * NaN and infinities stay in their row.  No workspace. */
+gdn_status gdn_add_norm_fwd(int64_t rows, int32_t n, gdn_dtype dtype, gdn_dtype res_dtype,
+                            const void* x, int64_t ldx, const void* res, int64_t ldr,
+                            const float* w, float eps, void* h, int64_t ldh, void* y, int64_t ldy,
+                            void* stream);
+
+/* The same with y in 8 bits: q [rows][ldq] in e4m3 (OCP: 4 bits of exponent,
+ * 3 of fraction, no infinities) with a power-of-two scale for each 32 columns,
+ * scale [rows][lds], bytes that stand for 2^(byte - 127).  Column j of a row
+ * is q[j] * 2^(scale[j / 32] - 127).  A group's scale is the smallest that
+ * keeps its largest magnitude within 448 (a group of zeros has the byte 0);
+ * values round to nearest, ties to even.  NaN stays NaN and is left out of the
+ * largest; infinities become NaN.  n a multiple of 32, ldq of 16; lds >= n / 32.
+ * q and scale may not overlap the other tensors. */
+gdn_status gdn_add_norm_fwd_mx8(int64_t rows, int32_t n, gdn_dtype dtype, gdn_dtype res_dtype,
+                                const void* x, int64_t ldx, const void* res, int64_t ldr,
+                                const float* w, float eps, void* h, int64_t ldh, void* q,
+                                int64_t ldq, uint8_t* scale, int64_t lds, void* stream);
+
+/* Backward, from the h that the forward wrote: with n = h / sqrt(mean(h^2) +
+ * eps) and dn = dy (1 + w),
+ *   d = dh + (dn - n mean(dn n)) / sqrt(mean(h^2) + eps)
+ * is the gradient of x and of res alike, and dw = sum over rows of dy n.
+ * dy [rows][lddy] in dtype; dh (the gradient of h from where the residual
+ * stream goes on; NULL: zero) in res_dtype; d goes to dx in dtype and to dres
+ * in res_dtype (each may be NULL); dw fp32 [n] (NULL: not formed, no
+ * workspace), summed in a fixed order, zero for no rows.  dres may be the
+ * memory of dh, dx that of dy (same row strides). */
+gdn_status gdn_add_norm_bwd(int64_t rows, int32_t n, gdn_dtype dtype, gdn_dtype res_dtype,
+                            const void* h, int64_t ldh, const float* w, float eps, const void* dy,
+                            int64_t lddy, const void* dh, int64_t lddh, void* dx, int64_t lddx,
+                            void* dres, int64_t lddr, float* dw, void* ws, size_t ws_bytes,
+                            void* stream);
+size_t gdn_add_norm_bwd_workspace(int64_t rows, int32_t n);
+
+/* Weights of 4 bits, W [n][k] (n outputs, k inputs): e2m1 values (codes 0 to 7:
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6; 8 to 15 the negative ones) with a power-of-two
+ * scale for each 32 inputs of an output.  They are held packed, in the
+ * library's own order, in gdn_w4_bytes(n, k) bytes (16-byte aligned); k is
+ * padded to a multiple of 512 and n to one of 16 there.  k a multiple of 32, at
+ * most 2^20; n at most 2^22; fewer than 2^26 tiles of 16 x 512 in all.  In every
+ * call below `bytes` is the size of `packed`, at least gdn_w4_bytes(n, k).
+ *
+ * gdn_w4_pack: W [n][ldw] in dtype into 4 bits.  Of the smallest scale that
+ * keeps a group within 6 and the next smaller one (values beyond 6 become 6),
+ * the one with the smaller sum of squared errors; the larger on a tie.  No
+ * scale is above 2^125, so that every value is finite in fp32.  Nearest codes,
+ * ties to even.  A group with a NaN or an infinity becomes NaN.
+ * gdn_w4_arrange: weights that are in 4 bits already, codes [n][ldc] (input 2j
+ * in the low four bits of byte j; 16-byte aligned, ldc a multiple of 16) and
+ * scales [n][lds] (2^(byte - 127); 255: NaN).
+ * gdn_w4_unpack: the values, W [n][ldw] in dtype (exact in bf16 and fp32; in
+ * fp16 within its range). */
+size_t gdn_w4_bytes(int32_t n, int32_t k);
+gdn_status gdn_w4_pack(int32_t n, int32_t k, gdn_dtype dtype, const void* w, int64_t ldw,
+                       void* packed, size_t bytes, void* stream);
+gdn_status gdn_w4_arrange(int32_t n, int32_t k, const uint8_t* codes, int64_t ldc,
+                          const uint8_t* scales, int64_t lds, void* packed, size_t bytes,
+                          void* stream);
+gdn_status gdn_w4_unpack(int32_t n, int32_t k, const void* packed, size_t bytes, gdn_dtype dtype,
+                         void* w, int64_t ldw, void* stream);
+
+/* y[t][j] = sum_i x[t][i] W[j][i], sums in fp32, rounded once.
+ * gdn_w4_fwd: x [rows][ldx] and y [rows][ldy] in dtype; the rows' values are
+ * not rounded (fp16 and fp32 values enter as sums of two or three bf16 ones).
+ * gdn_w4_fwd_mx8: rows as gdn_add_norm_fwd_mx8 writes them (q 16-byte aligned,
+ * ldq a multiple of 16), y in dtype.
+ * For few rows: the time is that of reading W up to a few dozen rows.  Any
+ * number of rows is served. */
+gdn_status gdn_w4_fwd(int64_t rows, int32_t n, int32_t k, gdn_dtype dtype, const void* x,
+                      int64_t ldx, const void* packed, size_t bytes, void* y, int64_t ldy,
+                      void* stream);
+gdn_status gdn_w4_fwd_mx8(int64_t rows, int32_t n, int32_t k, const void* q, int64_t ldq,
+                          const uint8_t* scale, int64_t lds, const void* packed, size_t bytes,
+                          gdn_dtype dtype, void* y, int64_t ldy, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
