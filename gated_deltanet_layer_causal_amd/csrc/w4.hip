@@ -2,10 +2,11 @@
 // W[n][k] = e2m1(code) * 2^(byte - 127) with a byte for each 32 inputs.
 //
 // Packed weights.  A tile is 16 outputs (lane % 16) by 512 inputs; its 16
-// blocks of 32 inputs are numbered b = 4 q + t, q = lane / 16.  Codes of a tile
-// are [t][lane][16 bytes], its scales [lane][t]: one load of 1 KB a wave for a
-// t, in the operand order of the matrix instructions, and one word a lane for
-// the four scales.  Outputs and inputs beyond the matrix have codes of 0.
+// blocks of 32 inputs are numbered 4 t + q, q = lane / 16.  Codes of a tile are
+// [t][lane][16 bytes], its scales [lane][t]: one load of 1 KB a wave for a t, in
+// the operand order of the matrix instructions, and one word a lane for the
+// four scales.  A t is 128 adjacent inputs, so that a load of rows takes 64
+// adjacent bytes of 8-bit rows, and two of 16-bit rows a whole line.  Outputs and inputs beyond the matrix have codes of 0.
 #include "common.h"
 #include "launch.h"
 
@@ -66,85 +67,158 @@ __device__ __forceinline__ void put4(T* y, int64_t n, int64_t n_all, floatx4 v) 
   }
 }
 
-// One wave: 16 outputs, 16 rows.  The weights are the A operand, so that a
-// lane ends with four adjacent outputs of a row.
-template <typename T>
-__global__ void __launch_bounds__(64) w4_kernel(W4Args a) {
-  const int lane = threadIdx.x, q = lane >> 4, r = lane & 15;
-  const int kt = w4_ktiles(a.k);
-  const int64_t nt = blockIdx.x;
-  const uint4* codes = (const uint4*)a.packed + nt * kt * (W4_TILE / 16) + lane;
-  const uint32_t* scales = (const uint32_t*)((const uint8_t*)a.packed + a.scales_at) + nt * kt * 64 + lane;
-  for (int64_t m0 = (int64_t)blockIdx.y * 16; m0 < a.rows; m0 += (int64_t)gridDim.y * 16) {
-    const bool live = m0 + r < a.rows;
-    const T* x = (const T*)a.x + (live ? m0 + r : 0) * a.ldx;
-    floatx4 acc = zero4();
-    for (int s = 0; s < kt; ++s) {
-      const uint32_t sc = scales[s * 64];
+struct Mx8 {};      // rows in e4m3 with a scale for each 32 columns
+
+// What a lane reads of its row for 128 inputs (t of a tile), and the products
+// with a weights' operand.  `mask`: inputs beyond the matrix, which read others
+// of the row, become zero (their weights are, but rows may hold what is not
+// finite).
+template <typename X> struct RowPart {
+  static constexpr int TERMS = Split<X>::TERMS;
+  uint4 raw[4][sizeof(X) / 2];
+  __device__ __forceinline__ void load(const W4Args& a, int64_t row, int s, int t, int q, int) {
+    const int k = s * 512 + (4 * t + q) * 32;
+    const X* p = (const X*)a.x + row * a.ldx + (k < a.k ? k : 0);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint4 w = codes[(s * 4 + t) * 64];
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-        const float f = scale_f(sc >> (8 * t) & 255);
-        const int k = s * 512 + (4 * q + t) * 32;
+    for (int d = 0; d < 4; ++d)
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          bf16x8 b[Split<T>::TERMS];
-          if (live && k < a.k) {
-            split8(x + k + 8 * d, b);
-          } else {
+      for (int i = 0; i < (int)(sizeof(X) / 2); ++i) raw[d][i] = reinterpret_cast<const uint4*>(p + 8 * d)[i];
+  }
+  __device__ __forceinline__ void mask(const W4Args& a, int s, int t, int q) {
+    if (s * 512 + (4 * t + q) * 32 >= a.k)
 #pragma unroll
-            for (int u = 0; u < Split<T>::TERMS; ++u) b[u] = bf16x8{0, 0, 0, 0, 0, 0, 0, 0};
-          }
-          const bf16x8 av = codes8(ws[d], f);
+      for (int d = 0; d < 4; ++d)
 #pragma unroll
-          for (int u = 0; u < Split<T>::TERMS; ++u)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, b[u], acc, 0, 0, 0);
-        }
+        for (int i = 0; i < (int)(sizeof(X) / 2); ++i) raw[d][i] = make_uint4(0, 0, 0, 0);
+  }
+};
+
+template <> struct RowPart<Mx8> {
+  // The instruction's 8-bit operand: lane group q holds columns 16 q .. 16 q +
+  // 15 and 64 + 16 q .. of its 128, the scale of lane group q that of columns
+  // 32 q .. 32 q + 31.
+  uint4 lo, hi;
+  int scale;
+  __device__ __forceinline__ void load(const W4Args& a, int64_t row, int s, int t, int q, int) {
+    const uint8_t* p = (const uint8_t*)a.x + row * a.ldx + 16 * (q & 1);
+    const int k0 = s * 512 + (4 * t + (q >> 1)) * 32, k1 = k0 + 64, b = s * 16 + 4 * t + q;
+    lo = *reinterpret_cast<const uint4*>(p + (k0 < a.k ? k0 : 0));
+    hi = *reinterpret_cast<const uint4*>(p + (k1 < a.k ? k1 : 0));
+    scale = a.xs[row * a.ldxs + (b * 32 < a.k ? b : 0)];
+  }
+  __device__ __forceinline__ void mask(const W4Args& a, int s, int t, int q) {
+    const int k0 = s * 512 + (4 * t + (q >> 1)) * 32, b = s * 16 + 4 * t + q;
+    if (k0 >= a.k) lo = make_uint4(0, 0, 0, 0);
+    if (k0 + 64 >= a.k) hi = make_uint4(0, 0, 0, 0);
+    if (b * 32 >= a.k) scale = 127;
+  }
+};
+
+template <int T>
+__device__ __forceinline__ floatx4 mx_mma(const uint4& w, int sc, const RowPart<Mx8>& x, floatx4 acc) {
+  const v8i av = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+  const v8i bv = {(int)x.lo.x, (int)x.lo.y, (int)x.lo.z, (int)x.lo.w,
+                  (int)x.hi.x, (int)x.hi.y, (int)x.hi.z, (int)x.hi.w};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 0, T, sc, 0, x.scale);
+}
+
+// acc[n][m] += the weights' tiles n by the rows' tiles m over 128 inputs
+template <int T, typename X, int NT, int MT>
+__device__ __forceinline__ void products(const uint4 (&w)[NT], const uint32_t (&sc)[NT], const RowPart<X> (&x)[MT],
+                                         floatx4 (&acc)[NT][MT]) {
+  if constexpr (__is_same(X, Mx8)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[n][m] = mx_mma<T>(w[n], (int)sc[n], x[m], acc[n][m]);
+  } else {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      constexpr int TERMS = Split<X>::TERMS;
+      bf16x8 b[MT][TERMS];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) split8(reinterpret_cast<const X*>(&x[m].raw[d][0]), b[m]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t ws[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+        const bf16x8 av = codes8(ws[d], scale_f(sc[n] >> (8 * T) & 255));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int u = 0; u < TERMS; ++u)
+            acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, b[m][u], acc[n][m], 0, 0, 0);
       }
     }
-    if (live) put4((T*)a.y + (m0 + r) * a.ldy, nt * 16 + 4 * q, a.n, acc);
   }
 }
 
-// The same for rows in e4m3 with a scale for each 32 columns: the scaled
-// matrix instruction takes codes, values and scales as they are.  Its 8-bit
-// operand holds in lane group q the columns 16 q .. 16 q + 15 and 64 + 16 q ..
-// of 128, the scale of lane group q is that of columns 32 q .. 32 q + 31.
-template <typename T>
-__global__ void __launch_bounds__(64) w4_mx8_kernel(W4Args a) {
-  const int lane = threadIdx.x, q = lane >> 4, r = lane & 15;
-  const int kt = w4_ktiles(a.k);
-  const int64_t nt = blockIdx.x;
-  const uint4* codes = (const uint4*)a.packed + nt * kt * (W4_TILE / 16) + lane;
-  const uint32_t* scales = (const uint32_t*)((const uint8_t*)a.packed + a.scales_at) + nt * kt * 64 + lane;
-  for (int64_t m0 = (int64_t)blockIdx.y * 16; m0 < a.rows; m0 += (int64_t)gridDim.y * 16) {
-    const bool live = m0 + r < a.rows;
-    const uint8_t* x = (const uint8_t*)a.x + (live ? m0 + r : 0) * a.ldx;
-    const uint8_t* xs = a.xs + (live ? m0 + r : 0) * a.ldxs;
-    floatx4 acc = zero4();
-    for (int s = 0; s < kt; ++s) {
-      const int sc = (int)scales[s * 64];
+// NT tiles of 16 outputs by MT tiles of 16 rows a workgroup.  Its waves share
+// the inputs out, tile s of 512 to wave s % waves, and join their sums through
+// LDS in wave order.  The weights are the A operand, so that a lane ends with
+// four adjacent outputs of a row.
+template <typename X, typename Y, int NT, int MT, int WMAX>
+__global__ void __launch_bounds__(64 * WMAX) w4_kernel(W4Args a) {
+  extern __shared__ floatx4 part[];     // [wave][NT * MT][lane]
+  const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int kt = w4_ktiles(a.k), tiles = (a.n + 15) / 16;
+  const int n0 = blockIdx.x * NT;
+  const uint4* codes = (const uint4*)a.packed + lane;
+  const uint32_t* scales = (const uint32_t*)((const uint8_t*)a.packed + a.scales_at) + lane;
+  for (int64_t m0 = (int64_t)blockIdx.y * 16 * MT; m0 < a.rows; m0 += (int64_t)gridDim.y * 16 * MT) {
+    floatx4 acc[NT][MT];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint4 w = codes[(s * 4 + t) * 64];
-        const v8i av = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
-        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-        int sx = 127;
-        const int k0 = s * 512 + (4 * (q >> 1) + t) * 32, k1 = k0 + 256, ks = s * 16 + 4 * q + t;
-        if (live && k0 < a.k) lo = *(const uint4*)(x + k0 + 16 * (q & 1));
-        if (live && k1 < a.k) hi = *(const uint4*)(x + k1 + 16 * (q & 1));
-        if (live && ks * 32 < a.k) sx = xs[ks];
-        const v8i bv = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-        switch (t) {
-          case 0: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 0, 0, sc, 0, sx); break;
-          case 1: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 0, 1, sc, 0, sx); break;
-          case 2: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 0, 2, sc, 0, sx); break;
-          default: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 0, 3, sc, 0, sx);
-        }
-      }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[n][m] = zero4();
+    int64_t row[MT];                    // rows beyond the last read it; their columns are not stored
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      row[m] = m0 + 16 * m + r;
+      row[m] = row[m] < a.rows ? row[m] : a.rows - 1;
     }
-    if (live) put4((T*)a.y + (m0 + r) * a.ldy, nt * 16 + 4 * q, a.n, acc);
+    for (int s = wave; s < kt; s += waves) {
+      uint4 w[4][NT];
+      uint32_t sc[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int64_t tile = (int64_t)(n0 + n < tiles ? n0 + n : tiles - 1) * kt + s;
+        sc[n] = scales[tile * 64];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w[t][n] = codes[(tile * 4 + t) * 64];
+      }
+      const bool tail = (s + 1) * 512 > a.k;
+#define GDN_W4_PART(T)                                                         \
+  {                                                                            \
+    RowPart<X> x[MT];                                                          \
+    _Pragma("unroll") for (int m = 0; m < MT; ++m) {                           \
+      x[m].load(a, row[m], s, T, q, r);                                        \
+      if (tail) x[m].mask(a, s, T, q);                                         \
+    }                                                                          \
+    products<T, X, NT, MT>(w[T], sc, x, acc);                                  \
+  }
+      GDN_W4_PART(0) GDN_W4_PART(1) GDN_W4_PART(2) GDN_W4_PART(3)
+#undef GDN_W4_PART
+    }
+    if (waves > 1) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) part[(wave * (NT * MT) + n * MT + m) * 64 + lane] = acc[n][m];
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < NT * MT; ++i) {
+      if (i % waves != wave) continue;
+      floatx4 v = acc[i / MT][i % MT];
+      if (waves > 1) {
+        v = part[i * 64 + lane];
+        for (int u = 1; u < waves; ++u) v += part[(u * (NT * MT) + i) * 64 + lane];
+      }
+      const int64_t m = m0 + 16 * (i % MT) + r;
+      if (m < a.rows) put4((Y*)a.y + m * a.ldy, (int64_t)(n0 + i / MT) * 16 + 4 * q, a.n, v);
+    }
+    if (waves > 1) __syncthreads();
   }
 }
 
@@ -158,8 +232,7 @@ __device__ __forceinline__ float e2m1_value(int c) {
   return c < 4 ? 0.5f * c : c < 6 ? c - 2.f : 2.f * c - 8.f;
 }
 
-// One wave a tile; a lane takes the four blocks 4 q .. 4 q + 3 of its output:
-// 128 adjacent inputs.  Of the smallest scale that keeps a block within 6 =
+// One wave a tile; a lane takes blocks 4 t + q of its output.  Of the smallest scale that keeps a block within 6 =
 // 0.75 * 2^3 and the next smaller one, which cuts its largest to 6, the one
 // with the smaller squared error (sums in 64 bits, so that near ties do not
 // hang on the order of the sum; the larger scale on a tie).
@@ -171,18 +244,18 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const T* w, int64_t ldw, i
   const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (tile >= tiles) return;
   const int64_t row = tile / kt * 16 + r;
-  const int k0 = (int)(tile % kt) * 512 + q * 128;
+  const int k0 = (int)(tile % kt) * 512 + q * 32;
   uint32_t sc = 0;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     uint32_t code[4] = {0, 0, 0, 0};
-    if (row < n && k0 + 32 * t < k) {
+    if (row < n && k0 + 128 * t < k) {
       f8 v[4];
       float amax = 0.f;
       bool finite = true;
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
-        v[d] = load8(w + row * ldw + k0 + 32 * t + 8 * d);
+        v[d] = load8(w + row * ldw + k0 + 128 * t + 8 * d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           amax = fmaxf(amax, fabsf(v[d].v[j]));
@@ -227,14 +300,14 @@ __global__ void __launch_bounds__(256) w4_arrange_kernel(const uint8_t* codes, i
   const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (tile >= tiles) return;
   const int64_t row = tile / kt * 16 + r;
-  const int k0 = (int)(tile % kt) * 512 + q * 128;
+  const int k0 = (int)(tile % kt) * 512 + q * 32;
   uint32_t sc = 0;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     uint4 c = make_uint4(0, 0, 0, 0);
-    if (row < n && k0 + 32 * t < k) {
-      c = *(const uint4*)(codes + row * ldc + (k0 + 32 * t) / 2);
-      sc |= (uint32_t)scales[row * lds + (k0 + 32 * t) / 32] << (8 * t);
+    if (row < n && k0 + 128 * t < k) {
+      c = *(const uint4*)(codes + row * ldc + (k0 + 128 * t) / 2);
+      sc |= (uint32_t)scales[row * lds + (k0 + 128 * t) / 32] << (8 * t);
     }
     ((uint4*)packed)[(tile * 4 + t) * 64 + lane] = c;
   }
@@ -250,11 +323,11 @@ __global__ void __launch_bounds__(256) w4_unpack_kernel(const uint8_t* packed, i
   const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (tile >= tiles) return;
   const int64_t row = tile / kt * 16 + r;
-  const int k0 = (int)(tile % kt) * 512 + q * 128;
+  const int k0 = (int)(tile % kt) * 512 + q * 32;
   const uint32_t sc = ((const uint32_t*)(packed + scales_at))[tile * 64 + lane];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    if (row < n && k0 + 32 * t < k) {
+    if (row < n && k0 + 128 * t < k) {
       const uint4 c = ((const uint4*)packed)[(tile * 4 + t) * 64 + lane];
       const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
       const int b = (int)(sc >> (8 * t) & 255);
@@ -267,7 +340,7 @@ __global__ void __launch_bounds__(256) w4_unpack_kernel(const uint8_t* packed, i
           const float m = ldexpf(e2m1_value(code & 7), b - 127);
           v.v[j] = b == 255 ? __builtin_nanf("") : code & 8 ? -m : m;
         }
-        store8(w + row * ldw + k0 + 32 * t + 8 * d, v);
+        store8(w + row * ldw + k0 + 128 * t + 8 * d, v);
       }
     }
   }
@@ -277,15 +350,32 @@ static int64_t w4_tiles(int n, int k) { return (int64_t)((n + 15) / 16) * w4_kti
 size_t w4_bytes(int n, int k) { return (size_t)w4_tiles(n, k) * (W4_TILE + 256); }
 int64_t w4_scales_at(int n, int k) { return w4_tiles(n, k) * W4_TILE; }
 
+template <typename X, typename Y, int NT, int MT, int WMAX>
+static hipError_t w4_go(const W4Args& a, hipStream_t st) {
+  const int kt = w4_ktiles(a.k), waves = kt < WMAX ? kt : WMAX;
+  const int64_t mb = (a.rows + 16 * MT - 1) / (16 * MT), nb = ((a.n + 15) / 16 + NT - 1) / NT;
+  int64_t most = ((int64_t)1 << 31) / (nb * 64 * waves);   // a launch holds fewer than 2^32 threads
+  most = most < 1 ? 1 : most < 65535 ? most : 65535;
+  hipLaunchKernelGGL((w4_kernel<X, Y, NT, MT, WMAX>), dim3((unsigned)nb, (unsigned)(mb < most ? mb : most)),
+                     dim3(64 * waves), waves > 1 ? 1024 * NT * MT * waves : 0, st, a);
+  return hipGetLastError();
+}
+
+// More outputs a workgroup read the rows less often, fewer leave more
+// workgroups to ask for the weights at once.  Measured (us; 16480 x 2560, bf16
+// rows, one / two / four tiles of outputs): 1 row 6.8 / 7.9 / 10.6, 16 rows
+// 14.5 / 11.2 / 11.9; 64 rows in 16s 43 / 31 / 31, in 32s by four tiles 24.
+template <typename X, typename Y> static hipError_t w4_m(const W4Args& a, hipStream_t st) {
+  if (a.rows <= 8) return w4_go<X, Y, 1, 1, 16>(a, st);
+  if (a.rows <= 16) return w4_go<X, Y, 2, 1, 8>(a, st);
+  return w4_go<X, Y, 4, 2, 4>(a, st);
+}
+
 hipError_t launch_w4(const W4Args& a, gdn_dtype dt, hipStream_t st) {
   if (a.rows == 0) return hipSuccess;
-  const int64_t mb = (a.rows + 15) / 16, nb = (a.n + 15) / 16;
-  const int64_t most = ((int64_t)1 << 25) / nb;      // a launch holds fewer than 2^32 threads
-  const dim3 grid((unsigned)nb, (unsigned)(mb < most ? mb : most < 1 ? 1 : most < 65535 ? most : 65535));
-  auto k = a.xs ? (dt == GDN_BF16 ? w4_mx8_kernel<bf16> : dt == GDN_FP16 ? w4_mx8_kernel<fp16> : w4_mx8_kernel<float>)
-                : (dt == GDN_BF16 ? w4_kernel<bf16> : dt == GDN_FP16 ? w4_kernel<fp16> : w4_kernel<float>);
-  hipLaunchKernelGGL(k, grid, dim3(64), 0, st, a);
-  return hipGetLastError();
+  if (a.xs)
+    return dt == GDN_BF16 ? w4_m<Mx8, bf16>(a, st) : dt == GDN_FP16 ? w4_m<Mx8, fp16>(a, st) : w4_m<Mx8, float>(a, st);
+  return dt == GDN_BF16 ? w4_m<bf16, bf16>(a, st) : dt == GDN_FP16 ? w4_m<fp16, fp16>(a, st) : w4_m<float, float>(a, st);
 }
 
 hipError_t launch_w4_pack(gdn_dtype dt, const void* w, int64_t ldw, int n, int k, void* packed, hipStream_t st) {
