@@ -93,6 +93,12 @@ template <typename X> struct RowPart {
   }
 };
 
+// 8-bit rows go through the scaled instruction, which takes codes, values and
+// scales as they are.  It adds the products of eight adjacent inputs with 13
+// bits below the largest (measured: 256 + 2^-5 counts, 256 + 2^-6 does not,
+// inputs eight apart add in full), 2^9 times finer than the rows' steps; all
+// other sums are fp32.  Through bf16, which is exact, the same rows would cost
+// four instructions of half the rate and sixteen conversions for its one.
 template <> struct RowPart<Mx8> {
   // The instruction's 8-bit operand: lane group q holds columns 16 q .. 16 q +
   // 15 and 64 + 16 q .. of its 128, the scale of lane group q that of columns
@@ -219,6 +225,171 @@ __global__ void __launch_bounds__(64 * WMAX) w4_kernel(W4Args a) {
       if (m < a.rows) put4((Y*)a.y + m * a.ldy, (int64_t)(n0 + i / MT) * 16 + 4 * q, a.n, v);
     }
     if (waves > 1) __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- more rows
+// Rows staged in LDS, where the waves of a workgroup share them: WN waves side
+// by side take NT tiles of 16 outputs each, WK such groups share the inputs
+// out.  A step is 512 bytes of each of 16 MT rows; while it is multiplied the
+// next one's rows and weights are on their way.
+//
+// LDS rows are 512 bytes without padding; the 16-byte pieces of row i are
+// permuted by i % 16, so that 16 lanes that read one piece of 16 rows touch
+// every bank once.
+template <typename X> struct Step {                    // bytes of a value, t's of a step
+  static constexpr int E = __is_same(X, Mx8) ? 1 : sizeof(X);
+  static constexpr int TS = 4 / E;
+};
+
+template <typename X, int WN, int MT> struct StageLds {
+  uint4 x[2][16 * MT * 32];
+  uint32_t xs[__is_same(X, Mx8) ? 2 : 1][__is_same(X, Mx8) ? 16 * MT * 4 : 1];
+};
+
+template <typename X, typename Y, int WN, int WK, int NT, int MT>
+__global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
+  typedef Step<X> S;
+  constexpr bool MX = __is_same(X, Mx8);
+  constexpr int GT = 64 * WN, NL = 16 * MT * 32 / GT, NS = (16 * MT * 4 + GT - 1) / GT;
+  __shared__ union {
+    StageLds<X, WN, MT> st[WK];
+    floatx4 part[WK > 1 ? (WK - 1) * WN * NT * MT * 64 : 1];
+  } lds;
+  const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave % WN, g = wave / WN;
+  const int gt = threadIdx.x % GT;
+  StageLds<X, WN, MT>& st = lds.st[g];
+  const int kt = w4_ktiles(a.k), tiles = (a.n + 15) / 16;
+  const int steps_all = (a.k * S::E + 511) / 512;      // of 512 bytes of a row
+  const int steps = (steps_all + WK - 1) / WK;         // a group's, the last one's perhaps empty
+  const int n0 = (blockIdx.x * WN + wn) * NT;
+  const uint4* codes = (const uint4*)a.packed + lane;
+  const uint32_t* scales = (const uint32_t*)((const uint8_t*)a.packed + a.scales_at) + lane;
+
+  for (int64_t m0 = (int64_t)blockIdx.y * 16 * MT; m0 < a.rows; m0 += (int64_t)gridDim.y * 16 * MT) {
+    const uint8_t* xrow[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int64_t m = m0 + (gt + GT * i) / 32;
+      xrow[i] = (const uint8_t*)a.x + (m < a.rows ? m : a.rows - 1) * a.ldx * S::E;
+    }
+    uint4 xn[NL], wn_[S::TS][NT];
+    uint32_t sn[NT], xsn[MX ? NS : 1];
+    const auto ask = [&](int j) {      // the group's step j
+      const int step = j * WK + g, t0 = step * S::TS;  // t's of the whole row
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int64_t tile = (int64_t)(n0 + n < tiles ? n0 + n : tiles - 1) * kt + (t0 / 4 < kt ? t0 / 4 : kt - 1);
+        sn[n] = scales[tile * 64];
+#pragma unroll
+        for (int t = 0; t < S::TS; ++t) wn_[t][n] = codes[(tile * 4 + t0 % 4 + t) * 64];
+      }
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int at = step * 512 + (gt + GT * i) % 32 * 16;
+        xn[i] = *(const uint4*)(xrow[i] + (at < a.k * S::E ? at : 0));
+        if (at >= a.k * S::E) xn[i] = make_uint4(0, 0, 0, 0);
+      }
+      if constexpr (MX) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const int id = gt + GT * i, b = step * 16 + id % 4 * 4, all = a.k / 32;
+          const int64_t m = m0 + id / 4;
+          xsn[i] = 0x7f7f7f7f;
+          if (id < 16 * MT * 4) {
+            const uint8_t* p = a.xs + (m < a.rows ? m : a.rows - 1) * a.ldxs + b;
+            if (b + 4 <= all) {
+              __builtin_memcpy(&xsn[i], p, 4);
+            } else {
+              for (int u = 0; u < 4; ++u)
+                if (b + u < all) xsn[i] = (xsn[i] & ~(255u << (8 * u))) | (uint32_t)p[u] << (8 * u);
+            }
+          }
+        }
+      }
+    };
+    const auto keep = [&](int buf) {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int id = gt + GT * i, row = id / 32;
+        st.x[buf][row * 32 + (id % 32 ^ (row & 15))] = xn[i];
+      }
+      if constexpr (MX) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+          if (gt + GT * i < 16 * MT * 4) st.xs[buf][gt + GT * i] = xsn[i];
+      }
+    };
+    floatx4 acc[NT][MT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[n][m] = zero4();
+    ask(0);
+    keep(0);
+    __syncthreads();
+    for (int j = 0; j < steps; ++j) {
+      uint4 w[S::TS][NT];
+      uint32_t sc[NT];
+      const bool full = j * WK + g < steps_all;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        sc[n] = sn[n] >> (j * WK + g) * S::TS % 4 * 8;
+#pragma unroll
+        for (int t = 0; t < S::TS; ++t) w[t][n] = wn_[t][n];
+      }
+      if (j + 1 < steps) ask(j + 1);
+      if (full) {
+        const uint4* xb = st.x[j & 1];
+#define GDN_W4_PART(T)                                                                                       \
+  if constexpr (T < S::TS) {                                                                                 \
+    RowPart<X> x[MT];                                                                                        \
+    _Pragma("unroll") for (int m = 0; m < MT; ++m) {                                                         \
+      const uint4* row = xb + (16 * m + r) * 32;                                                             \
+      if constexpr (MX) {                                                                                    \
+        x[m].lo = row[(8 * T + q) ^ r];                                                                      \
+        x[m].hi = row[(8 * T + 4 + q) ^ r];                                                                  \
+        x[m].scale = (int)(st.xs[j & 1][(16 * m + r) * 4 + T] >> (8 * q));                                   \
+      } else {                                                                                               \
+        _Pragma("unroll") for (int d = 0; d < 4; ++d)                                                        \
+            _Pragma("unroll") for (int i = 0; i < S::E / 2; ++i)                                             \
+                x[m].raw[d][i] = row[((4 * T + q) * 2 * S::E + d * (S::E / 2) + i) ^ r];                     \
+      }                                                                                                      \
+    }                                                                                                        \
+    products<T, X, NT, MT>(w[T < S::TS ? T : 0], sc, x, acc);                                                \
+  }
+        GDN_W4_PART(0) GDN_W4_PART(1) GDN_W4_PART(2) GDN_W4_PART(3)
+#undef GDN_W4_PART
+      }
+      if (j + 1 < steps) keep((j + 1) & 1);
+      __syncthreads();
+    }
+    if constexpr (WK > 1) {            // the groups' sums, in group order
+      if (g > 0)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            lds.part[((((g - 1) * WN + wn) * NT + n) * MT + m) * 64 + lane] = acc[n][m];
+      __syncthreads();
+      if (g == 0)
+#pragma unroll
+        for (int u = 0; u < WK - 1; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[n][m] += lds.part[(((u * WN + wn) * NT + n) * MT + m) * 64 + lane];
+      __syncthreads();
+    }
+    if (g == 0)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int64_t row = m0 + 16 * m + r;
+          if (row < a.rows) put4((Y*)a.y + row * a.ldy, (int64_t)(n0 + n) * 16 + 4 * q, a.n, acc[n][m]);
+        }
   }
 }
 
@@ -361,14 +532,33 @@ static hipError_t w4_go(const W4Args& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// More outputs a workgroup read the rows less often, fewer leave more
-// workgroups to ask for the weights at once.  Measured (us; 16480 x 2560, bf16
-// rows, one / two / four tiles of outputs): 1 row 6.8 / 7.9 / 10.6, 16 rows
-// 14.5 / 11.2 / 11.9; 64 rows in 16s 43 / 31 / 31, in 32s by four tiles 24.
+template <typename X, typename Y, int WN, int WK, int NT, int MT>
+static hipError_t w4_rows_go(const W4Args& a, hipStream_t st) {
+  const int64_t mb = (a.rows + 16 * MT - 1) / (16 * MT), nb = ((a.n + 15) / 16 + NT * WN - 1) / (NT * WN);
+  int64_t most = ((int64_t)1 << 31) / (nb * 64 * WN * WK);
+  most = most < 1 ? 1 : most < 65535 ? most : 65535;
+  hipLaunchKernelGGL((w4_rows_kernel<X, Y, WN, WK, NT, MT>), dim3((unsigned)nb, (unsigned)(mb < most ? mb : most)),
+                     dim3(64 * WN * WK), 0, st, a);
+  return hipGetLastError();
+}
+
+// Measured, us a launch; outputs x inputs 2560 x 6144 / 16480 x 2560 / 20480 x 8192:
+//                                    bf16 rows                8-bit rows
+//   1 row     every wave its inputs  4.0 /  6.9 / 24          3.5 /  6.6 / 21
+//             staged, 4 side by side 11  /  7.2 / 21 (2 sets) 9.0 /  6.3 / 19
+//   16 rows   every wave its inputs  8.0 / 15   / 49          6.8 / 10   / 38
+//             2 side by side, 4 sets 7.4 / 10   / 24          5.1 / 12   / 22
+//             4 side by side         11  /  7.5 / 21 (2 sets) 9.0 /  6.6 / 20
+//   64 rows   4 side by side, by 16  15  / 20   / 49          9.0 / 17   / 39
+//                             by 32  19  / 15   / 41          11  / 12   / 29
+//                             by 64  31  / 18   / 51          18  / 11   / 34
+//             2 side by side, 4 sets 9.8 / 26   / 61          8.6 / 35   / 71
+// So: where tiles of outputs are fewer than two a CU, the inputs are shared out
+// over more waves; single rows need no staging there.
 template <typename X, typename Y> static hipError_t w4_m(const W4Args& a, hipStream_t st) {
-  if (a.rows <= 8) return w4_go<X, Y, 1, 1, 16>(a, st);
-  if (a.rows <= 16) return w4_go<X, Y, 2, 1, 8>(a, st);
-  return w4_go<X, Y, 4, 2, 4>(a, st);
+  if (a.n <= 16 * 512) return a.rows <= 12 ? w4_go<X, Y, 1, 1, 16>(a, st) : w4_rows_go<X, Y, 2, 4, 1, 1>(a, st);
+  if (a.rows <= 16) return w4_rows_go<X, Y, 4, __is_same(X, Mx8) ? 1 : 2, 1, 1>(a, st);
+  return w4_rows_go<X, Y, 4, 1, 1, 2>(a, st);
 }
 
 hipError_t launch_w4(const W4Args& a, gdn_dtype dt, hipStream_t st) {
