@@ -48,27 +48,26 @@ class ResidualNorm:
 
     def _sum(self, x, res):
         """Where h goes: new memory; x itself where nothing is added or converted."""
-        if x.dtype != self.dtype or x.dim() != 2 or x.shape[1] != self.hidden:
+        if x.dtype is not self.dtype or x.dim() != 2 or x.shape[1] != self.hidden:
             raise ValueError(f"x must be {self.dtype} [T, {self.hidden}], got {x.dtype} {tuple(x.shape)}")
-        if res is None and self.dtype == self.res_dtype:
-            return None
-        if res is not None and res.dtype != self.res_dtype:
+        if res is not None and res.dtype is not self.res_dtype:
             raise TypeError(f"res must be {self.res_dtype}, got {res.dtype}")
-        return x.new_empty(x.shape, dtype=self.res_dtype)
+        if res is None and self.dtype is self.res_dtype:
+            return None
+        return torch.empty_like(x if res is None else res, dtype=self.res_dtype)
 
     def forward(self, x, res, w):
         """-> (y, h).  res None: h is x, in the stream's type."""
         h = self._sum(x, res)
-        y = x.new_empty(x.shape)
+        y = torch.empty_like(x)
         L.gdn_add_norm_fwd(x, res, w, h, y, self.eps)
         return y, x if h is None else h
 
     def forward8(self, x, res, w):
         """-> (Rows8, h): y in 8 bits, for Linear4.  hidden a multiple of 32."""
         h = self._sum(x, res)
-        T, n = x.shape
-        q = x.new_empty((T, n), dtype=torch.float8_e4m3fn)
-        scale = x.new_empty((T, n // 32), dtype=torch.uint8)
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        scale = x.new_empty((x.shape[0], self.hidden // 32), dtype=torch.uint8)
         L.gdn_add_norm_fwd_mx8(x, res, w, h, q, scale, self.eps)
         return Rows8(q, scale, self.dtype), x if h is None else h
 
@@ -78,8 +77,8 @@ class ResidualNorm:
         tensor where the types are) and dw (fp32)."""
         if dy.dtype != self.dtype or h.dtype != self.res_dtype:
             raise TypeError(f"dy must be {self.dtype} and h {self.res_dtype}, got {dy.dtype} and {h.dtype}")
-        dres = h.new_empty(h.shape)
-        dx = dy.new_empty(dy.shape) if self.dtype != self.res_dtype else None
+        dres = torch.empty_like(h)
+        dx = torch.empty_like(dy) if self.dtype != self.res_dtype else None
         dw = h.new_empty(h.shape[-1], dtype=torch.float32)
         ws = h.new_empty(L.gdn_add_norm_bwd_workspace(h.shape[0], h.shape[-1]), dtype=torch.uint8)
         L.gdn_add_norm_bwd(h, w, dy, dh, dx, dres, dw, ws, self.eps)

@@ -913,11 +913,6 @@ def _wide(name, t, dtype, T, cols, dev):
     return _width(t)
 
 
-def _mat(t, dtype, shape, index):
-    """Whether t is what _wide wants, in one expression."""
-    return t.dtype is dtype and t.shape == shape and t.stride(1) == 1 and t.get_device() == index
-
-
 _TYPES = {(a, b): (x, y) for a, x in _GDN_DT.items() for b, y in _GDN_DT.items()
           if b in (a, torch.float32)}
 
@@ -930,47 +925,80 @@ def _types(dtype, res_dtype):
     return got
 
 
-def _norm_rows(x, res, w, h):
-    """The checks of the residual norm's forward: (T, n, types, ldx, ldr, ldh, index, device)."""
+def _norm_rows(x, res, w, h, named):
+    """The checks of the residual norm's forward that say what is wrong:
+    T, n, device index, types and the row strides of x, res, h and the outputs
+    `named`, (name, tensor, columns to one of theirs, dtype or None for x's)."""
     if x is None or x.dim() != 2:
         raise ValueError("x must be a [T, n] matrix")
-    i, dev, shape = x.get_device(), x.device, x.shape
-    T, n = shape
+    (T, n), dev = x.shape, x.device
     rt = res.dtype if res is not None else h.dtype if h is not None else x.dtype
     types = _types(x.dtype, rt)
-    if not (T > 1 and i >= 0 and n > 1 and x.stride(1) == 1 and
-            (res is None or _mat(res, rt, shape, i)) and (h is None or _mat(h, rt, shape, i)) and
-            _is_flat(w, torch.float32, n, i)):
-        ldx = _wide("x", x, x.dtype, T, n, dev)
-        ldr = 0 if res is None else _wide("res", res, rt, T, n, dev)
-        ldh = 0 if h is None else _wide("h", h, rt, T, n, dev)
-        _need("w", w, torch.float32, n)
-        _on(dev, ("w", w))
-        return T, n, types, ldx, ldr, ldh, i, dev
-    return (T, n, types, x.stride(0), 0 if res is None else res.stride(0),
-            0 if h is None else h.stride(0), i, dev)
+    ld = [_wide("x", x, x.dtype, T, n, dev), 0 if res is None else _wide("res", res, rt, T, n, dev),
+          0 if h is None else _wide("h", h, rt, T, n, dev)]
+    ld += [_wide(nm, t, x.dtype if to is None else to, T, n // per, dev) for nm, t, per, to in named]
+    _need("w", w, torch.float32, n)
+    _on(dev, ("w", w))
+    return T, n, x.get_device(), *types, *ld
 
 
 def gdn_add_norm_fwd(x, res, w, h, y, eps=1e-6, stream=None):
     """h = x + res (None: h = x), y = h / sqrt(mean h^2 + eps) * (1 + w) over
     the rows of [T, n] matrices (rows may be strided).  h may be None (not
     written), res itself, or x of the same type; y may be x."""
-    T, n, (dt, rt), ldx, ldr, ldh, i, dev = _norm_rows(x, res, w, h)
-    ldy = y.stride(0) if T > 1 and _mat(y, x.dtype, x.shape, i) else _wide("y", y, x.dtype, T, n, dev)
+    try:
+        T, n = shape = x.shape
+        i, xt = x.get_device(), x.dtype
+        rt = res.dtype if res is not None else h.dtype if h is not None else xt
+        dt, rdt = _TYPES[xt, rt]
+        xs, ys = x.stride(), y.stride()
+        rs = xs if res is None else res.stride()
+        hs = xs if h is None else h.stride()
+        good = (xs[1] == rs[1] == hs[1] == ys[1] == 1 and i >= 0 and y.dtype is xt and y.shape == shape and
+                y.get_device() == i and (res is None or res.shape == shape and res.get_device() == i) and
+                (h is None or h.dtype is rt and h.shape == shape and h.get_device() == i) and
+                w.dtype is torch.float32 and w.numel() == n and w.get_device() == i and w.is_contiguous())
+        ldx, ldr, ldh, ldy = xs[0], rs[0], hs[0], ys[0]
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
+        good = False
+    if not good:
+        T, n, i, dt, rdt, ldx, ldr, ldh, ldy = _norm_rows(x, res, w, h, (("y", y, 1, None),))
+    elif T < 2:
+        ldx = ldr = ldh = ldy = n      # torch leaves a single row's stride open
     _run("gdn_add_norm_fwd", i, (
-        T, n, dt, rt, x.data_ptr(), ldx, _ptr(res), ldr, w.data_ptr(), eps, _ptr(h), ldh, y.data_ptr(),
-        ldy, _raw_stream(dev, i, stream)))
+        T, n, dt, rdt, x.data_ptr(), ldx, None if res is None else res.data_ptr(), ldr, w.data_ptr(), eps,
+        None if h is None else h.data_ptr(), ldh, y.data_ptr(), ldy, _raw_stream(x.device, i, stream)))
 
 
 def gdn_add_norm_fwd_mx8(x, res, w, h, q, scale, eps=1e-6, stream=None):
     """gdn_add_norm_fwd with y in 8 bits: q float8_e4m3fn [T, n] under a power
     of two for each 32 columns, scale uint8 [T, n / 32] (2^(byte - 127))."""
-    T, n, (dt, rt), ldx, ldr, ldh, i, dev = _norm_rows(x, res, w, h)
-    ldq = _wide("q", q, torch.float8_e4m3fn, T, n, dev)
-    lds = _wide("scale", scale, torch.uint8, T, n // 32, dev)
+    f8, u8 = torch.float8_e4m3fn, torch.uint8
+    try:
+        T, n = shape = x.shape
+        i, xt = x.get_device(), x.dtype
+        rt = res.dtype if res is not None else h.dtype if h is not None else xt
+        dt, rdt = _TYPES[xt, rt]
+        xs, qs, ss = x.stride(), q.stride(), scale.stride()
+        rs = xs if res is None else res.stride()
+        hs = xs if h is None else h.stride()
+        good = (xs[1] == rs[1] == hs[1] == qs[1] == 1 and (ss[1] == 1 or n == 32) and i >= 0 and
+                q.dtype is f8 and q.shape == shape and q.get_device() == i and
+                scale.dtype is u8 and scale.shape == (T, n // 32) and scale.get_device() == i and
+                (res is None or res.shape == shape and res.get_device() == i) and
+                (h is None or h.dtype is rt and h.shape == shape and h.get_device() == i) and
+                w.dtype is torch.float32 and w.numel() == n and w.get_device() == i and w.is_contiguous())
+        ldx, ldr, ldh, ldq, lds = xs[0], rs[0], hs[0], qs[0], ss[0]
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
+        good = False
+    if not good:
+        T, n, i, dt, rdt, ldx, ldr, ldh, ldq, lds = _norm_rows(x, res, w, h, (("q", q, 1, f8), ("scale", scale, 32, u8)))
+    elif T < 2:
+        ldx = ldr = ldh = ldq = lds = n
     _run("gdn_add_norm_fwd_mx8", i, (
-        T, n, dt, rt, x.data_ptr(), ldx, _ptr(res), ldr, w.data_ptr(), eps, _ptr(h), ldh, q.data_ptr(),
-        ldq, scale.data_ptr(), lds, _raw_stream(dev, i, stream)))
+        T, n, dt, rdt, x.data_ptr(), ldx, None if res is None else res.data_ptr(), ldr, w.data_ptr(), eps,
+        None if h is None else h.data_ptr(), ldh, q.data_ptr(), ldq, scale.data_ptr(), lds,
+        _raw_stream(x.device, i, stream)))
 
 
 def gdn_add_norm_bwd_workspace(rows, n):
@@ -981,21 +1009,39 @@ def gdn_add_norm_bwd(h, w, dy, dh, dx, dres, dw, ws, eps=1e-6, stream=None):
     """The backward, from the forward's h: dy [T, n] in the rows' type, dh (or
     None) in h's -> dx in dy's type, dres in h's, dw fp32 [n] (each may be
     None; ws is needed for dw only).  dres may be dh, dx may be dy."""
-    if h is None or dy is None or h.dim() != 2:
-        raise ValueError("h and dy must be [T, n] matrices")
-    T, n = h.shape
-    i, dev, rt, xt = h.get_device(), h.device, h.dtype, dy.dtype
-    dt, rdt = _types(xt, rt)
-    ld = [_wide(nm, t, to, T, n, dev) if t is not None else 0 for nm, t, to in (
-        ("h", h, rt), ("dy", dy, xt), ("dh", dh, rt), ("dx", dx, xt), ("dres", dres, rt))]
-    _need("w", w, torch.float32, n)
-    _need("dw", dw, torch.float32, n, optional=True)
-    _ws(ws)
-    _on(dev, ("w", w), ("dw", dw), ("workspace", ws))
+    try:
+        T, n = shape = h.shape
+        i, rt, xt = h.get_device(), h.dtype, dy.dtype
+        dt, rdt = _TYPES[xt, rt]
+        hs, ys = h.stride(), dy.stride()
+        us, gs, rs = (hs if v is None else v.stride() for v in (dh, dx, dres))
+        good = (hs[1] == ys[1] == us[1] == gs[1] == rs[1] == 1 and i >= 0 and
+                dy.shape == shape and dy.get_device() == i and
+                (dh is None or dh.dtype is rt and dh.shape == shape and dh.get_device() == i) and
+                (dx is None or dx.dtype is xt and dx.shape == shape and dx.get_device() == i) and
+                (dres is None or dres.dtype is rt and dres.shape == shape and dres.get_device() == i) and
+                _is_flat(w, torch.float32, n, i) and (dw is None or _is_flat(dw, torch.float32, n, i)) and
+                (ws is None or _is_flat(ws, torch.uint8, ws.numel(), i)))
+        ld = hs[0], ys[0], us[0], gs[0], rs[0]
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
+        good = False
+    if not good:
+        if h is None or dy is None or h.dim() != 2:
+            raise ValueError("h and dy must be [T, n] matrices")
+        (T, n), i, dev, rt, xt = h.shape, h.get_device(), h.device, h.dtype, dy.dtype
+        dt, rdt = _types(xt, rt)
+        ld = [_wide(nm, t, to, T, n, dev) if t is not None else 0 for nm, t, to in (
+            ("h", h, rt), ("dy", dy, xt), ("dh", dh, rt), ("dx", dx, xt), ("dres", dres, rt))]
+        _need("w", w, torch.float32, n)
+        _need("dw", dw, torch.float32, n, optional=True)
+        _ws(ws)
+        _on(dev, ("w", w), ("dw", dw), ("workspace", ws))
+    elif T < 2:
+        ld = (n,) * 5
     _run("gdn_add_norm_bwd", i, (
         T, n, dt, rdt, h.data_ptr(), ld[0], w.data_ptr(), eps, dy.data_ptr(), ld[1], _ptr(dh), ld[2],
         _ptr(dx), ld[3], _ptr(dres), ld[4], _ptr(dw), _ptr(ws), 0 if ws is None else ws.numel(),
-        _raw_stream(dev, i, stream)))
+        _raw_stream(h.device, i, stream)))
 
 
 def gdn_w4_bytes(n, k):
@@ -1045,26 +1091,54 @@ def gdn_w4_unpack(w4, weight, stream=None):
 
 def gdn_w4_fwd(x, w4, y, stream=None):
     """y [T, n] = x [T, k] W^T in x's storage type, rows may be strided."""
-    i, dt, T = w4.index, x.dtype, x.shape[0]
-    if T > 1 and dt in _GDN_DT and _mat(x, dt, (T, w4.k), i) and _mat(y, dt, (T, w4.n), i):
-        ldx, ldy = x.stride(0), y.stride(0)
-    else:
-        if dt not in _GDN_DT:
-            raise TypeError(f"unsupported dtype {dt}")
-        ldx = _wide("x", x, dt, T, w4.k, w4.device)
-        ldy = _wide("y", y, dt, T, w4.n, w4.device)
-    _run("gdn_w4_fwd", i, (T, w4.n, w4.k, _GDN_DT[dt], x.data_ptr(), ldx, *w4.args, y.data_ptr(), ldy,
+    i, n, k = w4.index, w4.n, w4.k
+    try:
+        T, xt = x.shape[0], x.dtype
+        dt = _GDN_DT[xt]
+        xs, ys = x.stride(), y.stride()
+        good = (xs[1] == 1 and (ys[1] == 1 or n == 1) and i >= 0 and x.shape == (T, k) and x.get_device() == i and
+                y.dtype is xt and y.shape == (T, n) and y.get_device() == i)
+        ldx, ldy = xs[0], ys[0]
+    except (AttributeError, IndexError, KeyError, TypeError):
+        good = False
+    if not good:
+        if x.dtype not in _GDN_DT:
+            raise TypeError(f"unsupported dtype {x.dtype}")
+        T, dt = x.shape[0], _GDN_DT[x.dtype]
+        ldx = _wide("x", x, x.dtype, T, k, w4.device)
+        ldy = _wide("y", y, x.dtype, T, n, w4.device)
+    elif T < 2:
+        ldx, ldy = k, (n + 7) // 8 * 8      # torch leaves a single row's stride open
+    packed, size = w4.args
+    _run("gdn_w4_fwd", i, (T, n, k, dt, x.data_ptr(), ldx, packed, size, y.data_ptr(), ldy,
                            _raw_stream(w4.device, i, stream)))
 
 
 def gdn_w4_fwd_mx8(q, scale, w4, y, stream=None):
     """gdn_w4_fwd for rows in 8 bits as gdn_add_norm_fwd_mx8 writes them; y in
     any storage type."""
-    i, dt, T = w4.index, y.dtype, q.shape[0]
-    if dt not in _GDN_DT:
-        raise TypeError(f"unsupported dtype {dt}")
-    ldq = _wide("q", q, torch.float8_e4m3fn, T, w4.k, w4.device)
-    lds = _wide("scale", scale, torch.uint8, T, w4.k // 32, w4.device)
-    ldy = _wide("y", y, dt, T, w4.n, w4.device)
-    _run("gdn_w4_fwd_mx8", i, (T, w4.n, w4.k, q.data_ptr(), ldq, scale.data_ptr(), lds, *w4.args,
-                               _GDN_DT[dt], y.data_ptr(), ldy, _raw_stream(w4.device, i, stream)))
+    i, n, k = w4.index, w4.n, w4.k
+    f8, u8 = torch.float8_e4m3fn, torch.uint8
+    try:
+        T, yt = q.shape[0], y.dtype
+        dt = _GDN_DT[yt]
+        qs, ss, ys = q.stride(), scale.stride(), y.stride()
+        good = (qs[1] == 1 and (ss[1] == 1 or k == 32) and (ys[1] == 1 or n == 1) and i >= 0 and
+                q.dtype is f8 and q.shape == (T, k) and q.get_device() == i and
+                scale.dtype is u8 and scale.shape == (T, k // 32) and scale.get_device() == i and
+                y.shape == (T, n) and y.get_device() == i)
+        ldq, lds, ldy = qs[0], ss[0], ys[0]
+    except (AttributeError, IndexError, KeyError, TypeError):
+        good = False
+    if not good:
+        if y.dtype not in _GDN_DT:
+            raise TypeError(f"unsupported dtype {y.dtype}")
+        T, dt = q.shape[0], _GDN_DT[y.dtype]
+        ldq = _wide("q", q, f8, T, k, w4.device)
+        lds = _wide("scale", scale, u8, T, k // 32, w4.device)
+        ldy = _wide("y", y, y.dtype, T, n, w4.device)
+    elif T < 2:
+        ldq, lds, ldy = k, k // 32, (n + 7) // 8 * 8
+    packed, size = w4.args
+    _run("gdn_w4_fwd_mx8", i, (T, n, k, q.data_ptr(), ldq, scale.data_ptr(), lds, packed, size, dt, y.data_ptr(), ldy,
+                               _raw_stream(w4.device, i, stream)))
