@@ -590,8 +590,8 @@ gdn_status gdn_add_norm_bwd(int64_t rows, int32_t n, gdn_dtype dtype, gdn_dtype 
 
 static gdn_status check_w4(int32_t n, int32_t k) {
   if (n < 1 || k < 1) return GDN_ERR_INVALID_ARG;
-  // groups of 32 inputs; at most 2^26 tiles of 16 x 512 weights
-  if (k % 32 || n > (1 << 22) || k > (1 << 20) || (int64_t)((n + 15) / 16) * ((k + 511) / 512) >= (1LL << 26))
+  // groups of 32 inputs; fewer than 2^24 tiles of 16 x 512 weights
+  if (k % 32 || n > (1 << 22) || k > (1 << 20) || (int64_t)((n + 15) / 16) * ((k + 511) / 512) >= (1LL << 24))
     return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }

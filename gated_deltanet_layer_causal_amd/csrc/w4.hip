@@ -394,72 +394,79 @@ __global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
 }
 
 // ---------------------------------------------------------------- packing
-// e2m1 code (no sign) of a >= 0, ties to the even code; 7 (6.0) from 5 on.
-__device__ __forceinline__ int e2m1(float a) {
-  const float c = a < 2.f ? rintf(2.f * a) : a < 4.f ? 4.f + rintf(a - 2.f) : 6.f + rintf(0.5f * a - 2.f);
-  return (int)fminf(c, 7.f);
-}
-__device__ __forceinline__ float e2m1_value(int c) {
-  return c < 4 ? 0.5f * c : c < 6 ? c - 2.f : 2.f * c - 8.f;
-}
-
-// One wave a tile; a lane takes blocks 4 t + q of its output.  Of the smallest scale that keeps a block within 6 =
-// 0.75 * 2^3 and the next smaller one, which cuts its largest to 6, the one
-// with the smaller squared error (sums in 64 bits, so that near ties do not
-// hang on the order of the sum; the larger scale on a tie).
+// One wave a t of a tile: a lane takes block 4 t + q of its output.
+//
+// Of the smallest scale u that keeps a block within 6 = 0.75 * 2^3 and u / 2,
+// which cuts its largest to 6, the one with the smaller squared error.  With
+// y = w / (u / 2), A and B the nearest values of w under u and u / 2 in units
+// of u / 2, the errors' difference is
+//   sum (y - B)^2 - (y - A)^2 = sum (A - B) (2 y - (A + B)),
+// one sum, most of whose terms are zero.  A term is exact in fp32 for 16-bit
+// weights (a few bits of A - B by at most 11 of the rest) and the sum is 64
+// bits, so that near ties do not hang on its order.
+typedef float floatx2 __attribute__((ext_vector_type(2)));
 template <typename T>
-__global__ void __launch_bounds__(256) w4_pack_kernel(const T* w, int64_t ldw, int n, int k, int64_t tiles,
+__global__ void __launch_bounds__(256) w4_pack_kernel(const T* w, int64_t ldw, int n, int k, int64_t parts,
                                                       uint8_t* packed, int64_t scales_at) {
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
   const int kt = w4_ktiles(k);
-  const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (tile >= tiles) return;
+  const int64_t part = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), tile = part >> 2;
+  if (part >= parts) return;
+  const int t = (int)(part & 3);
   const int64_t row = tile / kt * 16 + r;
-  const int k0 = (int)(tile % kt) * 512 + q * 32;
-  uint32_t sc = 0;
+  const int k0 = (int)(tile % kt) * 512 + 128 * t + 32 * q;
+  uint32_t code[4] = {0, 0, 0, 0};
+  int e = -127;
+  if (row < n && k0 < k) {
+    f8 v[4];
+    uint32_t top = 0;                  // the largest magnitude's bits; above those of infinity: NaN
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    uint32_t code[4] = {0, 0, 0, 0};
-    if (row < n && k0 + 128 * t < k) {
-      f8 v[4];
-      float amax = 0.f;
-      bool finite = true;
+    for (int d = 0; d < 4; ++d) v[d] = load8(w + row * ldw + k0 + 8 * d);
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t b = __float_as_uint(v[d].v[j]) & 0x7fffffffu;
+        top = top > b ? top : b;
+      }
+    if (top >= 0x7f800000u) {
+      e = 128;
+    } else if (top != 0) {
+      const float amax = __uint_as_float(top);
+      e = __builtin_amdgcn_frexp_expf(amax) - 3 + (__builtin_amdgcn_frexp_mantf(amax) > 0.75f);
+      e = e < -127 ? -127 : e > 125 ? 125 : e;       // 6 * 2^125 is finite, 4 * 2^126 is not
+      const float u = scale_f(e + 127), half = scale_f(e > -127 ? e + 126 : 0);
+      uint32_t fine[4];
+      double sum = 0;
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
-        v[d] = load8(w + row * ldw + k0 + 128 * t + 8 * d);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          amax = fmaxf(amax, fabsf(v[d].v[j]));
-          finite &= __builtin_isfinite(v[d].v[j]);
-        }
-      }
-      int e = __builtin_amdgcn_frexp_expf(amax) - 3 + (__builtin_amdgcn_frexp_mantf(amax) > 0.75f);
-      e = amax == 0.f || e < -127 ? -127 : e > 125 ? 125 : e;    // 6 * 2^125 is finite, 4 * 2^126 is not
-      double wide = 0, fine = 0;       // squared errors, in units of 4^e and 4^(e - 1)
-#pragma unroll
-      for (int d = 0; d < 4; ++d)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float a = ldexpf(fabsf(v[d].v[j]), -e);
-          const double x = (double)a - e2m1_value(e2m1(a)), y = (double)(2.f * a) - e2m1_value(e2m1(2.f * a));
-          wide += x * x;
-          fine += y * y;
-        }
-      if (e > -127 && fine < 4 * wide) --e;
-#pragma unroll
-      for (int d = 0; d < 4; ++d)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float a = ldexpf(fabsf(v[d].v[j]), -e);
-          code[d] |= (uint32_t)(e2m1(a) | (v[d].v[j] < 0.f ? 8 : 0)) << (4 * j);
-        }
-      if (!finite) e = 128;
-      if (!finite) code[0] = code[1] = code[2] = code[3] = 0;
-      sc |= (uint32_t)(e + 127) << (8 * t);
-    }
-    ((uint4*)packed)[(tile * 4 + t) * 64 + lane] = make_uint4(code[0], code[1], code[2], code[3]);
+        uint32_t cw = 0, cf = 0;
+#define GDN_PAIR(I)                                                                                     \
+  cw = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(cw, v[d].v[2 * I], v[d].v[2 * I + 1], u, I);            \
+  cf = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(cf, v[d].v[2 * I], v[d].v[2 * I + 1], half, I);
+        GDN_PAIR(0) GDN_PAIR(1) GDN_PAIR(2) GDN_PAIR(3)
+#undef GDN_PAIR
+#define GDN_PAIR(I)                                                                                     \
+  {                                                                                                     \
+    const floatx2 A = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw, 2.f, I);                             \
+    const floatx2 B = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cf, 1.f, I);                             \
+    _Pragma("unroll") for (int j = 0; j < 2; ++j)                                                       \
+        sum += (double)((A[j] - B[j]) * (ldexpf(v[d].v[2 * I + j], 2 - e) - (A[j] + B[j])));            \
   }
-  ((uint32_t*)(packed + scales_at))[tile * 64 + lane] = sc;
+        GDN_PAIR(0) GDN_PAIR(1) GDN_PAIR(2) GDN_PAIR(3)
+#undef GDN_PAIR
+        code[d] = cw;
+        fine[d] = cf;
+      }
+      if (e > -127 && sum < 0) {
+        --e;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) code[d] = fine[d];
+      }
+    }
+  }
+  ((uint4*)packed)[part * 64 + lane] = make_uint4(code[0], code[1], code[2], code[3]);
+  packed[scales_at + (tile * 64 + lane) * 4 + t] = (uint8_t)(e + 127);
 }
 
 // Codes [n][k/2] and scales [n][k/32] into the packed order.
@@ -485,35 +492,48 @@ __global__ void __launch_bounds__(256) w4_arrange_kernel(const uint8_t* codes, i
   ((uint32_t*)(packed + scales_at))[tile * 64 + lane] = sc;
 }
 
-// Packed weights into dense rows of a storage type.
+// Packed weights into dense rows of a storage type: one wave a t of a tile,
+// turned in LDS so that 16 lanes store 256 adjacent bytes of an output.
 template <typename T>
 __global__ void __launch_bounds__(256) w4_unpack_kernel(const uint8_t* packed, int64_t scales_at, int n, int k,
-                                                        int64_t tiles, T* w, int64_t ldw) {
-  const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+                                                        int64_t parts, T* w, int64_t ldw) {
+  constexpr int V = 16 / sizeof(T), P = 128 / V;       // values of a 16-byte piece, pieces of a row
+  __shared__ uint4 turn[4][16 * (P + 1)];              // rows a piece apart: all banks once
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, r = lane & 15;
   const int kt = w4_ktiles(k);
-  const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (tile >= tiles) return;
-  const int64_t row = tile / kt * 16 + r;
-  const int k0 = (int)(tile % kt) * 512 + q * 32;
-  const uint32_t sc = ((const uint32_t*)(packed + scales_at))[tile * 64 + lane];
+  const int64_t part = (int64_t)blockIdx.x * 4 + wave, tile = part >> 2;
+  const int t = (int)(part & 3);
+  if (part < parts) {
+    const uint4 c = ((const uint4*)packed)[part * 64 + lane];
+    const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
+    const float s = scale_f(packed[scales_at + (tile * 64 + lane) * 4 + t]);
+    uint4* at = turn[wave] + r * (P + 1) + q * (P / 4);
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    if (row < n && k0 + 128 * t < k) {
-      const uint4 c = ((const uint4*)packed)[(tile * 4 + t) * 64 + lane];
-      const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
-      const int b = (int)(sc >> (8 * t) & 255);
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        f8 v;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int code = (int)(cs[d] >> (4 * j) & 15);
-          const float m = ldexpf(e2m1_value(code & 7), b - 127);
-          v.v[j] = b == 255 ? __builtin_nanf("") : code & 8 ? -m : m;
-        }
-        store8(w + row * ldw + k0 + 128 * t + 8 * d, v);
+    for (int d = 0; d < 4; ++d) {
+      if constexpr (sizeof(T) == 4) {
+#define GDN_PAIR(I) const floatx2 v##I = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cs[d], s, I);
+        GDN_PAIR(0) GDN_PAIR(1) GDN_PAIR(2) GDN_PAIR(3)
+#undef GDN_PAIR
+        at[2 * d] = __builtin_bit_cast(uint4, floatx4{v0[0], v0[1], v1[0], v1[1]});
+        at[2 * d + 1] = __builtin_bit_cast(uint4, floatx4{v2[0], v2[1], v3[0], v3[1]});
+      } else if constexpr (__is_same(T, bf16)) {
+        at[d] = __builtin_bit_cast(uint4, codes8(cs[d], s));
+      } else {
+#define GDN_PAIR(I) __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(cs[d], s, I))
+        at[d] = make_uint4(GDN_PAIR(0), GDN_PAIR(1), GDN_PAIR(2), GDN_PAIR(3));
+#undef GDN_PAIR
       }
     }
+  }
+  __syncthreads();
+  if (part >= parts) return;
+  const int64_t row0 = tile / kt * 16;
+  const int k0 = (int)(tile % kt) * 512 + 128 * t;
+#pragma unroll
+  for (int i = 0; i < 16 * P / 64; ++i) {
+    const int id = i * 64 + lane, row = id / P, piece = id % P;
+    if (row0 + row < n && k0 + piece * V < k)
+      *reinterpret_cast<uint4*>(w + (row0 + row) * ldw + k0 + piece * V) = turn[wave][row * (P + 1) + piece];
   }
 }
 
@@ -569,14 +589,14 @@ hipError_t launch_w4(const W4Args& a, gdn_dtype dt, hipStream_t st) {
 }
 
 hipError_t launch_w4_pack(gdn_dtype dt, const void* w, int64_t ldw, int n, int k, void* packed, hipStream_t st) {
-  const int64_t tiles = w4_tiles(n, k), at = w4_scales_at(n, k);
-  const dim3 grid((unsigned)((tiles + 3) / 4));
+  const int64_t parts = 4 * w4_tiles(n, k), at = w4_scales_at(n, k);
+  const dim3 grid((unsigned)((parts + 3) / 4));
   if (dt == GDN_BF16)
-    hipLaunchKernelGGL(w4_pack_kernel<bf16>, grid, dim3(256), 0, st, (const bf16*)w, ldw, n, k, tiles, (uint8_t*)packed, at);
+    hipLaunchKernelGGL(w4_pack_kernel<bf16>, grid, dim3(256), 0, st, (const bf16*)w, ldw, n, k, parts, (uint8_t*)packed, at);
   else if (dt == GDN_FP16)
-    hipLaunchKernelGGL(w4_pack_kernel<fp16>, grid, dim3(256), 0, st, (const fp16*)w, ldw, n, k, tiles, (uint8_t*)packed, at);
+    hipLaunchKernelGGL(w4_pack_kernel<fp16>, grid, dim3(256), 0, st, (const fp16*)w, ldw, n, k, parts, (uint8_t*)packed, at);
   else
-    hipLaunchKernelGGL(w4_pack_kernel<float>, grid, dim3(256), 0, st, (const float*)w, ldw, n, k, tiles, (uint8_t*)packed, at);
+    hipLaunchKernelGGL(w4_pack_kernel<float>, grid, dim3(256), 0, st, (const float*)w, ldw, n, k, parts, (uint8_t*)packed, at);
   return hipGetLastError();
 }
 
@@ -589,14 +609,14 @@ hipError_t launch_w4_arrange(const void* codes, int64_t ldc, const void* scales,
 }
 
 hipError_t launch_w4_unpack(gdn_dtype dt, const void* packed, int n, int k, void* w, int64_t ldw, hipStream_t st) {
-  const int64_t tiles = w4_tiles(n, k), at = w4_scales_at(n, k);
-  const dim3 grid((unsigned)((tiles + 3) / 4));
+  const int64_t parts = 4 * w4_tiles(n, k), at = w4_scales_at(n, k);
+  const dim3 grid((unsigned)((parts + 3) / 4));
   if (dt == GDN_BF16)
-    hipLaunchKernelGGL(w4_unpack_kernel<bf16>, grid, dim3(256), 0, st, (const uint8_t*)packed, at, n, k, tiles, (bf16*)w, ldw);
+    hipLaunchKernelGGL(w4_unpack_kernel<bf16>, grid, dim3(256), 0, st, (const uint8_t*)packed, at, n, k, parts, (bf16*)w, ldw);
   else if (dt == GDN_FP16)
-    hipLaunchKernelGGL(w4_unpack_kernel<fp16>, grid, dim3(256), 0, st, (const uint8_t*)packed, at, n, k, tiles, (fp16*)w, ldw);
+    hipLaunchKernelGGL(w4_unpack_kernel<fp16>, grid, dim3(256), 0, st, (const uint8_t*)packed, at, n, k, parts, (fp16*)w, ldw);
   else
-    hipLaunchKernelGGL(w4_unpack_kernel<float>, grid, dim3(256), 0, st, (const uint8_t*)packed, at, n, k, tiles, (float*)w, ldw);
+    hipLaunchKernelGGL(w4_unpack_kernel<float>, grid, dim3(256), 0, st, (const uint8_t*)packed, at, n, k, parts, (float*)w, ldw);
   return hipGetLastError();
 }
 

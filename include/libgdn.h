@@ -483,7 +483,7 @@ size_t gdn_add_norm_bwd_workspace(int64_t rows, int32_t n);
  * scale for each 32 inputs of an output.  They are held packed, in the
  * library's own order, in gdn_w4_bytes(n, k) bytes (16-byte aligned); k is
  * padded to a multiple of 512 and n to one of 16 there.  k a multiple of 32, at
- * most 2^20; n at most 2^22; fewer than 2^26 tiles of 16 x 512 in all.  In every
+ * most 2^20; n at most 2^22; fewer than 2^24 tiles of 16 x 512 in all.  In every
  * call below `bytes` is the size of `packed`, at least gdn_w4_bytes(n, k).
  *
  * gdn_w4_pack: W [n][ldw] in dtype into 4 bits.  Of the smallest scale that
