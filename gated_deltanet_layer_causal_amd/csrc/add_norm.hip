@@ -3,26 +3,37 @@
 // and its backward.  HBM-bound: each row is read once, held in registers and
 // written once.  The norm reads the sum before h is rounded to its storage
 // type, so y carries one rounding.
+//
+// A thread owns 8 columns (two times 8 beyond 8192) for the whole call, with
+// their weights in registers, and takes RB rows at a time, so that the loads
+// of RB rows are on their way together (PF: the next rows' while these are
+// worked on).  A row is owned by LPR lanes, or by all
+// waves of a workgroup where it is wider than a wave's 512 columns.
 #include "common.h"
 #include "launch.h"
 
 namespace gdn {
 
-// A row is owned by TPR threads (WPR waves); thread i of them holds the 8
-// columns at (p * TPR + i) * 8 of each piece p < P.
-template <int WPR>
-__device__ __forceinline__ float group_sum(float x, float* red) {
+// Sums of N values over a row's threads; every thread gets them.  red: two
+// buffers used in turn, so that one barrier a call is enough.
+template <int LPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N], int waves) {
 #pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m);
-  if constexpr (WPR > 1) {
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int m = LPR / 2; m >= 1; m >>= 1) v[i] += __shfl_xor(v[i], m);
+  if (LPR == 64 && waves > 1) {
     const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) red[wave] = x;
-    __syncthreads();
-    x = 0.f;
+    if ((threadIdx.x & 63) == 0)
 #pragma unroll
-    for (int i = 0; i < WPR; ++i) x += red[wave / WPR * WPR + i];
+      for (int i = 0; i < N; ++i) red[wave][i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.f;
+    for (int u = 0; u < waves; ++u)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += red[u][i];
   }
-  return x;
 }
 
 // 8 values of a group of 32 columns (4 adjacent lanes) in e4m3 under the
@@ -49,49 +60,112 @@ __device__ __forceinline__ uint2 to_mx8(const f8& v, int* scale) {
   return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
-template <typename T, typename R, bool MX8, int WPR, int P>
-__global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) add_norm_fwd_kernel(AddNormArgs a) {
-  constexpr int TPR = 64 * WPR, GROUPS = WPR == 1 ? 4 : 1;
-  __shared__ float red[WPR == 1 ? 1 : WPR];
-  const int i = threadIdx.x % TPR;
-  const int64_t r = (int64_t)blockIdx.x * GROUPS + threadIdx.x / TPR;
-  if (r >= a.rows) return;       // a whole row's threads: no barrier is missed
-  const T* x = (const T*)a.x + r * a.ldx;
-  const R* res = (const R*)a.res + r * a.ldr;
-  f8 v[P];
-  float ss = 0.f;
+template <typename T, bool NT> __device__ __forceinline__ Raw8<T> ask8(const T* p) {
+  if constexpr (NT) {
+    Raw8<T> r;
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int c = (p * TPR + i) * 8;
-    if (c < a.n) {
-      v[p] = load8(x + c);
-      if (a.res) {
-        const f8 s = load8(res + c);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[p].v[j] += s.v[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss += v[p].v[j] * v[p].v[j];
-    }
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+      r.v[i] = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const nt_u32x4*>(p) + i));
+    return r;
+  } else {
+    return ld_raw8(p);
   }
-  ss = group_sum<WPR>(ss, red);
-  const float rho = rsqrtf(ss / (float)a.n + a.eps);
+}
+template <typename T, bool NT> __device__ __forceinline__ void put8(T* p, const f8& v) {
+  if constexpr (NT) store8_nt(p, v);
+  else store8(p, v);
+}
+
+// The columns of piece p of a thread, and whether they are in the row (those
+// that are not read the first ones and count for nothing).
+struct Cols {
+  int c;
+  bool in;
+};
+template <int P> __device__ __forceinline__ void cols(Cols (&at)[P], int i, int threads, int n) {
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int c = (p * TPR + i) * 8;
-    if (c < a.n) {
-      if (a.h) store8((R*)a.h + r * a.ldh + c, v[p]);
-      const f8 w = load8(a.w + c);
-      f8 y;
+    const int c = (p * threads + i) * 8;
+    at[p].in = c < n;
+    at[p].c = at[p].in ? c : 0;
+  }
+}
+template <int P> __device__ __forceinline__ void weights(f8 (&w)[P], const float* wp, const Cols (&at)[P]) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y.v[j] = v[p].v[j] * rho * (1.f + w.v[j]);
-      if constexpr (MX8) {
-        int e;
-        const uint2 q = to_mx8(y, &e);
-        *(uint2*)((uint8_t*)a.y + r * a.ldy + c) = q;
-        if (i % 4 == 0) a.scale[r * a.lds + c / 32] = (uint8_t)e;
-      } else {
-        store8((T*)a.y + r * a.ldy + c, y);
+  for (int p = 0; p < P; ++p) {
+    w[p] = load8(wp + at[p].c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[p].v[j] += 1.f;
+  }
+}
+
+template <typename T, typename R, bool MX8, int LPR, int P, int RB, bool NT, int MAXT>
+__global__ void __launch_bounds__(MAXT) add_norm_fwd_kernel(AddNormArgs a) {
+  __shared__ float red[2][LPR == 64 ? 16 : 1][RB];
+  const int waves = a.waves;                         // of a row; 1: rows of LPR lanes
+  const int per = waves > 1 ? 1 : blockDim.x / LPR;  // rows side by side in a workgroup
+  const int i = waves > 1 ? threadIdx.x : threadIdx.x % LPR;
+  Cols at[P];
+  cols<P>(at, i, waves > 1 ? blockDim.x : LPR, a.n);
+  f8 w[P];
+  weights<P>(w, a.w, at);
+  const float inv = 1.f / (float)a.n;
+  const int64_t step = (int64_t)gridDim.x * per * RB;
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * per * RB; r0 < a.rows; r0 += step, turn ^= 1) {
+    const int64_t r1 = r0 + (waves > 1 ? 0 : threadIdx.x / LPR);
+    Raw8<T> x[RB][P];
+    Raw8<R> s[RB][P];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      const int64_t r = r1 + b * per, rr = r < a.rows ? r : a.rows - 1;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        x[b][p] = ask8<T, NT>((const T*)a.x + rr * a.ldx + at[p].c);
+        if (a.res) s[b][p] = ask8<R, NT>((const R*)a.res + rr * a.ldr + at[p].c);
+      }
+    }
+    f8 v[RB][P];
+    float ss[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      ss[b] = 0.f;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        v[b][p] = raw_f8(x[b][p]);
+        if (a.res) {
+          const f8 u = raw_f8(s[b][p]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[b][p].v[j] += u.v[j];
+        }
+        float q = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q += v[b][p].v[j] * v[b][p].v[j];
+        ss[b] += at[p].in ? q : 0.f;
+      }
+    }
+    row_sums<LPR, RB>(ss, red[turn], waves);
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      const int64_t r = r1 + b * per;
+      const float rho = rsqrtf(ss[b] * inv + a.eps);
+      if (r < a.rows) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          if (!at[p].in) continue;
+          if (a.h) put8<R, NT>((R*)a.h + r * a.ldh + at[p].c, v[b][p]);
+          f8 y;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y.v[j] = v[b][p].v[j] * rho * w[p].v[j];
+          if constexpr (MX8) {
+            int e;
+            const uint2 q = to_mx8(y, &e);
+            *(uint2*)((uint8_t*)a.y + r * a.ldy + at[p].c) = q;
+            if (i % 4 == 0) a.scale[r * a.lds + at[p].c / 32] = (uint8_t)e;
+          } else {
+            put8<T, NT>((T*)a.y + r * a.ldy + at[p].c, y);
+          }
+        }
       }
     }
   }
@@ -99,138 +173,183 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) add_norm_fwd_kernel
 
 // With n = h rho and dn = dy (1 + w):
 //   d = dh + rho (dn - n mean(dn n)),  dw = sum over rows of dy n.
-// A block walks rows and keeps its dw in registers; the blocks' partial sums
-// are added in a fixed order.
-template <typename T, typename R, int WPR, int P>
-__global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) add_norm_bwd_kernel(AddNormBwdArgs a) {
-  constexpr int TPR = 64 * WPR, GROUPS = WPR == 1 ? 4 : 1;
-  __shared__ float red[2][WPR == 1 ? 1 : WPR];
-  __shared__ float4 dws[GROUPS == 1 ? 1 : 3][GROUPS == 1 ? 1 : 2][TPR];
-  const int i = threadIdx.x % TPR, g = threadIdx.x / TPR;
-  f8 dw[P];
+// A workgroup walks rows and keeps its dw in registers; the workgroups' partial
+// sums are added in a fixed order.
+template <typename T, typename R, int LPR, int P, int RB, bool NT, int MAXT, bool PF>
+__global__ void __launch_bounds__(MAXT) add_norm_bwd_kernel(AddNormBwdArgs a) {
+  __shared__ float red[2][LPR == 64 ? 16 : 1][2 * RB];
+  __shared__ float dws[MAXT == 256 ? 256 : 1][8 * P + 1];
+  const int waves = a.waves;
+  const int per = waves > 1 ? 1 : blockDim.x / LPR;
+  const int i = waves > 1 ? threadIdx.x : threadIdx.x % LPR;
+  Cols at[P];
+  cols<P>(at, i, waves > 1 ? blockDim.x : LPR, a.n);
+  f8 w[P], dw[P];
+  if (P == 1) weights<P>(w, a.w, at);  // twice as many columns leave no registers: read where needed
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[p].v[j] = 0.f;
-  for (int64_t r = (int64_t)blockIdx.x * GROUPS + g; r < a.rows; r += (int64_t)gridDim.x * GROUPS) {
-    const R* h = (const R*)a.h + r * a.ldh;
-    const T* dy = (const T*)a.dy + r * a.lddy;
-    f8 hv[P], dv[P];
-    float ss = 0.f, sd = 0.f;
+  const float inv = 1.f / (float)a.n;
+  const int64_t step = (int64_t)gridDim.x * per * RB;
+  int turn = 0;
+  const int64_t first = (int64_t)blockIdx.x * per * RB + (waves > 1 ? 0 : threadIdx.x / LPR);
+  struct Batch {
+    Raw8<R> h[RB][P], up[RB][P];
+    Raw8<T> dy[RB][P];
+  } next;
+  const auto ask = [&](Batch& to, int64_t r1) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int c = (p * TPR + i) * 8;
-      if (c < a.n) {
-        hv[p] = load8(h + c);
-        dv[p] = load8(dy + c);
-        const f8 w = load8(a.w + c);
+    for (int b = 0; b < RB; ++b) {
+      const int64_t r = r1 + b * per, rr = r < a.rows ? r : a.rows - 1;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        to.h[b][p] = ask8<R, NT>((const R*)a.h + rr * a.ldh + at[p].c);
+        to.dy[b][p] = ask8<T, NT>((const T*)a.dy + rr * a.lddy + at[p].c);
+        if (a.dh) to.up[b][p] = ask8<R, NT>((const R*)a.dh + rr * a.lddh + at[p].c);
+      }
+    }
+  };
+  if (PF) ask(next, first);
+  for (int64_t r0 = (int64_t)blockIdx.x * per * RB; r0 < a.rows; r0 += step, turn ^= 1) {
+    const int64_t r1 = r0 + first - (int64_t)blockIdx.x * per * RB;
+    Batch now;
+    if (PF) {
+      now = next;
+      if (r0 + step < a.rows) ask(next, r1 + step);
+    } else {
+      ask(now, r1);
+    }
+    const auto& h = now.h;
+    const auto& dy = now.dy;
+    const auto& up = now.up;
+    float sums[2 * RB];                // h^2 and dn h
+    if (P > 1) weights<P>(w, a.w, at);
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      sums[2 * b] = sums[2 * b + 1] = 0.f;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const f8 hv = raw_f8(h[b][p]), dv = raw_f8(dy[b][p]);
+        float q = 0.f, g = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          ss += hv[p].v[j] * hv[p].v[j];
-          sd += dv[p].v[j] * (1.f + w.v[j]) * hv[p].v[j];
+          q += hv.v[j] * hv.v[j];
+          g += dv.v[j] * w[p].v[j] * hv.v[j];
+        }
+        sums[2 * b] += at[p].in ? q : 0.f;
+        sums[2 * b + 1] += at[p].in ? g : 0.f;
+      }
+    }
+    row_sums<LPR, 2 * RB>(sums, red[turn], waves);
+    if (P > 1) weights<P>(w, a.w, at);
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      const int64_t r = r1 + b * per;
+      const float rho = rsqrtf(sums[2 * b] * inv + a.eps);
+      const float m = sums[2 * b + 1] * rho * inv;      // mean(dn n)
+      if (r < a.rows) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const f8 hv = raw_f8(h[b][p]), dv = raw_f8(dy[b][p]);
+          f8 d;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float n = hv.v[j] * rho;
+            d.v[j] = rho * (dv.v[j] * w[p].v[j] - n * m);
+            dw[p].v[j] += dv.v[j] * n;
+          }
+          if (!at[p].in) continue;
+          if (a.dh) {
+            const f8 u = raw_f8(up[b][p]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d.v[j] += u.v[j];
+          }
+          if (a.dx) put8<T, NT>((T*)a.dx + r * a.lddx + at[p].c, d);
+          if (a.dres) put8<R, NT>((R*)a.dres + r * a.lddr + at[p].c, d);
         }
       }
     }
-    ss = group_sum<WPR>(ss, red[0]);
-    sd = group_sum<WPR>(sd, red[1]);
-    const float rho = rsqrtf(ss / (float)a.n + a.eps);
-    const float m = sd * rho / (float)a.n;     // mean(dn n)
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int c = (p * TPR + i) * 8;
-      if (c < a.n) {
-        const f8 w = load8(a.w + c);
-        f8 d;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float n = hv[p].v[j] * rho;
-          d.v[j] = rho * (dv[p].v[j] * (1.f + w.v[j]) - n * m);
-          dw[p].v[j] += dv[p].v[j] * n;
-        }
-        if (a.dh) {
-          const f8 u = load8((const R*)a.dh + r * a.lddh + c);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) d.v[j] += u.v[j];
-        }
-        if (a.dx) store8((T*)a.dx + r * a.lddx + c, d);
-        if (a.dres) store8((R*)a.dres + r * a.lddr + c, d);
-      }
-    }
-    if constexpr (WPR > 1) __syncthreads();    // red is written again
   }
   if (!a.partials) return;
-  if constexpr (GROUPS > 1) {                  // the four waves' sums, in wave order
+  if constexpr (MAXT == 256) {         // rows side by side: their sums, in order
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      if (g > 0) {
-        dws[g - 1][0][i] = make_float4(dw[p].v[0], dw[p].v[1], dw[p].v[2], dw[p].v[3]);
-        dws[g - 1][1][i] = make_float4(dw[p].v[4], dw[p].v[5], dw[p].v[6], dw[p].v[7]);
-      }
-      __syncthreads();
-      if (g == 0) {
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int k = 0; k < GROUPS - 1; ++k) {
-          const float4 lo = dws[k][0][i], hi = dws[k][1][i];
-          dw[p].v[0] += lo.x; dw[p].v[1] += lo.y; dw[p].v[2] += lo.z; dw[p].v[3] += lo.w;
-          dw[p].v[4] += hi.x; dw[p].v[5] += hi.y; dw[p].v[6] += hi.z; dw[p].v[7] += hi.w;
-        }
-      }
-      __syncthreads();
-    }
+      for (int j = 0; j < 8; ++j) dws[threadIdx.x][8 * p + j] = dw[p].v[j];
+    __syncthreads();
+    if (threadIdx.x >= LPR) return;
+    for (int u = 1; u < per; ++u)
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[p].v[j] += dws[u * LPR + i][8 * p + j];
   }
-  if (g == 0) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int c = (p * TPR + i) * 8;
-      if (c < a.n) store8(a.partials + (int64_t)blockIdx.x * a.n + c, dw[p]);
-    }
-  }
+  for (int p = 0; p < P; ++p)
+    if (at[p].in) store8(a.partials + (int64_t)blockIdx.x * a.n + at[p].c, dw[p]);
 }
 
+static int norm_waves(int n) { return n <= 512 ? 1 : n <= 8192 ? (n + 511) / 512 : 16; }
+static int norm_lanes(int n) { return n <= 64 ? 8 : n <= 256 ? 32 : 64; }
+
+// Workgroups of the backward: about ten to sixteen waves a CU.  More only add
+// partial sums of dw, fewer leave loads unasked.  Measured, us by workgroups
+// 256 / 512 / 1024: 16384 x 1000 - / 28 / 25, 16384 x 2560 - / 54.6 / 65,
+// 3001 x 8192 34 / 38 / 43 (bf16).
 int64_t add_norm_blocks(int64_t rows, int32_t n) {
-  const int64_t b = n <= ADD_NORM_WAVE ? (rows + 3) / 4 : rows;
-  return b < ADD_NORM_BLOCKS_MAX ? b : ADD_NORM_BLOCKS_MAX;
+  const int64_t per = n <= 512 ? 256 / norm_lanes(n) : 1, b = (rows + per - 1) / per;
+  const int64_t most = n <= 1024 ? 1024 : n <= 4096 ? 512 : 256;
+  return b < most ? b : most;
 }
 
-template <typename T, typename R, bool MX8, int WPR, int P>
-static hipError_t fwd_go(const AddNormArgs& a, hipStream_t st) {
-  // a launch holds fewer than 2^32 threads
-  constexpr int64_t G = WPR == 1 ? 4 : 1, STEP = (int64_t)1 << 20;
-  for (int64_t r0 = 0; r0 < a.rows; r0 += STEP) {
-    AddNormArgs b = a;
-    b.rows = a.rows - r0 < STEP ? a.rows - r0 : STEP;
-    b.x = (const T*)a.x + r0 * a.ldx;
-    if (a.res) b.res = (const R*)a.res + r0 * a.ldr;
-    if (a.h) b.h = (R*)a.h + r0 * a.ldh;
-    b.y = MX8 ? (void*)((uint8_t*)a.y + r0 * a.ldy) : (void*)((T*)a.y + r0 * a.ldy);
-    if (MX8) b.scale = a.scale + r0 * a.lds;
-    hipLaunchKernelGGL((add_norm_fwd_kernel<T, R, MX8, WPR, P>), dim3((unsigned)((b.rows + G - 1) / G)),
-                       dim3(WPR == 1 ? 256 : 64 * WPR), 0, st, b);
-  }
+template <typename T, typename R, bool MX8, int LPR, int P, int RB, bool NT, int MAXT>
+static hipError_t fwd_go(AddNormArgs a, hipStream_t st) {
+  a.waves = norm_waves(a.n);
+  const int threads = a.waves > 1 ? 64 * a.waves : 256, per = a.waves > 1 ? 1 : 256 / LPR;
+  // one batch a workgroup; a launch holds fewer than 2^32 threads
+  const int64_t b = (a.rows + per * RB - 1) / (per * RB), most = 1 << 21;
+  hipLaunchKernelGGL((add_norm_fwd_kernel<T, R, MX8, LPR, P, RB, NT, MAXT>), dim3((unsigned)(b < most ? b : most)),
+                     dim3(threads), 0, st, a);
   return hipGetLastError();
 }
 
+// Few rows: one at a time, for latency (16 rows of 2560: 2.9 us, two at a time
+// 3.3).  Many: two at a time and non-temporal, since nothing of them is still
+// cached when it is read again (65536 x 2560, bf16: one 220, two 210, four
+// 216 us, two without the hint 259; a fixed grid that walks rows 224 to 247).
+// Rows of more than eight waves one at a time (8192 x 8192: 88 us).
 template <typename T, typename R, bool MX8>
 static hipError_t fwd_n(const AddNormArgs& a, hipStream_t st) {
-  if (a.n <= 1024) return fwd_go<T, R, MX8, 1, 2>(a, st);
-  if (a.n <= ADD_NORM_WAVE) return fwd_go<T, R, MX8, 1, 5>(a, st);
-  if (a.n <= 8192) return fwd_go<T, R, MX8, 4, 4>(a, st);
-  return fwd_go<T, R, MX8, 16, 2>(a, st);
+  if (a.n <= 64) return fwd_go<T, R, MX8, 8, 1, 1, false, 256>(a, st);
+  if (a.n <= 256) return fwd_go<T, R, MX8, 32, 1, 1, false, 256>(a, st);
+  if (a.n <= 512) return fwd_go<T, R, MX8, 64, 1, 1, false, 256>(a, st);
+  if (a.n > 8192) return fwd_go<T, R, MX8, 64, 2, 1, true, 1024>(a, st);
+  if (a.rows <= 2048) return fwd_go<T, R, MX8, 64, 1, 1, false, 1024>(a, st);
+  if (a.n > 4096) return fwd_go<T, R, MX8, 64, 1, 1, true, 1024>(a, st);
+  return fwd_go<T, R, MX8, 64, 1, 2, true, 512>(a, st);
 }
 
-template <typename T, typename R, int WPR, int P>
-static hipError_t bwd_go(const AddNormBwdArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((add_norm_bwd_kernel<T, R, WPR, P>), dim3((unsigned)add_norm_blocks(a.rows, a.n)),
-                     dim3(WPR == 1 ? 256 : 64 * WPR), 0, st, a);
+template <typename T, typename R, int LPR, int P, int RB, bool NT, int MAXT, bool PF>
+static hipError_t bwd_go(AddNormBwdArgs a, hipStream_t st) {
+  a.waves = norm_waves(a.n);
+  hipLaunchKernelGGL((add_norm_bwd_kernel<T, R, LPR, P, RB, NT, MAXT, PF>), dim3((unsigned)add_norm_blocks(a.rows, a.n)),
+                     dim3(a.waves > 1 ? 64 * a.waves : 256), 0, st, a);
   return hipGetLastError();
 }
 
+// One workgroup of wide rows fills a CU, so that it has to ask for its next row
+// itself (3001 x 8192: 34 us, 39 without); of narrower ones there are several,
+// and two rows at a time are better (16384 x 2560: 54.6 us; one and the next
+// 58.5, four 109).
 template <typename T, typename R>
 static hipError_t bwd_n(const AddNormBwdArgs& a, hipStream_t st) {
-  if (a.n <= 1024) return bwd_go<T, R, 1, 2>(a, st);
-  if (a.n <= ADD_NORM_WAVE) return bwd_go<T, R, 1, 5>(a, st);
-  if (a.n <= 8192) return bwd_go<T, R, 4, 4>(a, st);
-  return bwd_go<T, R, 16, 2>(a, st);
+  if (a.n <= 64) return bwd_go<T, R, 8, 1, 1, false, 256, false>(a, st);
+  if (a.n <= 256) return bwd_go<T, R, 32, 1, 1, false, 256, false>(a, st);
+  if (a.n <= 512) return bwd_go<T, R, 64, 1, 1, false, 256, false>(a, st);
+  if (a.n > 8192) return bwd_go<T, R, 64, 2, 1, true, 1024, false>(a, st);
+  if (a.n > 4096) return bwd_go<T, R, 64, 1, 1, true, 1024, true>(a, st);
+  return bwd_go<T, R, 64, 1, 2, true, 512, false>(a, st);
 }
 
 template <bool MX8> static hipError_t fwd_t(const AddNormArgs& a, hipStream_t st) {

@@ -164,6 +164,7 @@ struct AddNormArgs {
   void *h, *y;
   uint8_t* scale;
   int64_t ldx, ldr, ldh, ldy, lds;
+  int waves;                                     // of a row, set by the launcher
 };
 struct AddNormBwdArgs {
   int64_t rows;
@@ -175,10 +176,9 @@ struct AddNormBwdArgs {
   void *dx, *dres;
   float *dw, *partials;                          // partials: NULL where dw is
   int64_t ldh, lddy, lddh, lddx, lddr;
+  int waves;
 };
 constexpr int ADD_NORM_MAX = 16384;              // widest row
-constexpr int ADD_NORM_WAVE = 2560;              // widest row that one wave holds
-constexpr int64_t ADD_NORM_BLOCKS_MAX = 1024;    // blocks of the backward, each with partial sums of dw
 int64_t add_norm_blocks(int64_t rows, int32_t n);
 hipError_t launch_add_norm_fwd(const AddNormArgs& a, hipStream_t st);
 hipError_t launch_add_norm_bwd(const AddNormBwdArgs& a, hipStream_t st);
