@@ -193,6 +193,7 @@ struct W4Args {
   int64_t scales_at;
   void* y;
   int64_t ldx, ldxs, ldy;
+  int64_t row_blocks;                            // set by the launcher
 };
 size_t w4_bytes(int n, int k);
 int64_t w4_scales_at(int n, int k);

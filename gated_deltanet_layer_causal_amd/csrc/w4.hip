@@ -263,11 +263,16 @@ __global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
   const int kt = w4_ktiles(a.k), tiles = (a.n + 15) / 16;
   const int steps_all = (a.k * S::E + 511) / 512;      // of 512 bytes of a row
   const int steps = (steps_all + WK - 1) / WK;         // a group's, the last one's perhaps empty
-  const int n0 = (blockIdx.x * WN + wn) * NT;
+  // Workgroups go to the eight XCDs in turn.  Those of one piece of outputs and
+  // all pieces of rows follow each other on one of them, so that its L2 serves
+  // the weights but once (16480 x 2560, 64 8-bit rows in 32s: 11.6 -> 9.4 us).
+  const int64_t turn = blockIdx.x / 8, block = turn / a.row_blocks * 8 + blockIdx.x % 8;
+  const int n0 = (int)((block * WN + wn) * NT);
+  if (block * WN * NT >= tiles) return;       // the whole workgroup
   const uint4* codes = (const uint4*)a.packed + lane;
   const uint32_t* scales = (const uint32_t*)((const uint8_t*)a.packed + a.scales_at) + lane;
 
-  for (int64_t m0 = (int64_t)blockIdx.y * 16 * MT; m0 < a.rows; m0 += (int64_t)gridDim.y * 16 * MT) {
+  for (int64_t m0 = turn % a.row_blocks * 16 * MT; m0 < a.rows; m0 += a.row_blocks * 16 * MT) {
     const uint8_t* xrow[NL];
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
@@ -553,31 +558,43 @@ static hipError_t w4_go(const W4Args& a, hipStream_t st) {
 }
 
 template <typename X, typename Y, int WN, int WK, int NT, int MT>
-static hipError_t w4_rows_go(const W4Args& a, hipStream_t st) {
-  const int64_t mb = (a.rows + 16 * MT - 1) / (16 * MT), nb = ((a.n + 15) / 16 + NT * WN - 1) / (NT * WN);
-  int64_t most = ((int64_t)1 << 31) / (nb * 64 * WN * WK);
-  most = most < 1 ? 1 : most < 65535 ? most : 65535;
-  hipLaunchKernelGGL((w4_rows_kernel<X, Y, WN, WK, NT, MT>), dim3((unsigned)nb, (unsigned)(mb < most ? mb : most)),
-                     dim3(64 * WN * WK), 0, st, a);
+static hipError_t w4_rows_go(const W4Args& args, hipStream_t st) {
+  W4Args a = args;
+  const int64_t mb = (a.rows + 16 * MT - 1) / (16 * MT), nb = (((a.n + 15) / 16 + NT * WN - 1) / (NT * WN) + 7) / 8 * 8;
+  const int64_t most = ((int64_t)1 << 31) / (nb * 64 * WN * WK);
+  a.row_blocks = mb < most ? mb : most < 1 ? 1 : most;
+  hipLaunchKernelGGL((w4_rows_kernel<X, Y, WN, WK, NT, MT>), dim3((unsigned)(nb * a.row_blocks)), dim3(64 * WN * WK), 0,
+                     st, a);
   return hipGetLastError();
 }
 
-// Measured, us a launch; outputs x inputs 2560 x 6144 / 16480 x 2560 / 20480 x 8192:
-//                                    bf16 rows                8-bit rows
-//   1 row     every wave its inputs  4.0 /  6.9 / 24          3.5 /  6.6 / 21
-//             staged, 4 side by side 11  /  7.2 / 21 (2 sets) 9.0 /  6.3 / 19
-//   16 rows   every wave its inputs  8.0 / 15   / 49          6.8 / 10   / 38
-//             2 side by side, 4 sets 7.4 / 10   / 24          5.1 / 12   / 22
-//             4 side by side         11  /  7.5 / 21 (2 sets) 9.0 /  6.6 / 20
-//   64 rows   4 side by side, by 16  15  / 20   / 49          9.0 / 17   / 39
-//                             by 32  19  / 15   / 41          11  / 12   / 29
-//                             by 64  31  / 18   / 51          18  / 11   / 34
-//             2 side by side, 4 sets 9.8 / 26   / 61          8.6 / 35   / 71
-// So: where tiles of outputs are fewer than two a CU, the inputs are shared out
-// over more waves; single rows need no staging there.
+// A unit is a tile of 16 outputs by one of 16 rows.  The inputs are shared out
+// over as many waves a unit as leave all waves on the chip at once (about 16 a
+// CU, 12 with 8-bit rows); beyond that, workgroups take 32 rows.  Fewer waves
+// a unit leave CUs idle, more wait for a second round.  Measured, us a launch
+// (outputs x inputs, rows: units; each with 4, 2 and 1 waves a unit, and with
+// 1 and 32 rows):
+//   bf16   2560 x 8192,  32:  320   9.4  14.0  19.6  25.9
+//         10240 x 8192,  16:  640  13.8  16.2  21.2
+//         10240 x 2560,  16:  640   7.1   6.6   8.1
+//         10240 x 8192,  48: 1920  23.6  18.4  21.8  31.3
+//         16480 x 2560,  48: 3090  18.5  13.0  11.3  13.9
+//         20480 x 8192,  64: 5120  55.8  48.3  48.8  40.8
+//   8 bit  2560 x 8192,  32:  320   6.4   9.2  11.4  14.1
+//         10240 x 8192,  48: 1920  21.9  12.8  13.4  17.2
+//         10240 x 2560,  48: 1920  15.4   6.9   6.0   7.3
+//         16480 x 2560,  64: 4120  31.4  14.4  10.1   9.4
+// Up to 12 rows by few outputs want no staging at all: 1 row of bf16 by
+// 2560 x 6144 takes 4.0 us with a wave for each 512 inputs, 7.3 staged; 12 rows
+// 7.0 and 7.4.
 template <typename X, typename Y> static hipError_t w4_m(const W4Args& a, hipStream_t st) {
-  if (a.n <= 16 * 512) return a.rows <= 12 ? w4_go<X, Y, 1, 1, 16>(a, st) : w4_rows_go<X, Y, 2, 4, 1, 1>(a, st);
-  if (a.rows <= 16) return w4_rows_go<X, Y, 4, __is_same(X, Mx8) ? 1 : 2, 1, 1>(a, st);
+  constexpr bool MX = __is_same(X, Mx8);
+  const int64_t tiles = (a.n + 15) / 16, units = tiles * ((a.rows + 15) / 16);
+  const bool deep = a.k >= 4096;
+  if (tiles <= 512 && a.rows <= 12) return w4_go<X, Y, 1, 1, 16>(a, st);
+  if (units <= 512 || (!MX && units <= 1024 && deep)) return w4_rows_go<X, Y, 2, 4, 1, 1>(a, st);
+  if (units <= 1024 || (units <= 2048 && (!MX || deep))) return w4_rows_go<X, Y, 4, 2, 1, 1>(a, st);
+  if (units <= 4096) return w4_rows_go<X, Y, 4, 1, 1, 1>(a, st);
   return w4_rows_go<X, Y, 4, 1, 1, 2>(a, st);
 }
 
