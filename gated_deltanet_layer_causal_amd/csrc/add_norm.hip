@@ -4,7 +4,7 @@
 // written once.  The norm reads the sum before h is rounded to its storage
 // type, so y carries one rounding.
 //
-// A thread owns 8 columns (two times 8 beyond 8192) for the whole call, with
+// A thread owns 8 columns (16 beyond 8192) for the whole call, with
 // their weights in registers, and takes RB rows at a time, so that the loads
 // of RB rows are on their way together (PF: the next rows' while these are
 // worked on).  A row is owned by LPR lanes, or by all
@@ -36,79 +36,105 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N], int wav
   }
 }
 
-// 8 values of a group of 32 columns (4 adjacent lanes) in e4m3 under the
-// smallest power of two that keeps the group within 448 = 0.875 * 2^9.
-// NaN stays NaN and leaves the scale to the others; infinities become NaN.
-__device__ __forceinline__ uint2 to_mx8(const f8& v, int* scale) {
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v.v[i]));
-  amax = fmaxf(amax, dpp_f<0xB1>(amax));
-  amax = fmaxf(amax, dpp_f<0x4E>(amax));
+// e4m3 under the smallest power of two that keeps a group's largest within
+// 448 = 0.875 * 2^9.  NaN stays NaN and leaves the scale to the others;
+// infinities become NaN.
+__device__ __forceinline__ int mx8_exponent(float amax) {
   int e = __builtin_amdgcn_frexp_expf(amax) - 9 + (__builtin_amdgcn_frexp_mantf(amax) > 0.875f);
   if (amax == 0.f) e = -127;
   if (__builtin_isinf(amax)) e = 127;
-  e = e < -127 ? -127 : e > 127 ? 127 : e;
-  *scale = e + 127;
-  float q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = ldexpf(v.v[i], -e);
-  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
-  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
-  return make_uint2((uint32_t)lo, (uint32_t)hi);
+  return e < -127 ? -127 : e > 127 ? 127 : e;
+}
+__device__ __forceinline__ float amax4(const float* v) {
+  return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+}
+__device__ __forceinline__ uint32_t mx8_word(const float* v, int e) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(ldexpf(v[0], -e), ldexpf(v[1], -e), 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(ldexpf(v[2], -e), ldexpf(v[3], -e), lo, true);
 }
 
-template <typename T, bool NT> __device__ __forceinline__ Raw8<T> ask8(const T* p) {
-  if constexpr (NT) {
-    Raw8<T> r;
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-      r.v[i] = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const nt_u32x4*>(p) + i));
-    return r;
-  } else {
-    return ld_raw8(p);
-  }
-}
-template <typename T, bool NT> __device__ __forceinline__ void put8(T* p, const f8& v) {
-  if constexpr (NT) store8_nt(p, v);
-  else store8(p, v);
-}
-
-// The columns of piece p of a thread, and whether they are in the row (those
-// that are not read the first ones and count for nothing).
+// A thread's columns of piece p.  Where all tensors are 16-bit: 8 adjacent
+// ones, a 16-byte access.  Where one is fp32: two runs of 4, as far apart as
+// the row's threads reach, so that an access of 16 bytes a lane leaves no gaps
+// between lanes; with 8 adjacent columns each access would touch every other
+// 16 bytes (32768 x 2560 in
+// fp32: 250 us, in runs 218; backward 281 and 235).
 struct Cols {
-  int c;
-  bool in;
+  int a, b;
+  bool in_a, in_b;       // columns that are not in the row read its first ones and count for nothing
 };
-template <int P> __device__ __forceinline__ void cols(Cols (&at)[P], int i, int threads, int n) {
+template <bool SPLIT, int P> __device__ __forceinline__ void cols(Cols (&at)[P], int i, int threads, int n) {
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int c = (p * threads + i) * 8;
-    at[p].in = c < n;
-    at[p].c = at[p].in ? c : 0;
+    const int a = SPLIT ? (2 * p * threads + i) * 4 : (p * threads + i) * 8;
+    const int b = SPLIT ? a + threads * 4 : a + 4;
+    at[p].in_a = a < n;
+    at[p].in_b = b < n;
+    at[p].a = at[p].in_a ? a : 0;
+    at[p].b = at[p].in_b ? b : SPLIT ? 0 : 4;
   }
 }
-template <int P> __device__ __forceinline__ void weights(f8 (&w)[P], const float* wp, const Cols (&at)[P]) {
+
+template <typename V, bool NT> __device__ __forceinline__ V ask(const void* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+  else return *reinterpret_cast<const V*>(p);
+}
+template <typename V, bool NT> __device__ __forceinline__ void put(void* p, V v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
+  else *reinterpret_cast<V*>(p) = v;
+}
+typedef uint32_t nt_u32x2 __attribute__((ext_vector_type(2)));
+
+template <typename T, bool SPLIT, bool NT> __device__ __forceinline__ Raw8<T> ask8(const T* row, const Cols& at) {
+  Raw8<T> r;
+  if constexpr (sizeof(T) == 4) {
+    r.v[0] = __builtin_bit_cast(uint4, ask<nt_u32x4, NT>(row + at.a));
+    r.v[1] = __builtin_bit_cast(uint4, ask<nt_u32x4, NT>(row + at.b));
+  } else if constexpr (SPLIT) {
+    const nt_u32x2 a = ask<nt_u32x2, NT>(row + at.a), b = ask<nt_u32x2, NT>(row + at.b);
+    r.v[0] = make_uint4(a[0], a[1], b[0], b[1]);
+  } else {
+    r.v[0] = __builtin_bit_cast(uint4, ask<nt_u32x4, NT>(row + at.a));
+  }
+  return r;
+}
+template <typename T, bool SPLIT, bool NT> __device__ __forceinline__ void put8(T* row, const Cols& at, const f8& v) {
+  Raw8<T> r;
+  store8(reinterpret_cast<T*>(&r.v[0]), v);
+  if constexpr (sizeof(T) == 4) {
+    if (at.in_a) put<nt_u32x4, NT>(row + at.a, __builtin_bit_cast(nt_u32x4, r.v[0]));
+    if (at.in_b) put<nt_u32x4, NT>(row + at.b, __builtin_bit_cast(nt_u32x4, r.v[1]));
+  } else if constexpr (SPLIT) {
+    if (at.in_a) put<nt_u32x2, NT>(row + at.a, nt_u32x2{r.v[0].x, r.v[0].y});
+    if (at.in_b) put<nt_u32x2, NT>(row + at.b, nt_u32x2{r.v[0].z, r.v[0].w});
+  } else {
+    if (at.in_a) put<nt_u32x4, NT>(row + at.a, __builtin_bit_cast(nt_u32x4, r.v[0]));
+  }
+}
+template <bool SPLIT, int P> __device__ __forceinline__ void weights(f8 (&w)[P], const float* wp, const Cols (&at)[P]) {
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    w[p] = load8(wp + at[p].c);
+    w[p] = raw_f8(ask8<float, SPLIT, false>(wp, at[p]));
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[p].v[j] += 1.f;
   }
 }
+// The parts of a sum over a piece that are in the row.
+__device__ __forceinline__ float in_row(const Cols& at, float a, float b) {
+  return (at.in_a ? a : 0.f) + (at.in_b ? b : 0.f);
+}
 
 template <typename T, typename R, bool MX8, int LPR, int P, int RB, bool NT, int MAXT>
 __global__ void __launch_bounds__(MAXT) add_norm_fwd_kernel(AddNormArgs a) {
+  constexpr bool SPLIT = sizeof(T) == 4 || sizeof(R) == 4;
   __shared__ float red[2][LPR == 64 ? 16 : 1][RB];
   const int waves = a.waves;                         // of a row; 1: rows of LPR lanes
   const int per = waves > 1 ? 1 : blockDim.x / LPR;  // rows side by side in a workgroup
   const int i = waves > 1 ? threadIdx.x : threadIdx.x % LPR;
   Cols at[P];
-  cols<P>(at, i, waves > 1 ? blockDim.x : LPR, a.n);
+  cols<SPLIT, P>(at, i, waves > 1 ? blockDim.x : LPR, a.n);
   f8 w[P];
-  weights<P>(w, a.w, at);
+  weights<SPLIT, P>(w, a.w, at);
   const float inv = 1.f / (float)a.n;
   const int64_t step = (int64_t)gridDim.x * per * RB;
   int turn = 0;
@@ -121,8 +147,8 @@ __global__ void __launch_bounds__(MAXT) add_norm_fwd_kernel(AddNormArgs a) {
       const int64_t r = r1 + b * per, rr = r < a.rows ? r : a.rows - 1;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        x[b][p] = ask8<T, NT>((const T*)a.x + rr * a.ldx + at[p].c);
-        if (a.res) s[b][p] = ask8<R, NT>((const R*)a.res + rr * a.ldr + at[p].c);
+        x[b][p] = ask8<T, SPLIT, NT>((const T*)a.x + rr * a.ldx, at[p]);
+        if (a.res) s[b][p] = ask8<R, SPLIT, NT>((const R*)a.res + rr * a.ldr, at[p]);
       }
     }
     f8 v[RB][P];
@@ -138,10 +164,13 @@ __global__ void __launch_bounds__(MAXT) add_norm_fwd_kernel(AddNormArgs a) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[b][p].v[j] += u.v[j];
         }
-        float q = 0.f;
+        float qa = 0.f, qb = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q += v[b][p].v[j] * v[b][p].v[j];
-        ss[b] += at[p].in ? q : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          qa += v[b][p].v[j] * v[b][p].v[j];
+          qb += v[b][p].v[j + 4] * v[b][p].v[j + 4];
+        }
+        ss[b] += in_row(at[p], qa, qb);
       }
     }
     row_sums<LPR, RB>(ss, red[turn], waves);
@@ -152,18 +181,40 @@ __global__ void __launch_bounds__(MAXT) add_norm_fwd_kernel(AddNormArgs a) {
       if (r < a.rows) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          if (!at[p].in) continue;
-          if (a.h) put8<R, NT>((R*)a.h + r * a.ldh + at[p].c, v[b][p]);
+          if (a.h) put8<R, SPLIT, NT>((R*)a.h + r * a.ldh, at[p], v[b][p]);
           f8 y;
 #pragma unroll
           for (int j = 0; j < 8; ++j) y.v[j] = v[b][p].v[j] * rho * w[p].v[j];
-          if constexpr (MX8) {
-            int e;
-            const uint2 q = to_mx8(y, &e);
-            *(uint2*)((uint8_t*)a.y + r * a.ldy + at[p].c) = q;
-            if (i % 4 == 0) a.scale[r * a.lds + at[p].c / 32] = (uint8_t)e;
+          if constexpr (MX8) {         // groups of 32 columns: 4 adjacent lanes, or 8 of each run
+            uint8_t* q = (uint8_t*)a.y + r * a.ldy;
+            uint8_t* scale = a.scale + r * a.lds;
+            float ma = amax4(y.v), mb = amax4(y.v + 4);
+            if (!SPLIT) ma = mb = fmaxf(ma, mb);
+            ma = fmaxf(ma, dpp_f<0xB1>(ma));
+            ma = fmaxf(ma, dpp_f<0x4E>(ma));
+            if (SPLIT) {
+              ma = fmaxf(ma, dpp_f<0x141>(ma));
+              mb = fmaxf(mb, dpp_f<0xB1>(mb));
+              mb = fmaxf(mb, dpp_f<0x4E>(mb));
+              mb = fmaxf(mb, dpp_f<0x141>(mb));
+            }
+            const int ea = mx8_exponent(ma), eb = SPLIT ? mx8_exponent(mb) : ea;
+            const uint32_t wa = mx8_word(y.v, ea), wb = mx8_word(y.v + 4, eb);
+            if constexpr (SPLIT) {
+              if (at[p].in_a) {
+                *(uint32_t*)(q + at[p].a) = wa;
+                if (i % 8 == 0) scale[at[p].a / 32] = (uint8_t)(ea + 127);
+              }
+              if (at[p].in_b) {
+                *(uint32_t*)(q + at[p].b) = wb;
+                if (i % 8 == 0) scale[at[p].b / 32] = (uint8_t)(eb + 127);
+              }
+            } else if (at[p].in_a) {
+              *(uint2*)(q + at[p].a) = make_uint2(wa, wb);
+              if (i % 4 == 0) scale[at[p].a / 32] = (uint8_t)(ea + 127);
+            }
           } else {
-            put8<T, NT>((T*)a.y + r * a.ldy + at[p].c, y);
+            put8<T, SPLIT, NT>((T*)a.y + r * a.ldy, at[p], y);
           }
         }
       }
@@ -177,15 +228,16 @@ __global__ void __launch_bounds__(MAXT) add_norm_fwd_kernel(AddNormArgs a) {
 // sums are added in a fixed order.
 template <typename T, typename R, int LPR, int P, int RB, bool NT, int MAXT, bool PF>
 __global__ void __launch_bounds__(MAXT) add_norm_bwd_kernel(AddNormBwdArgs a) {
+  constexpr bool SPLIT = sizeof(T) == 4 || sizeof(R) == 4;
   __shared__ float red[2][LPR == 64 ? 16 : 1][2 * RB];
   __shared__ float dws[MAXT == 256 ? 256 : 1][8 * P + 1];
   const int waves = a.waves;
   const int per = waves > 1 ? 1 : blockDim.x / LPR;
   const int i = waves > 1 ? threadIdx.x : threadIdx.x % LPR;
   Cols at[P];
-  cols<P>(at, i, waves > 1 ? blockDim.x : LPR, a.n);
+  cols<SPLIT, P>(at, i, waves > 1 ? blockDim.x : LPR, a.n);
   f8 w[P], dw[P];
-  if (P == 1) weights<P>(w, a.w, at);  // twice as many columns leave no registers: read where needed
+  if (P == 1) weights<SPLIT, P>(w, a.w, at);  // twice as many columns leave no registers: read where needed
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
@@ -204,9 +256,9 @@ __global__ void __launch_bounds__(MAXT) add_norm_bwd_kernel(AddNormBwdArgs a) {
       const int64_t r = r1 + b * per, rr = r < a.rows ? r : a.rows - 1;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        to.h[b][p] = ask8<R, NT>((const R*)a.h + rr * a.ldh + at[p].c);
-        to.dy[b][p] = ask8<T, NT>((const T*)a.dy + rr * a.lddy + at[p].c);
-        if (a.dh) to.up[b][p] = ask8<R, NT>((const R*)a.dh + rr * a.lddh + at[p].c);
+        to.h[b][p] = ask8<R, SPLIT, NT>((const R*)a.h + rr * a.ldh, at[p]);
+        to.dy[b][p] = ask8<T, SPLIT, NT>((const T*)a.dy + rr * a.lddy, at[p]);
+        if (a.dh) to.up[b][p] = ask8<R, SPLIT, NT>((const R*)a.dh + rr * a.lddh, at[p]);
       }
     }
   };
@@ -224,25 +276,27 @@ __global__ void __launch_bounds__(MAXT) add_norm_bwd_kernel(AddNormBwdArgs a) {
     const auto& dy = now.dy;
     const auto& up = now.up;
     float sums[2 * RB];                // h^2 and dn h
-    if (P > 1) weights<P>(w, a.w, at);
+    if (P > 1) weights<SPLIT, P>(w, a.w, at);
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
       sums[2 * b] = sums[2 * b + 1] = 0.f;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const f8 hv = raw_f8(h[b][p]), dv = raw_f8(dy[b][p]);
-        float q = 0.f, g = 0.f;
+        float qa = 0.f, qb = 0.f, ga = 0.f, gb = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          q += hv.v[j] * hv.v[j];
-          g += dv.v[j] * w[p].v[j] * hv.v[j];
+        for (int j = 0; j < 4; ++j) {
+          qa += hv.v[j] * hv.v[j];
+          ga += dv.v[j] * w[p].v[j] * hv.v[j];
+          qb += hv.v[j + 4] * hv.v[j + 4];
+          gb += dv.v[j + 4] * w[p].v[j + 4] * hv.v[j + 4];
         }
-        sums[2 * b] += at[p].in ? q : 0.f;
-        sums[2 * b + 1] += at[p].in ? g : 0.f;
+        sums[2 * b] += in_row(at[p], qa, qb);
+        sums[2 * b + 1] += in_row(at[p], ga, gb);
       }
     }
     row_sums<LPR, 2 * RB>(sums, red[turn], waves);
-    if (P > 1) weights<P>(w, a.w, at);
+    if (P > 1) weights<SPLIT, P>(w, a.w, at);
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
       const int64_t r = r1 + b * per;
@@ -259,14 +313,13 @@ __global__ void __launch_bounds__(MAXT) add_norm_bwd_kernel(AddNormBwdArgs a) {
             d.v[j] = rho * (dv.v[j] * w[p].v[j] - n * m);
             dw[p].v[j] += dv.v[j] * n;
           }
-          if (!at[p].in) continue;
           if (a.dh) {
             const f8 u = raw_f8(up[b][p]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) d.v[j] += u.v[j];
           }
-          if (a.dx) put8<T, NT>((T*)a.dx + r * a.lddx + at[p].c, d);
-          if (a.dres) put8<R, NT>((R*)a.dres + r * a.lddr + at[p].c, d);
+          if (a.dx) put8<T, SPLIT, NT>((T*)a.dx + r * a.lddx, at[p], d);
+          if (a.dres) put8<R, SPLIT, NT>((R*)a.dres + r * a.lddr, at[p], d);
         }
       }
     }
@@ -287,7 +340,7 @@ __global__ void __launch_bounds__(MAXT) add_norm_bwd_kernel(AddNormBwdArgs a) {
   }
 #pragma unroll
   for (int p = 0; p < P; ++p)
-    if (at[p].in) store8(a.partials + (int64_t)blockIdx.x * a.n + at[p].c, dw[p]);
+    put8<float, SPLIT, false>(a.partials + (int64_t)blockIdx.x * a.n, at[p], dw[p]);
 }
 
 static int norm_waves(int n) { return n <= 512 ? 1 : n <= 8192 ? (n + 511) / 512 : 16; }
