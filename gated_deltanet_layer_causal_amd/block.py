@@ -12,22 +12,10 @@ from typing import Optional
 import torch
 
 from . import capi as L
+from .capi import Rows8
 from .layer import GDNCore
 
 __all__ = ["ResidualNorm", "Rows8", "Linear4", "GDNLayer4"]
-
-
-class Rows8:
-    """Rows in 8 bits: q float8_e4m3fn [T, n] under a power of two for each 32
-    columns, scale uint8 [T, n / 32] (2^(byte - 127)).  dtype: the storage
-    type of the rows that they stand for, which a product's outputs take."""
-
-    def __init__(self, q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = torch.bfloat16):
-        self.q, self.scale, self.dtype = q, scale, dtype
-
-    @property
-    def shape(self):
-        return self.q.shape
 
 
 class ResidualNorm:
@@ -66,10 +54,9 @@ class ResidualNorm:
     def forward8(self, x, res, w):
         """-> (Rows8, h): y in 8 bits, for Linear4.  hidden a multiple of 32."""
         h = self._sum(x, res)
-        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-        scale = x.new_empty((x.shape[0], self.hidden // 32), dtype=torch.uint8)
-        L.gdn_add_norm_fwd_mx8(x, res, w, h, q, scale, self.eps)
-        return Rows8(q, scale, self.dtype), x if h is None else h
+        rows = Rows8.empty(x.shape[0], self.hidden, self.dtype, x)
+        L.add_norm_fwd_rows8(x, res, w, h, rows, self.eps)
+        return rows, x if h is None else h
 
     def backward(self, h, w, dy, dh=None):
         """From the forward's h: dy is y's gradient, dh that of h from where the
@@ -90,7 +77,7 @@ class Linear4:
     32 inputs), for few rows: Linear4(weight [N, K])(x [T, K]) -> [T, N]."""
 
     def __init__(self, weight: torch.Tensor):
-        self._make(*weight.shape, weight.device)
+        self._make(weight.shape[0], weight.shape[1], weight)
         L.gdn_w4_pack(weight, self.w4)
 
     @classmethod
@@ -98,33 +85,35 @@ class Linear4:
         """Weights that are in 4 bits already: codes uint8 [N, K / 2] (input 2j
         in the low four bits of byte j), scales uint8 [N, K / 32] (2^(byte - 127))."""
         self = cls.__new__(cls)
-        self._make(codes.shape[0], 2 * codes.shape[1], codes.device)
+        self._make(codes.shape[0], 2 * codes.shape[1], codes)
         L.gdn_w4_arrange(codes, scales, self.w4)
         return self
 
-    def _make(self, n, k, device):
+    def _make(self, n, k, like):
         self.n, self.k = n, k
-        self.w4 = L.W4(torch.empty(L.gdn_w4_bytes(n, k), dtype=torch.uint8, device=device), n, k)
+        self.w4 = L.W4(like, n, k, make=True)
 
     def weight(self, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
         """The values [N, K] that the weights stand for, for a dense product
         of many rows."""
-        w = torch.empty((self.n, self.k), dtype=dtype, device=self.w4.device)
+        w = self.w4.packed.new_empty((self.n, self.k), dtype=dtype)
         L.gdn_w4_unpack(self.w4, w)
         return w
 
     def __call__(self, x) -> torch.Tensor:
         """x: a tensor [T, K] of a storage type (rows may be strided) or Rows8."""
         n = self.n
-        T, k = x.shape
-        t = x.q if isinstance(x, Rows8) else x
-        y = t.new_empty((T, n if n % 8 == 0 else n // 8 * 8 + 8), dtype=x.dtype)
-        if n % 8:
-            y = y[:, :n]
-        if t is x:
-            L.gdn_w4_fwd(x, self.w4, y)
+        wide = n if n % 8 == 0 else n // 8 * 8 + 8     # the row stride is a multiple of 8
+        if isinstance(x, Rows8):
+            y = self.w4.packed.new_empty((x.shape[0], wide), dtype=x.dtype)
+            if wide != n:
+                y = y[:, :n]
+            L.w4_fwd_rows8(x, self.w4, y)
         else:
-            L.gdn_w4_fwd_mx8(t, x.scale, self.w4, y)
+            y = x.new_empty((x.shape[0], wide))
+            if wide != n:
+                y = y[:, :n]
+            L.gdn_w4_fwd(x, self.w4, y)
         return y
 
 

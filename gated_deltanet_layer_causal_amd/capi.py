@@ -970,35 +970,84 @@ def gdn_add_norm_fwd(x, res, w, h, y, eps=1e-6, stream=None):
         None if h is None else h.data_ptr(), ldh, y.data_ptr(), ldy, _raw_stream(x.device, i, stream)))
 
 
-def gdn_add_norm_fwd_mx8(x, res, w, h, q, scale, eps=1e-6, stream=None):
-    """gdn_add_norm_fwd with y in 8 bits: q float8_e4m3fn [T, n] under a power
-    of two for each 32 columns, scale uint8 [T, n / 32] (2^(byte - 127))."""
-    f8, u8 = torch.float8_e4m3fn, torch.uint8
+class Rows8:
+    """Rows in 8 bits: q float8_e4m3fn [T, n] under a power of two for each 32
+    columns, scale uint8 [T, n / 32] (2^(byte - 127)); rows may be strided.
+    dtype: the storage type of the rows that they stand for, which a product's
+    outputs take.  Checked once and kept."""
+
+    def __init__(self, q, scale, dtype=torch.bfloat16):
+        if q is None or q.dim() != 2 or q.shape[1] % 32 or q.shape[1] < 32:
+            raise ValueError("8-bit rows are [T, n] with n a multiple of 32")
+        if dtype not in _GDN_DT:
+            raise TypeError(f"unsupported dtype {dtype}")
+        (T, n), dev = q.shape, q.device
+        ldq = _wide("q", q, torch.float8_e4m3fn, T, n, dev)
+        lds = _wide("scale", scale, torch.uint8, T, n // 32, dev)
+        self.shape, self.dtype, self.device, self.index = (T, n), dtype, dev, q.get_device()
+        self.ptrs = q.data_ptr(), ldq, scale.data_ptr(), lds
+        self._memory, self._views = None, (q, scale)
+
+    @classmethod
+    def empty(cls, T, n, dtype, like):
+        """New memory for T rows of n columns on the device of `like`."""
+        self = cls.__new__(cls)
+        self._memory = memory = like.new_empty(T * (n + n // 32), dtype=torch.uint8)
+        self._views = None
+        at = memory.data_ptr()
+        self.shape, self.dtype, self.device, self.index = (T, n), dtype, memory.device, memory.get_device()
+        self.ptrs = at, n, at + T * n, n // 32
+        return self
+
+    def _tensors(self):
+        if self._views is None:
+            (T, n), m = self.shape, self._memory
+            self._views = m[:T * n].view(torch.float8_e4m3fn).view(T, n), m[T * n:].view(T, n // 32)
+        return self._views
+
+    @property
+    def q(self) -> torch.Tensor:
+        return self._tensors()[0]
+
+    @property
+    def scale(self) -> torch.Tensor:
+        return self._tensors()[1]
+
+
+def add_norm_fwd_rows8(x, res, w, h, rows, eps=1e-6, stream=None):
+    """gdn_add_norm_fwd_mx8 into a Rows8."""
     try:
         T, n = shape = x.shape
         i, xt = x.get_device(), x.dtype
         rt = res.dtype if res is not None else h.dtype if h is not None else xt
         dt, rdt = _TYPES[xt, rt]
-        xs, qs, ss = x.stride(), q.stride(), scale.stride()
+        xs = x.stride()
         rs = xs if res is None else res.stride()
         hs = xs if h is None else h.stride()
-        good = (xs[1] == rs[1] == hs[1] == qs[1] == 1 and (ss[1] == 1 or n == 32) and i >= 0 and
-                q.dtype is f8 and q.shape == shape and q.get_device() == i and
-                scale.dtype is u8 and scale.shape == (T, n // 32) and scale.get_device() == i and
+        good = (xs[1] == rs[1] == hs[1] == 1 and i >= 0 and rows.shape == shape and rows.index == i and
                 (res is None or res.shape == shape and res.get_device() == i) and
                 (h is None or h.dtype is rt and h.shape == shape and h.get_device() == i) and
                 w.dtype is torch.float32 and w.numel() == n and w.get_device() == i and w.is_contiguous())
-        ldx, ldr, ldh, ldq, lds = xs[0], rs[0], hs[0], qs[0], ss[0]
+        ldx, ldr, ldh = xs[0], rs[0], hs[0]
     except (AttributeError, IndexError, KeyError, TypeError, ValueError):
         good = False
     if not good:
-        T, n, i, dt, rdt, ldx, ldr, ldh, ldq, lds = _norm_rows(x, res, w, h, (("q", q, 1, f8), ("scale", scale, 32, u8)))
+        T, n, i, dt, rdt, ldx, ldr, ldh = _norm_rows(x, res, w, h, ())
+        if tuple(rows.shape) != (T, n):
+            raise ValueError(f"8-bit rows {tuple(rows.shape)} for rows {(T, n)}")
+        _on(x.device, ("rows", rows))
     elif T < 2:
-        ldx = ldr = ldh = ldq = lds = n
+        ldx = ldr = ldh = n
+    q, ldq, scale, lds = rows.ptrs
     _run("gdn_add_norm_fwd_mx8", i, (
         T, n, dt, rdt, x.data_ptr(), ldx, None if res is None else res.data_ptr(), ldr, w.data_ptr(), eps,
-        None if h is None else h.data_ptr(), ldh, q.data_ptr(), ldq, scale.data_ptr(), lds,
-        _raw_stream(x.device, i, stream)))
+        None if h is None else h.data_ptr(), ldh, q, ldq, scale, lds, _raw_stream(x.device, i, stream)))
+
+
+def gdn_add_norm_fwd_mx8(x, res, w, h, q, scale, eps=1e-6, stream=None):
+    """gdn_add_norm_fwd with y in 8 bits: q float8_e4m3fn [T, n] under a power
+    of two for each 32 columns, scale uint8 [T, n / 32] (2^(byte - 127))."""
+    add_norm_fwd_rows8(x, res, w, h, Rows8(q, scale), eps, stream)
 
 
 def gdn_add_norm_bwd_workspace(rows, n):
@@ -1049,25 +1098,40 @@ def gdn_w4_bytes(n, k):
 
 
 class W4:
-    """Packed 4-bit weights of n outputs and k inputs, checked once and kept."""
+    """Packed 4-bit weights of n outputs and k inputs, checked once and kept.
+    packed: a uint8 tensor, or where to make one (a tensor of any type)."""
 
-    def __init__(self, packed, n, k):
+    def __init__(self, packed, n, k, make=False):
         need = gdn_w4_bytes(n, k)
         if need == 0:
             raise ValueError(f"no 4-bit weights of {n} outputs and {k} inputs: inputs come in groups of 32")
-        if packed.dtype != torch.uint8 or not packed.is_contiguous() or packed.numel() < need:
+        if make:
+            packed = packed.new_empty(need, dtype=torch.uint8)
+        elif packed.dtype != torch.uint8 or not packed.is_contiguous() or packed.numel() < need:
             raise ValueError(f"the packed weights must be a contiguous uint8 tensor of {need} bytes")
         self.packed, self.n, self.k = packed, n, k
         self.device, self.index = packed.device, packed.get_device()
         self.args = packed.data_ptr(), packed.numel()
 
 
-def gdn_w4_pack(weight, w4, stream=None):
-    """weight [n, k] in a storage type (rows may be strided) into w4."""
+def _weight(w4, weight):
+    """The checks of dense weights [n, k]: their type and row stride."""
+    n, k, i = w4.n, w4.k, w4.index
+    try:
+        dt, s = _GDN_DT[weight.dtype], weight.stride()
+        if n > 1 and i >= 0 and weight.shape == (n, k) and s[1] == 1 and weight.get_device() == i:
+            return dt, s[0]
+    except (AttributeError, IndexError, KeyError):
+        pass
     if weight.dtype not in _GDN_DT:
         raise TypeError(f"unsupported dtype {weight.dtype}")
-    ld = _wide("weight", weight, weight.dtype, w4.n, w4.k, w4.device)
-    _run("gdn_w4_pack", w4.index, (w4.n, w4.k, _GDN_DT[weight.dtype], weight.data_ptr(), ld, *w4.args,
+    return _GDN_DT[weight.dtype], _wide("weight", weight, weight.dtype, n, k, w4.device)
+
+
+def gdn_w4_pack(weight, w4, stream=None):
+    """weight [n, k] in a storage type (rows may be strided) into w4."""
+    dt, ld = _weight(w4, weight)
+    _run("gdn_w4_pack", w4.index, (w4.n, w4.k, dt, weight.data_ptr(), ld, *w4.args,
                                    _raw_stream(w4.device, w4.index, stream)))
 
 
@@ -1082,10 +1146,8 @@ def gdn_w4_arrange(codes, scales, w4, stream=None):
 
 def gdn_w4_unpack(w4, weight, stream=None):
     """The values of w4 into weight [n, k], in its storage type."""
-    if weight.dtype not in _GDN_DT:
-        raise TypeError(f"unsupported dtype {weight.dtype}")
-    ld = _wide("weight", weight, weight.dtype, w4.n, w4.k, w4.device)
-    _run("gdn_w4_unpack", w4.index, (w4.n, w4.k, *w4.args, _GDN_DT[weight.dtype], weight.data_ptr(), ld,
+    dt, ld = _weight(w4, weight)
+    _run("gdn_w4_unpack", w4.index, (w4.n, w4.k, *w4.args, dt, weight.data_ptr(), ld,
                                      _raw_stream(w4.device, w4.index, stream)))
 
 
@@ -1114,31 +1176,33 @@ def gdn_w4_fwd(x, w4, y, stream=None):
                            _raw_stream(w4.device, i, stream)))
 
 
-def gdn_w4_fwd_mx8(q, scale, w4, y, stream=None):
-    """gdn_w4_fwd for rows in 8 bits as gdn_add_norm_fwd_mx8 writes them; y in
-    any storage type."""
+def w4_fwd_rows8(rows, w4, y, stream=None):
+    """gdn_w4_fwd_mx8 of a Rows8."""
     i, n, k = w4.index, w4.n, w4.k
-    f8, u8 = torch.float8_e4m3fn, torch.uint8
+    T, width = rows.shape
     try:
-        T, yt = q.shape[0], y.dtype
-        dt = _GDN_DT[yt]
-        qs, ss, ys = q.stride(), scale.stride(), y.stride()
-        good = (qs[1] == 1 and (ss[1] == 1 or k == 32) and (ys[1] == 1 or n == 1) and i >= 0 and
-                q.dtype is f8 and q.shape == (T, k) and q.get_device() == i and
-                scale.dtype is u8 and scale.shape == (T, k // 32) and scale.get_device() == i and
-                y.shape == (T, n) and y.get_device() == i)
-        ldq, lds, ldy = qs[0], ss[0], ys[0]
+        yt = y.dtype
+        dt, ys = _GDN_DT[yt], y.stride()
+        good = (width == k and rows.index == i >= 0 and (ys[1] == 1 or n == 1) and y.shape == (T, n) and
+                y.get_device() == i)
+        ldy = ys[0] if T > 1 else (n + 7) // 8 * 8
     except (AttributeError, IndexError, KeyError, TypeError):
         good = False
     if not good:
+        if width != k:
+            raise ValueError(f"rows of {width} columns by weights of {k} inputs")
         if y.dtype not in _GDN_DT:
             raise TypeError(f"unsupported dtype {y.dtype}")
-        T, dt = q.shape[0], _GDN_DT[y.dtype]
-        ldq = _wide("q", q, f8, T, k, w4.device)
-        lds = _wide("scale", scale, u8, T, k // 32, w4.device)
+        _on(w4.device, ("rows", rows))
+        dt = _GDN_DT[y.dtype]
         ldy = _wide("y", y, y.dtype, T, n, w4.device)
-    elif T < 2:
-        ldq, lds, ldy = k, k // 32, (n + 7) // 8 * 8
+    q, ldq, scale, lds = rows.ptrs
     packed, size = w4.args
-    _run("gdn_w4_fwd_mx8", i, (T, n, k, q.data_ptr(), ldq, scale.data_ptr(), lds, packed, size, dt, y.data_ptr(), ldy,
+    _run("gdn_w4_fwd_mx8", i, (T, n, k, q, ldq, scale, lds, packed, size, dt, y.data_ptr(), ldy,
                                _raw_stream(w4.device, i, stream)))
+
+
+def gdn_w4_fwd_mx8(q, scale, w4, y, stream=None):
+    """gdn_w4_fwd for rows in 8 bits as gdn_add_norm_fwd_mx8 writes them; y in
+    any storage type."""
+    w4_fwd_rows8(Rows8(q, scale), w4, y, stream)

@@ -180,10 +180,18 @@ def test_binding_refuses_before_the_call():
     with pytest.raises(TypeError):
         Linear4.from_codes(torch.zeros(8, 32, dtype=torch.int8), torch.zeros(8, 2, dtype=torch.uint8))
     proj = Linear4.__new__(Linear4)
-    proj._make(8, 64, torch.device("cpu"))
-    for bad in (x[:, :32], torch.zeros(3, 64, dtype=torch.float64), Rows8(x, torch.zeros(3, 2, dtype=torch.uint8)),
-                Rows8(x.to(torch.float8_e4m3fn), torch.zeros(3, 1, dtype=torch.uint8))):
+    proj._make(8, 64, torch.zeros(1))
+    q, s = x.to(torch.float8_e4m3fn), torch.zeros(3, 2, dtype=torch.uint8)
+    for bad in (x[:, :32], torch.zeros(3, 64, dtype=torch.float64), Rows8(q[:, :32], s[:, :1])):
         with pytest.raises((ValueError, TypeError)):
             proj(bad)
+    for bad in ((x, s), (q, s[:, :1]), (q, s.to(torch.int8)), (q[:, :40], s), (q.t().contiguous().t(), s), (q[0], s),
+                (q, s, torch.int8)):
+        with pytest.raises((ValueError, TypeError)):
+            Rows8(*bad)
+    with pytest.raises(ValueError, match="host tensor"):
+        norm.forward8(x, x, w)
+    with pytest.raises(ValueError, match="host tensor"):
+        proj(Rows8(q, s))
     with pytest.raises(ValueError, match="host tensor"):
         proj(x)
