@@ -33,29 +33,6 @@ __device__ __forceinline__ bf16x8 codes8(uint32_t w, float s) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Eight row values as TERMS bf16 each, whose sum they are: one for bf16, two
-// for fp16 (11 bits in 8 + 8), three for fp32 (24 bits).
-template <typename T> struct Split;
-template <> struct Split<bf16> { static constexpr int TERMS = 1; };
-template <> struct Split<fp16> { static constexpr int TERMS = 2; };
-template <> struct Split<float> { static constexpr int TERMS = 3; };
-template <typename T> __device__ __forceinline__ void split8(const T* p, bf16x8 (&out)[Split<T>::TERMS]) {
-  if constexpr (__is_same(T, bf16)) {
-    out[0] = *reinterpret_cast<const bf16x8*>(p);
-  } else {
-    f8 v = load8(p);
-#pragma unroll
-    for (int t = 0; t < Split<T>::TERMS; ++t)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bf16 hi = (bf16)v.v[j];
-        out[t][j] = hi;
-        // what is not finite stays in the first term
-        v.v[j] = __builtin_isfinite((float)hi) ? v.v[j] - (float)hi : 0.f;
-      }
-  }
-}
-
 template <typename T>
 __device__ __forceinline__ void put4(T* y, int64_t n, int64_t n_all, floatx4 v) {
   if (n + 4 <= n_all) {
@@ -69,27 +46,75 @@ __device__ __forceinline__ void put4(T* y, int64_t n, int64_t n_all, floatx4 v) 
 
 struct Mx8 {};      // rows in e4m3 with a scale for each 32 columns
 
-// What a lane reads of its row for 128 inputs (t of a tile), and the products
-// with a weights' operand.  `mask`: inputs beyond the matrix, which read others
-// of the row, become zero (their weights are, but rows may hold what is not
-// finite).
-template <typename X> struct RowPart {
-  static constexpr int TERMS = Split<X>::TERMS;
-  uint4 raw[4][sizeof(X) / 2];
-  __device__ __forceinline__ void load(const W4Args& a, int64_t row, int s, int t, int q, int) {
-    const int k = s * 512 + (4 * t + q) * 32;
-    const X* p = (const X*)a.x + row * a.ldx + (k < a.k ? k : 0);
+// Rows lie in LDS in steps of COLS inputs, 512 bytes of a row in memory, as
+// TERMS planes of bf16 whose sum they are: one for bf16, two for fp16 (11 bits
+// in 8 + 8), three for fp32 (24 bits).  A value is taken apart once, where it
+// is put there (taken apart by every lane that multiplies it, 9 rows of fp16 by
+// 2560 x 6144 took 7.9 us for bf16's 4.4).  Planes have no padding; the 16-byte
+// pieces of row i are permuted by i % 16, so that 16 lanes that read one piece
+// of 16 rows touch every bank once.
+template <typename X> struct Step {
+  static constexpr int E = sizeof(X), TERMS = E == 4 ? 3 : __is_same(X, bf16) ? 1 : 2;
+  static constexpr int COLS = 512 / E, TS = COLS / 128;      // inputs and t's of a step
+  static constexpr int PP = COLS / 8;                        // pieces of a plane's row
+  __device__ __forceinline__ static int at(int row, int piece) { return row * PP + (piece ^ (row & 15)); }
+  // piece i of row `row` in memory into planes `stride` pieces apart
+  __device__ __forceinline__ static void put(uint4* planes, int stride, int row, int i, const uint4& raw) {
+    if constexpr (TERMS == 1) {
+      planes[at(row, i)] = raw;
+    } else {
+      // A term is the value's upper 16 bits (8 significant ones), cut, not
+      // rounded, so that what is left is exact and no term overflows.  What is
+      // not finite stays in the first term: an infinity leaves NaN, which
+      // becomes 0 (max() takes the number; what an fp16 value leaves is above -256).
+      constexpr int N = 16 / E;
+      const X* p = reinterpret_cast<const X*>(&raw);
+      float v[N];
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
+      for (int j = 0; j < N; ++j) v[j] = __builtin_canonicalizef(to_f(p[j]));
 #pragma unroll
-      for (int i = 0; i < (int)(sizeof(X) / 2); ++i) raw[d][i] = reinterpret_cast<const uint4*>(p + 8 * d)[i];
+      for (int u = 0; u < TERMS; ++u) {
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+          const uint32_t a = __float_as_uint(v[j]), b = __float_as_uint(v[j + 1]);
+          w[j / 2] = __builtin_amdgcn_perm(b, a, 0x07060302u);     // the upper halves
+          if (u + 1 < TERMS) {
+            const float c = v[j] - __uint_as_float(a & 0xffff0000u), d = v[j + 1] - __uint_as_float(b & 0xffff0000u);
+            if constexpr (E == 2) {
+              v[j] = fmaxf(c, -256.f);
+              v[j + 1] = fmaxf(d, -256.f);
+            } else {
+              v[j] = c == c ? c : 0.f;
+              v[j + 1] = d == d ? d : 0.f;
+            }
+          }
+        }
+        if constexpr (E == 2)
+          planes[u * stride + at(row, i)] = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+          reinterpret_cast<uint2*>(planes + u * stride + at(row, i / 2))[i % 2] = make_uint2(w[0], w[1]);
+      }
+    }
   }
-  __device__ __forceinline__ void mask(const W4Args& a, int s, int t, int q) {
-    if (s * 512 + (4 * t + q) * 32 >= a.k)
+};
+template <> struct Step<Mx8> {
+  static constexpr int E = 1, TERMS = 1, COLS = 512, TS = 4, PP = 32;
+  __device__ __forceinline__ static int at(int row, int piece) { return row * PP + (piece ^ (row & 15)); }
+  __device__ __forceinline__ static void put(uint4* planes, int, int row, int i, const uint4& raw) {
+    planes[at(row, i)] = raw;
+  }
+};
+
+// What a lane reads of its row for 128 inputs, t of a step.
+template <typename X> struct RowPart {
+  bf16x8 b[Step<X>::TERMS][4];
+  __device__ __forceinline__ void read(const uint4* planes, int stride, int row, int t, int q) {
+#pragma unroll
+    for (int u = 0; u < Step<X>::TERMS; ++u)
 #pragma unroll
       for (int d = 0; d < 4; ++d)
-#pragma unroll
-        for (int i = 0; i < (int)(sizeof(X) / 2); ++i) raw[d][i] = make_uint4(0, 0, 0, 0);
+        b[u][d] = __builtin_bit_cast(bf16x8, planes[u * stride + Step<X>::at(row, 4 * (4 * t + q) + d)]);
   }
 };
 
@@ -105,18 +130,9 @@ template <> struct RowPart<Mx8> {
   // 32 q .. 32 q + 31.
   uint4 lo, hi;
   int scale;
-  __device__ __forceinline__ void load(const W4Args& a, int64_t row, int s, int t, int q, int) {
-    const uint8_t* p = (const uint8_t*)a.x + row * a.ldx + 16 * (q & 1);
-    const int k0 = s * 512 + (4 * t + (q >> 1)) * 32, k1 = k0 + 64, b = s * 16 + 4 * t + q;
-    lo = *reinterpret_cast<const uint4*>(p + (k0 < a.k ? k0 : 0));
-    hi = *reinterpret_cast<const uint4*>(p + (k1 < a.k ? k1 : 0));
-    scale = a.xs[row * a.ldxs + (b * 32 < a.k ? b : 0)];
-  }
-  __device__ __forceinline__ void mask(const W4Args& a, int s, int t, int q) {
-    const int k0 = s * 512 + (4 * t + (q >> 1)) * 32, b = s * 16 + 4 * t + q;
-    if (k0 >= a.k) lo = make_uint4(0, 0, 0, 0);
-    if (k0 + 64 >= a.k) hi = make_uint4(0, 0, 0, 0);
-    if (b * 32 >= a.k) scale = 127;
+  __device__ __forceinline__ void read(const uint4* planes, int, int row, int t, int q) {
+    lo = planes[Step<Mx8>::at(row, 8 * t + q)];
+    hi = planes[Step<Mx8>::at(row, 8 * t + 4 + q)];
   }
 };
 
@@ -139,11 +155,7 @@ __device__ __forceinline__ void products(const uint4 (&w)[NT], const uint32_t (&
       for (int m = 0; m < MT; ++m) acc[n][m] = mx_mma<T>(w[n], (int)sc[n], x[m], acc[n][m]);
   } else {
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      constexpr int TERMS = Split<X>::TERMS;
-      bf16x8 b[MT][TERMS];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) split8(reinterpret_cast<const X*>(&x[m].raw[d][0]), b[m]);
+    for (int d = 0; d < 4; ++d)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint32_t ws[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
@@ -151,81 +163,91 @@ __device__ __forceinline__ void products(const uint4 (&w)[NT], const uint32_t (&
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int u = 0; u < TERMS; ++u)
-            acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, b[m][u], acc[n][m], 0, 0, 0);
+          for (int u = 0; u < Step<X>::TERMS; ++u)
+            acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, x[m].b[u][d], acc[n][m], 0, 0, 0);
       }
-    }
   }
 }
 
-// NT tiles of 16 outputs by MT tiles of 16 rows a workgroup.  Its waves share
-// the inputs out, tile s of 512 to wave s % waves, and join their sums through
-// LDS in wave order.  The weights are the A operand, so that a lane ends with
-// four adjacent outputs of a row.
-template <typename X, typename Y, int NT, int MT, int WMAX>
-__global__ void __launch_bounds__(64 * WMAX) w4_kernel(W4Args a) {
-  extern __shared__ floatx4 part[];     // [wave][NT * MT][lane]
+// ---------------------------------------------------------------- few rows
+// A tile of 16 outputs a workgroup, up to 2 RP rows.  Its waves share the
+// inputs out, tile s of 512 to wave s % waves, and join their sums through LDS
+// in wave order.  Every wave turns its inputs of the rows through LDS of its
+// own: lanes read whole lines of a row, where an operand's own addresses are 64
+// different ones (9 rows of fp16 by 2560 x 6144: MEASURED).  The weights are
+// the A operand, so that a lane ends with four adjacent outputs of a row.
+template <typename X, typename Y, int RP>
+__global__ void __launch_bounds__(1024) w4_kernel(W4Args a) {
+  constexpr bool MX = __is_same(X, Mx8);
+  constexpr int E = Step<X>::E, TS = Step<X>::TS, PLANE = 2 * RP * Step<X>::PP, AHEAD = E == 2 ? 2 : 1;      // steps asked for together (registers)
+  extern __shared__ uint4 stage[];      // [wave][plane][2 RP rows], then the waves' sums
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-  const int kt = w4_ktiles(a.k), tiles = (a.n + 15) / 16;
-  const int n0 = blockIdx.x * NT;
-  const uint4* codes = (const uint4*)a.packed + lane;
-  const uint32_t* scales = (const uint32_t*)((const uint8_t*)a.packed + a.scales_at) + lane;
-  for (int64_t m0 = (int64_t)blockIdx.y * 16 * MT; m0 < a.rows; m0 += (int64_t)gridDim.y * 16 * MT) {
-    floatx4 acc[NT][MT];
+  const int kt = w4_ktiles(a.k), rows = (int)a.rows;
+  const int64_t tile0 = (int64_t)blockIdx.x * kt;
+  const uint4* codes = (const uint4*)a.packed;
+  const uint32_t* scales = (const uint32_t*)((const uint8_t*)a.packed + a.scales_at);
+  uint4* mine = stage + wave * (Step<X>::TERMS * PLANE);
+  const int piece = lane & 31, rr = r < 2 * RP ? r : 2 * RP - 1;
+  const uint8_t* x[RP];                 // rows beyond the last read it; their sums are not stored
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+  for (int i = 0; i < RP; ++i) {
+    const int row = 2 * i + (lane >> 5);
+    x[i] = (const uint8_t*)a.x + (row < rows ? row : rows - 1) * a.ldx * E;
+  }
+  const uint8_t* xs = MX ? a.xs + (r < rows ? r : rows - 1) * a.ldxs : nullptr;
+  floatx4 acc[1][1] = {{zero4()}};
+  for (int s = wave; s < kt; s += waves) {
+    uint4 w[4], raw[AHEAD][RP];
+    const uint32_t sc = (scales + (tile0 + s) * 64)[lane];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) acc[n][m] = zero4();
-    int64_t row[MT];                    // rows beyond the last read it; their columns are not stored
+    for (int t = 0; t < 4; ++t) w[t] = (codes + ((tile0 + s) * 4 + t) * 64)[lane];
+    int sx[4];
+    if constexpr (MX)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      row[m] = m0 + 16 * m + r;
-      row[m] = row[m] < a.rows ? row[m] : a.rows - 1;
-    }
-    for (int s = wave; s < kt; s += waves) {
-      uint4 w[4][NT];
-      uint32_t sc[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int64_t tile = (int64_t)(n0 + n < tiles ? n0 + n : tiles - 1) * kt + s;
-        sc[n] = scales[tile * 64];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) w[t][n] = codes[(tile * 4 + t) * 64];
+      for (int t = 0; t < 4; ++t) {
+        const int b = s * 16 + 4 * t + q;
+        sx[t] = xs[b * 32 < a.k ? b : 0];
       }
-      const bool tail = (s + 1) * 512 > a.k;
-#define GDN_W4_PART(T)                                                         \
-  {                                                                            \
-    RowPart<X> x[MT];                                                          \
-    _Pragma("unroll") for (int m = 0; m < MT; ++m) {                           \
-      x[m].load(a, row[m], s, T, q, r);                                        \
-      if (tail) x[m].mask(a, s, T, q);                                         \
-    }                                                                          \
-    products<T, X, NT, MT>(w[T], sc, x, acc);                                  \
+#pragma unroll
+    for (int h = 0; h < E; ++h) {
+      if (h % AHEAD == 0)
+#pragma unroll
+        for (int g = 0; g < AHEAD; ++g) {
+          const int at = (s * E + h + g) * 512 + piece * 16;
+#pragma unroll
+          for (int i = 0; i < RP; ++i) raw[g][i] = *(const uint4*)(x[i] + (at < a.k * E ? at : 0));
+        }
+      // inputs beyond the matrix become zero: their weights are, but what was read may not be finite
+      const bool in = (s * E + h) * 512 + piece * 16 < a.k * E;
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < RP; ++i)
+        Step<X>::put(mine, PLANE, 2 * i + (lane >> 5), piece, in ? raw[h % AHEAD][i] : make_uint4(0, 0, 0, 0));
+      __builtin_amdgcn_wave_barrier();
+#define GDN_W4_PART(T)                                                                              \
+  if constexpr (T < TS) {                                                                           \
+    RowPart<X> part[1];                                                                             \
+    part[0].read(mine, PLANE, rr, T, q);                                                                   \
+    if constexpr (MX) part[0].scale = (s * 16 + 4 * T + q) * 32 < a.k ? sx[T] : 127;                \
+    const uint4 wt[1] = {w[MX ? T : h * TS + T]};                                                   \
+    const uint32_t st[1] = {MX ? sc : sc >> (8 * (h * TS))};                                        \
+    products<T, X, 1, 1>(wt, st, part, acc);                                                        \
   }
       GDN_W4_PART(0) GDN_W4_PART(1) GDN_W4_PART(2) GDN_W4_PART(3)
 #undef GDN_W4_PART
     }
-    if (waves > 1) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) part[(wave * (NT * MT) + n * MT + m) * 64 + lane] = acc[n][m];
-      __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < NT * MT; ++i) {
-      if (i % waves != wave) continue;
-      floatx4 v = acc[i / MT][i % MT];
-      if (waves > 1) {
-        v = part[i * 64 + lane];
-        for (int u = 1; u < waves; ++u) v += part[(u * (NT * MT) + i) * 64 + lane];
-      }
-      const int64_t m = m0 + 16 * (i % MT) + r;
-      if (m < a.rows) put4((Y*)a.y + m * a.ldy, (int64_t)(n0 + i / MT) * 16 + 4 * q, a.n, v);
-    }
-    if (waves > 1) __syncthreads();
   }
+  floatx4 v = acc[0][0];
+  if (waves > 1) {
+    __syncthreads();
+    floatx4* sums = (floatx4*)stage;
+    sums[wave * 64 + lane] = v;
+    __syncthreads();
+    if (wave > 0) return;
+    for (int u = 1; u < waves; ++u) v += sums[u * 64 + lane];
+  }
+  if (r < rows) put4((Y*)a.y + r * a.ldy, (int64_t)blockIdx.x * 16 + 4 * q, a.n, v);
 }
 
 // ---------------------------------------------------------------- more rows
@@ -233,17 +255,8 @@ __global__ void __launch_bounds__(64 * WMAX) w4_kernel(W4Args a) {
 // by side take NT tiles of 16 outputs each, WK such groups share the inputs
 // out.  A step is 512 bytes of each of 16 MT rows; while it is multiplied the
 // next one's rows and weights are on their way.
-//
-// LDS rows are 512 bytes without padding; the 16-byte pieces of row i are
-// permuted by i % 16, so that 16 lanes that read one piece of 16 rows touch
-// every bank once.
-template <typename X> struct Step {                    // bytes of a value, t's of a step
-  static constexpr int E = __is_same(X, Mx8) ? 1 : sizeof(X);
-  static constexpr int TS = 4 / E;
-};
-
-template <typename X, int WN, int MT> struct StageLds {
-  uint4 x[2][16 * MT * 32];
+template <typename X, int MT> struct StageLds {
+  uint4 x[2][Step<X>::TERMS * 16 * MT * Step<X>::PP];
   uint32_t xs[__is_same(X, Mx8) ? 2 : 1][__is_same(X, Mx8) ? 16 * MT * 4 : 1];
 };
 
@@ -253,13 +266,13 @@ __global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
   constexpr bool MX = __is_same(X, Mx8);
   constexpr int GT = 64 * WN, NL = 16 * MT * 32 / GT, NS = (16 * MT * 4 + GT - 1) / GT;
   __shared__ union {
-    StageLds<X, WN, MT> st[WK];
+    StageLds<X, MT> st[WK];
     floatx4 part[WK > 1 ? (WK - 1) * WN * NT * MT * 64 : 1];
   } lds;
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave % WN, g = wave / WN;
   const int gt = threadIdx.x % GT;
-  StageLds<X, WN, MT>& st = lds.st[g];
+  StageLds<X, MT>& st = lds.st[g];
   const int kt = w4_ktiles(a.k), tiles = (a.n + 15) / 16;
   const int steps_all = (a.k * S::E + 511) / 512;      // of 512 bytes of a row
   const int steps = (steps_all + WK - 1) / WK;         // a group's, the last one's perhaps empty
@@ -318,7 +331,7 @@ __global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
         const int id = gt + GT * i, row = id / 32;
-        st.x[buf][row * 32 + (id % 32 ^ (row & 15))] = xn[i];
+        S::put(st.x[buf], 16 * MT * S::PP, row, id % 32, xn[i]);
       }
       if constexpr (MX) {
 #pragma unroll
@@ -351,16 +364,8 @@ __global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
   if constexpr (T < S::TS) {                                                                                 \
     RowPart<X> x[MT];                                                                                        \
     _Pragma("unroll") for (int m = 0; m < MT; ++m) {                                                         \
-      const uint4* row = xb + (16 * m + r) * 32;                                                             \
-      if constexpr (MX) {                                                                                    \
-        x[m].lo = row[(8 * T + q) ^ r];                                                                      \
-        x[m].hi = row[(8 * T + 4 + q) ^ r];                                                                  \
-        x[m].scale = (int)(st.xs[j & 1][(16 * m + r) * 4 + T] >> (8 * q));                                   \
-      } else {                                                                                               \
-        _Pragma("unroll") for (int d = 0; d < 4; ++d)                                                        \
-            _Pragma("unroll") for (int i = 0; i < S::E / 2; ++i)                                             \
-                x[m].raw[d][i] = row[((4 * T + q) * 2 * S::E + d * (S::E / 2) + i) ^ r];                     \
-      }                                                                                                      \
+      x[m].read(xb, 16 * MT * S::PP, 16 * m + r, T, q);                                                      \
+      if constexpr (MX) x[m].scale = (int)(st.xs[j & 1][(16 * m + r) * 4 + T] >> (8 * q));                   \
     }                                                                                                        \
     products<T, X, NT, MT>(w[T < S::TS ? T : 0], sc, x, acc);                                                \
   }
@@ -546,14 +551,10 @@ static int64_t w4_tiles(int n, int k) { return (int64_t)((n + 15) / 16) * w4_kti
 size_t w4_bytes(int n, int k) { return (size_t)w4_tiles(n, k) * (W4_TILE + 256); }
 int64_t w4_scales_at(int n, int k) { return w4_tiles(n, k) * W4_TILE; }
 
-template <typename X, typename Y, int NT, int MT, int WMAX>
-static hipError_t w4_go(const W4Args& a, hipStream_t st) {
-  const int kt = w4_ktiles(a.k), waves = kt < WMAX ? kt : WMAX;
-  const int64_t mb = (a.rows + 16 * MT - 1) / (16 * MT), nb = ((a.n + 15) / 16 + NT - 1) / NT;
-  int64_t most = ((int64_t)1 << 31) / (nb * 64 * waves);   // a launch holds fewer than 2^32 threads
-  most = most < 1 ? 1 : most < 65535 ? most : 65535;
-  hipLaunchKernelGGL((w4_kernel<X, Y, NT, MT, WMAX>), dim3((unsigned)nb, (unsigned)(mb < most ? mb : most)),
-                     dim3(64 * waves), waves > 1 ? 1024 * NT * MT * waves : 0, st, a);
+template <typename X, typename Y, int RP> static hipError_t w4_go(const W4Args& a, hipStream_t st) {
+  constexpr int LDS = 16 * 2 * RP * Step<X>::PP * Step<X>::TERMS, MOST = 160 * 1024 / LDS < 16 ? 160 * 1024 / LDS : 16;
+  const int kt = w4_ktiles(a.k), turns = (kt + MOST - 1) / MOST, waves = (kt + turns - 1) / turns;
+  hipLaunchKernelGGL((w4_kernel<X, Y, RP>), dim3((unsigned)((a.n + 15) / 16)), dim3(64 * waves), LDS * waves, st, a);
   return hipGetLastError();
 }
 
@@ -591,7 +592,9 @@ template <typename X, typename Y> static hipError_t w4_m(const W4Args& a, hipStr
   constexpr bool MX = __is_same(X, Mx8);
   const int64_t tiles = (a.n + 15) / 16, units = tiles * ((a.rows + 15) / 16);
   const bool deep = a.k >= 4096;
-  if (tiles <= 512 && a.rows <= 12) return w4_go<X, Y, 1, 1, 16>(a, st);
+  if (tiles <= 512 && a.rows <= 12)
+    return a.rows <= 2 ? w4_go<X, Y, 1>(a, st) : a.rows <= 4 ? w4_go<X, Y, 2>(a, st)
+         : a.rows <= 8 ? w4_go<X, Y, 4>(a, st) : w4_go<X, Y, 6>(a, st);
   if (units <= 512 || (!MX && units <= 1024 && deep)) return w4_rows_go<X, Y, 2, 4, 1, 1>(a, st);
   if (units <= 1024 || (units <= 2048 && (!MX || deep))) return w4_rows_go<X, Y, 4, 2, 1, 1>(a, st);
   if (units <= 4096) return w4_rows_go<X, Y, 4, 1, 1, 1>(a, st);
