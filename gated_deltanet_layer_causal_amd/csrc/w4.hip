@@ -44,17 +44,45 @@ __device__ __forceinline__ void put4(T* y, int64_t n, int64_t n_all, floatx4 v) 
   }
 }
 
+// The same as fp16, exact for scales of 2^-13 to 2^13 (0.5 * 2^-13 is the
+// smallest normal number); whether all four scales of a tile's lane are.
+__device__ __forceinline__ fp16x8 codes8_f16(uint32_t w, float s) {
+  typedef _Float16 fp16x2 __attribute__((ext_vector_type(2)));
+  const auto a = __builtin_bit_cast(fp16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0));
+  const auto b = __builtin_bit_cast(fp16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1));
+  const auto c = __builtin_bit_cast(fp16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2));
+  const auto d = __builtin_bit_cast(fp16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3));
+  return fp16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ bool scales_f16(uint32_t sc) {
+  bool in = true;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) in &= (sc >> (8 * t) & 255) - 114u <= 26u;
+  return in;
+}
+
+// Eight fp16 values as two terms of bf16 whose sum they are (11 bits in 8 + 8).
+// What is not finite stays in the first.
+__device__ __forceinline__ void split8(const bf16x8& bits, bf16x8 (&out)[2]) {
+  const fp16x8 v = __builtin_bit_cast(fp16x8, bits);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    out[0][j] = (bf16)(float)v[j];
+    const float hi = (float)out[0][j];
+    out[1][j] = (bf16)(__builtin_isfinite(hi) ? (float)v[j] - hi : 0.f);
+  }
+}
+
 struct Mx8 {};      // rows in e4m3 with a scale for each 32 columns
 
-// Rows lie in LDS in steps of COLS inputs, 512 bytes of a row in memory, as
-// TERMS planes of bf16 whose sum they are: one for bf16, two for fp16 (11 bits
-// in 8 + 8), three for fp32 (24 bits).  A value is taken apart once, where it
-// is put there (taken apart by every lane that multiplies it, 9 rows of fp16 by
-// 2560 x 6144 took 7.9 us for bf16's 4.4).  Planes have no padding; the 16-byte
-// pieces of row i are permuted by i % 16, so that 16 lanes that read one piece
-// of 16 rows touch every bank once.
+// Rows lie in LDS in steps of COLS inputs, 512 bytes of a row in memory: 8- and
+// 16-bit ones as they are, fp32 as three planes of bf16 whose sum they are (24
+// bits in 8 + 8 + 8), taken apart once, where they are put there (taken apart
+// by every lane that multiplies them one row by 2560 x 6144 took 11.2 us, so
+// 5.5).  Planes have no padding; the 16-byte pieces of row i are permuted by
+// i % 16, so that 16 lanes that read one piece of 16 rows touch every bank once.
 template <typename X> struct Step {
-  static constexpr int E = sizeof(X), TERMS = E == 4 ? 3 : __is_same(X, bf16) ? 1 : 2;
+  static constexpr int E = sizeof(X), TERMS = E == 4 ? 3 : 1;
   static constexpr int COLS = 512 / E, TS = COLS / 128;      // inputs and t's of a step
   static constexpr int PP = COLS / 8;                        // pieces of a plane's row
   __device__ __forceinline__ static int at(int row, int piece) { return row * PP + (piece ^ (row & 15)); }
@@ -65,35 +93,23 @@ template <typename X> struct Step {
     } else {
       // A term is the value's upper 16 bits (8 significant ones), cut, not
       // rounded, so that what is left is exact and no term overflows.  What is
-      // not finite stays in the first term: an infinity leaves NaN, which
-      // becomes 0 (max() takes the number; what an fp16 value leaves is above -256).
-      constexpr int N = 16 / E;
-      const X* p = reinterpret_cast<const X*>(&raw);
-      float v[N];
+      // not finite stays in the first term.
+      const float* p = reinterpret_cast<const float*>(&raw);
+      float v[4];
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = __builtin_canonicalizef(to_f(p[j]));
+      for (int j = 0; j < 4; ++j) v[j] = __builtin_canonicalizef(p[j]);
 #pragma unroll
       for (int u = 0; u < TERMS; ++u) {
-        uint32_t w[N / 2];
+        uint32_t w[2];
 #pragma unroll
-        for (int j = 0; j < N; j += 2) {
+        for (int j = 0; j < 4; j += 2) {
           const uint32_t a = __float_as_uint(v[j]), b = __float_as_uint(v[j + 1]);
           w[j / 2] = __builtin_amdgcn_perm(b, a, 0x07060302u);     // the upper halves
-          if (u + 1 < TERMS) {
-            const float c = v[j] - __uint_as_float(a & 0xffff0000u), d = v[j + 1] - __uint_as_float(b & 0xffff0000u);
-            if constexpr (E == 2) {
-              v[j] = fmaxf(c, -256.f);
-              v[j + 1] = fmaxf(d, -256.f);
-            } else {
-              v[j] = c == c ? c : 0.f;
-              v[j + 1] = d == d ? d : 0.f;
-            }
-          }
+          const float c = v[j] - __uint_as_float(a & 0xffff0000u), d = v[j + 1] - __uint_as_float(b & 0xffff0000u);
+          v[j] = c == c ? c : 0.f;               // an infinity leaves NaN
+          v[j + 1] = d == d ? d : 0.f;
         }
-        if constexpr (E == 2)
-          planes[u * stride + at(row, i)] = make_uint4(w[0], w[1], w[2], w[3]);
-        else
-          reinterpret_cast<uint2*>(planes + u * stride + at(row, i / 2))[i % 2] = make_uint2(w[0], w[1]);
+        reinterpret_cast<uint2*>(planes + u * stride + at(row, i / 2))[i % 2] = make_uint2(w[0], w[1]);
       }
     }
   }
@@ -144,18 +160,43 @@ __device__ __forceinline__ floatx4 mx_mma(const uint4& w, int sc, const RowPart<
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 0, T, sc, 0, x.scale);
 }
 
-// acc[n][m] += the weights' tiles n by the rows' tiles m over 128 inputs
+// acc[n][m] += the weights' tiles n by the rows' tiles m over 128 inputs.
+// fp16 rows meet weights in fp16 (near: all scales are such that they are exact
+// there) or else are taken apart into bf16: the first cost 9 rows by
+// 2560 x 6144 MEASURED us, the second 7.9.
 template <int T, typename X, int NT, int MT>
-__device__ __forceinline__ void products(const uint4 (&w)[NT], const uint32_t (&sc)[NT], const RowPart<X> (&x)[MT],
-                                         floatx4 (&acc)[NT][MT]) {
+__device__ __forceinline__ void products(const uint4 (&w)[NT], const uint32_t (&sc)[NT], bool near,
+                                         const RowPart<X> (&x)[MT], floatx4 (&acc)[NT][MT]) {
   if constexpr (__is_same(X, Mx8)) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[n][m] = mx_mma<T>(w[n], (int)sc[n], x[m], acc[n][m]);
-  } else {
+    return;
+  } else if (__is_same(X, fp16) && near) {
 #pragma unroll
     for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t ws[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+        const fp16x8 av = codes8_f16(ws[d], scale_f(sc[n] >> (8 * T) & 255));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, __builtin_bit_cast(fp16x8, x[m].b[0][d]), acc[n][m],
+                                                             0, 0, 0);
+      }
+  } else {
+    constexpr int TERMS = __is_same(X, fp16) ? 2 : Step<X>::TERMS;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      bf16x8 b[MT][TERMS];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if constexpr (__is_same(X, fp16)) split8(x[m].b[0][d], b[m]);
+        else
+#pragma unroll
+          for (int u = 0; u < TERMS; ++u) b[m][u] = x[m].b[u][d];
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint32_t ws[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
@@ -163,9 +204,10 @@ __device__ __forceinline__ void products(const uint4 (&w)[NT], const uint32_t (&
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int u = 0; u < Step<X>::TERMS; ++u)
-            acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, x[m].b[u][d], acc[n][m], 0, 0, 0);
+          for (int u = 0; u < TERMS; ++u)
+            acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, b[m][u], acc[n][m], 0, 0, 0);
       }
+    }
   }
 }
 
@@ -202,6 +244,7 @@ __global__ void __launch_bounds__(1024) w4_kernel(W4Args a) {
     const uint32_t sc = (scales + (tile0 + s) * 64)[lane];
 #pragma unroll
     for (int t = 0; t < 4; ++t) w[t] = (codes + ((tile0 + s) * 4 + t) * 64)[lane];
+    const bool near = __is_same(X, fp16) && __all(scales_f16(sc));
     int sx[4];
     if constexpr (MX)
 #pragma unroll
@@ -232,7 +275,7 @@ __global__ void __launch_bounds__(1024) w4_kernel(W4Args a) {
     if constexpr (MX) part[0].scale = (s * 16 + 4 * T + q) * 32 < a.k ? sx[T] : 127;                \
     const uint4 wt[1] = {w[MX ? T : h * TS + T]};                                                   \
     const uint32_t st[1] = {MX ? sc : sc >> (8 * (h * TS))};                                        \
-    products<T, X, 1, 1>(wt, st, part, acc);                                                        \
+    products<T, X, 1, 1>(wt, st, near, part, acc);                                                  \
   }
       GDN_W4_PART(0) GDN_W4_PART(1) GDN_W4_PART(2) GDN_W4_PART(3)
 #undef GDN_W4_PART
@@ -350,6 +393,9 @@ __global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
     for (int j = 0; j < steps; ++j) {
       uint4 w[S::TS][NT];
       uint32_t sc[NT];
+      bool near = __is_same(X, fp16);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) near = near && __all(scales_f16(sn[n]));
       const bool full = j * WK + g < steps_all;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -367,7 +413,7 @@ __global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
       x[m].read(xb, 16 * MT * S::PP, 16 * m + r, T, q);                                                      \
       if constexpr (MX) x[m].scale = (int)(st.xs[j & 1][(16 * m + r) * 4 + T] >> (8 * q));                   \
     }                                                                                                        \
-    products<T, X, NT, MT>(w[T < S::TS ? T : 0], sc, x, acc);                                                \
+    products<T, X, NT, MT>(w[T < S::TS ? T : 0], sc, near, x, acc);                                          \
   }
         GDN_W4_PART(0) GDN_W4_PART(1) GDN_W4_PART(2) GDN_W4_PART(3)
 #undef GDN_W4_PART
@@ -426,7 +472,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const T* w, int64_t ldw, i
   const int64_t row = tile / kt * 16 + r;
   const int k0 = (int)(tile % kt) * 512 + 128 * t + 32 * q;
   uint32_t code[4] = {0, 0, 0, 0};
-  int e = -127;
+  int e = 0;             // of zeros, and beyond the matrix: products in fp16 want scales near 1
   if (row < n && k0 < k) {
     f8 v[4];
     uint32_t top = 0;                  // the largest magnitude's bits; above those of infinity: NaN
@@ -489,13 +535,13 @@ __global__ void __launch_bounds__(256) w4_arrange_kernel(const uint8_t* codes, i
   if (tile >= tiles) return;
   const int64_t row = tile / kt * 16 + r;
   const int k0 = (int)(tile % kt) * 512 + q * 32;
-  uint32_t sc = 0;
+  uint32_t sc = 0x7f7f7f7f;          // 1 beyond the matrix
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     uint4 c = make_uint4(0, 0, 0, 0);
     if (row < n && k0 + 128 * t < k) {
       c = *(const uint4*)(codes + row * ldc + (k0 + 128 * t) / 2);
-      sc |= (uint32_t)scales[row * lds + (k0 + 128 * t) / 32] << (8 * t);
+      sc = (sc & ~(255u << (8 * t))) | (uint32_t)scales[row * lds + (k0 + 128 * t) / 32] << (8 * t);
     }
     ((uint4*)packed)[(tile * 4 + t) * 64 + lane] = c;
   }

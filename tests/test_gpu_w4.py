@@ -215,6 +215,26 @@ def test_scales_at_the_ends(dt):
     assert w[5, 32:].isnan().all() and w[5, :32].isfinite().all()
 
 
+@pytest.mark.parametrize("T", [1, 7, 40])
+def test_fp16_rows_by_weights_that_fp16_does_not_hold(T):
+    """Scales just inside and just outside of what fp16 holds exactly, and far
+    outside, next to each other; rows bring the products back into range."""
+    n, k = 64, 1056
+    codes, _ = make_codes(n, k, 16)
+    g = torch.Generator().manual_seed(17)
+    for lo, hi in ((113, 117), (138, 142), (114, 115), (140, 141), (20, 60), (0, 1)):
+        scales = torch.full((n, k // 32), 127, dtype=torch.uint8)
+        scales[:, 5::7] = torch.randint(lo, hi, scales[:, 5::7].shape, generator=g, dtype=torch.int64).to(torch.uint8)
+        proj = Linear4.from_codes(codes.to(DEV), scales.to(DEV))
+        x = rows_of(T, k, torch.float16, 18) * (2.0 ** -12 if lo > 127 else 1.0)
+        check(proj(x), x.cpu().double(), values(codes, scales), 2 * (k // 32) + 64)
+        only = torch.zeros(n, k // 32, dtype=torch.bool)
+        only[:, 5::7] = True
+        c2 = torch.where(only.repeat_interleave(16, 1), codes, 0)
+        y = Linear4.from_codes(c2.to(DEV), scales.to(DEV))(x)
+        check(y, x.cpu().double(), values(c2, scales), 2 * (k // 32) + 64)
+
+
 def test_values_across_the_types_ranges():
     """fp16 and fp32 rows enter whole: the smallest and largest of their
     values, next to each other."""
