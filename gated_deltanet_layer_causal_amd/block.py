@@ -102,18 +102,16 @@ class Linear4:
 
     def __call__(self, x) -> torch.Tensor:
         """x: a tensor [T, K] of a storage type (rows may be strided) or Rows8."""
-        n = self.n
-        wide = n if n % 8 == 0 else n // 8 * 8 + 8     # the row stride is a multiple of 8
-        if isinstance(x, Rows8):
-            y = self.w4.packed.new_empty((x.shape[0], wide), dtype=x.dtype)
-            if wide != n:
-                y = y[:, :n]
-            L.w4_fwd_rows8(x, self.w4, y)
-        else:
-            y = x.new_empty((x.shape[0], wide))
-            if wide != n:
-                y = y[:, :n]
+        rows, n = x.shape[0], self.n
+        t = self.w4.packed if isinstance(x, Rows8) else x
+        if n % 8 == 0:
+            y = t.new_empty((rows, n), dtype=x.dtype)
+        else:                           # the row stride is a multiple of 8
+            y = t.new_empty_strided((rows, n), (n // 8 * 8 + 8, 1), dtype=x.dtype)
+        if t is x:
             L.gdn_w4_fwd(x, self.w4, y)
+        else:
+            L.w4_fwd_rows8(x, self.w4, y)
         return y
 
 

@@ -7,6 +7,8 @@
 // the operand order of the matrix instructions, and one word a lane for the
 // four scales.  A t is 128 adjacent inputs, so that a load of rows takes 64
 // adjacent bytes of 8-bit rows, and two of 16-bit rows a whole line.  Outputs and inputs beyond the matrix have codes of 0.
+#include <type_traits>
+
 #include "common.h"
 #include "launch.h"
 
@@ -162,8 +164,8 @@ __device__ __forceinline__ floatx4 mx_mma(const uint4& w, int sc, const RowPart<
 
 // acc[n][m] += the weights' tiles n by the rows' tiles m over 128 inputs.
 // fp16 rows meet weights in fp16 (near: all scales are such that they are exact
-// there) or else are taken apart into bf16: the first cost 9 rows by
-// 2560 x 6144 MEASURED us, the second 7.9.
+// there) or else are taken apart into bf16: 9 rows by 2560 x 6144 take 4.6 us with
+// the first and 7.9 with the second.
 template <int T, typename X, int NT, int MT>
 __device__ __forceinline__ void products(const uint4 (&w)[NT], const uint32_t (&sc)[NT], bool near,
                                          const RowPart<X> (&x)[MT], floatx4 (&acc)[NT][MT]) {
@@ -216,12 +218,13 @@ __device__ __forceinline__ void products(const uint4 (&w)[NT], const uint32_t (&
 // inputs out, tile s of 512 to wave s % waves, and join their sums through LDS
 // in wave order.  Every wave turns its inputs of the rows through LDS of its
 // own: lanes read whole lines of a row, where an operand's own addresses are 64
-// different ones (9 rows of fp16 by 2560 x 6144: MEASURED).  The weights are
+// different ones (9 rows of bf16 by 2560 x 6144: 6.1 -> 4.4 us).  The weights are
 // the A operand, so that a lane ends with four adjacent outputs of a row.
 template <typename X, typename Y, int RP>
 __global__ void __launch_bounds__(1024) w4_kernel(W4Args a) {
   constexpr bool MX = __is_same(X, Mx8);
-  constexpr int E = Step<X>::E, TS = Step<X>::TS, PLANE = 2 * RP * Step<X>::PP, AHEAD = E == 2 ? 2 : 1;      // steps asked for together (registers)
+  constexpr int E = Step<X>::E, TS = Step<X>::TS, PLANE = 2 * RP * Step<X>::PP, 
+                AHEAD = E == 2 && RP * __is_same(X, fp16) < 8 ? 2 : 1;     // steps asked for together (registers)
   extern __shared__ uint4 stage[];      // [wave][plane][2 RP rows], then the waves' sums
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
@@ -457,9 +460,10 @@ __global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
 // y = w / (u / 2), A and B the nearest values of w under u and u / 2 in units
 // of u / 2, the errors' difference is
 //   sum (y - B)^2 - (y - A)^2 = sum (A - B) (2 y - (A + B)),
-// one sum, most of whose terms are zero.  A term is exact in fp32 for 16-bit
-// weights (a few bits of A - B by at most 11 of the rest) and the sum is 64
-// bits, so that near ties do not hang on its order.
+// one sum, most of whose terms are zero.  Near ties must not hang on the sum's
+// order: of 16-bit weights it is exact in fp32 (where A and B differ, y is above
+// 1/4, so that a term is a multiple of 2^-12; |A - B| and |2 y - (A + B)| are at
+// most 8 each, 32 terms at most 2^11: 23 bits), of fp32 ones it is 64 bits.
 typedef float floatx2 __attribute__((ext_vector_type(2)));
 template <typename T>
 __global__ void __launch_bounds__(256) w4_pack_kernel(const T* w, int64_t ldw, int n, int k, int64_t parts,
@@ -474,17 +478,34 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const T* w, int64_t ldw, i
   uint32_t code[4] = {0, 0, 0, 0};
   int e = 0;             // of zeros, and beyond the matrix: products in fp16 want scales near 1
   if (row < n && k0 < k) {
+    Raw8<T> raw[4];
     f8 v[4];
-    uint32_t top = 0;                  // the largest magnitude's bits; above those of infinity: NaN
+    uint32_t top = 0;                  // the largest magnitude's bits as a float; above those of infinity: NaN
 #pragma unroll
-    for (int d = 0; d < 4; ++d) v[d] = load8(w + row * ldw + k0 + 8 * d);
+    for (int d = 0; d < 4; ++d) raw[d] = ld_raw8(w + row * ldw + k0 + 8 * d);
+    if constexpr (sizeof(T) == 2) {
+      typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+      u16x2 most = {0, 0};
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
+      for (int d = 0; d < 4; ++d) {
+        const uint32_t ws[4] = {raw[d].v[0].x, raw[d].v[0].y, raw[d].v[0].z, raw[d].v[0].w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t b = __float_as_uint(v[d].v[j]) & 0x7fffffffu;
-        top = top > b ? top : b;
+        for (int j = 0; j < 4; ++j)
+          most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, ws[j] & 0x7fff7fffu));
       }
+      const uint16_t one = most[0] > most[1] ? most[0] : most[1];
+      top = __float_as_uint(to_f(__builtin_bit_cast(T, one)));
+    }
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      v[d] = raw_f8(raw[d]);
+      if constexpr (sizeof(T) == 4)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t b = __float_as_uint(v[d].v[j]) & 0x7fffffffu;
+          top = top > b ? top : b;
+        }
+    }
     if (top >= 0x7f800000u) {
       e = 128;
     } else if (top != 0) {
@@ -493,7 +514,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const T* w, int64_t ldw, i
       e = e < -127 ? -127 : e > 125 ? 125 : e;       // 6 * 2^125 is finite, 4 * 2^126 is not
       const float u = scale_f(e + 127), half = scale_f(e > -127 ? e + 126 : 0);
       uint32_t fine[4];
-      double sum = 0;
+      typename std::conditional<sizeof(T) == 4, double, float>::type sum = 0;
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
         uint32_t cw = 0, cf = 0;
@@ -507,7 +528,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const T* w, int64_t ldw, i
     const floatx2 A = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw, 2.f, I);                             \
     const floatx2 B = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cf, 1.f, I);                             \
     _Pragma("unroll") for (int j = 0; j < 2; ++j)                                                       \
-        sum += (double)((A[j] - B[j]) * (ldexpf(v[d].v[2 * I + j], 2 - e) - (A[j] + B[j])));            \
+        sum += (A[j] - B[j]) * (ldexpf(v[d].v[2 * I + j], 2 - e) - (A[j] + B[j]));                      \
   }
         GDN_PAIR(0) GDN_PAIR(1) GDN_PAIR(2) GDN_PAIR(3)
 #undef GDN_PAIR
@@ -631,16 +652,25 @@ static hipError_t w4_rows_go(const W4Args& args, hipStream_t st) {
 //         10240 x 8192,  48: 1920  21.9  12.8  13.4  17.2
 //         10240 x 2560,  48: 1920  15.4   6.9   6.0   7.3
 //         16480 x 2560,  64: 4120  31.4  14.4  10.1   9.4
-// Up to 12 rows by few outputs want no staging at all: 1 row of bf16 by
-// 2560 x 6144 takes 4.0 us with a wave for each 512 inputs, 7.3 staged; 12 rows
-// 7.0 and 7.4.
+//
+// Few rows: every wave its own inputs, all of the weights asked for at once;
+// against the above, of which one row takes as long as 16:
+//   bf16   2560 x  6144:  1, 4, 8, 12, 16 rows  3.5  3.7  4.0  4.5  5.0    7.6
+//          8192 x  4096:                        5.3  5.3  5.2  6.1  6.7    6.7
+//         16480 x  2560:                        6.0  6.1  6.8  9.7 10.6    7.3
+//         20480 x  8192:                       15.7 16.1 21.9 26.7 29.9   21.3
+//   8 bit  2560 x  6144:                        2.9  3.3  4.0  4.6  5.1    5.1
+//          8192 x  4096:                        4.8  4.9  5.7  6.2  6.8    5.5
+//         16480 x  2560:                        5.3  5.5  5.8  7.0  9.1    6.5
+//         20480 x  8192:                       14.7 14.5 21.1 26.8 30.1   19.9
 template <typename X, typename Y> static hipError_t w4_m(const W4Args& a, hipStream_t st) {
   constexpr bool MX = __is_same(X, Mx8);
   const int64_t tiles = (a.n + 15) / 16, units = tiles * ((a.rows + 15) / 16);
   const bool deep = a.k >= 4096;
-  if (tiles <= 512 && a.rows <= 12)
-    return a.rows <= 2 ? w4_go<X, Y, 1>(a, st) : a.rows <= 4 ? w4_go<X, Y, 2>(a, st)
-         : a.rows <= 8 ? w4_go<X, Y, 4>(a, st) : w4_go<X, Y, 6>(a, st);
+  if (a.rows <= 2) return w4_go<X, Y, 1>(a, st);
+  if (a.rows <= 4) return w4_go<X, Y, 2>(a, st);
+  if (a.rows <= 8 && (tiles <= 512 || !deep)) return w4_go<X, Y, 4>(a, st);
+  if (a.rows <= 16 && tiles <= (MX ? 256 : 512)) return a.rows <= 12 ? w4_go<X, Y, 6>(a, st) : w4_go<X, Y, 8>(a, st);
   if (units <= 512 || (!MX && units <= 1024 && deep)) return w4_rows_go<X, Y, 2, 4, 1, 1>(a, st);
   if (units <= 1024 || (units <= 2048 && (!MX || deep))) return w4_rows_go<X, Y, 4, 2, 1, 1>(a, st);
   if (units <= 4096) return w4_rows_go<X, Y, 4, 1, 1, 1>(a, st);

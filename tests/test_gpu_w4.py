@@ -34,7 +34,8 @@ MAG = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64)
 SIZES = [(1, 1, 32), (1, 16, 512), (2, 17, 64), (3, 15, 480), (16, 50, 544), (17, 33, 1056), (1, 1544, 2560),
          (5, 1544, 2560), (9, 640, 6144), (33, 48, 1504), (40, 100, 8224), (64, 333, 2560), (130, 40, 96), (1, 8, 16416),
          (1, 8200, 512), (7, 8208, 1056), (30, 8216, 544), (70, 8200, 1568),
-         (20, 8190, 4128), (33, 8100, 608), (100, 10250, 544), (300, 4100, 96)]
+         (20, 8190, 4128), (33, 8100, 608), (100, 10250, 544), (300, 4100, 96),
+         (14, 100, 2080), (4, 16400, 544), (8, 9000, 4128), (2, 100, 16928), (10, 50, 12320)]
 
 
 def half(dt):
