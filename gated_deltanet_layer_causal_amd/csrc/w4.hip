@@ -468,13 +468,26 @@ typedef float floatx2 __attribute__((ext_vector_type(2)));
 template <typename T>
 __global__ void __launch_bounds__(256) w4_pack_kernel(const T* w, int64_t ldw, int n, int k, int64_t parts,
                                                       uint8_t* packed, int64_t scales_at) {
-  const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+  constexpr int V = 16 / sizeof(T), P = 128 / V;       // values of a 16-byte piece, pieces of a row
+  __shared__ uint4 turn[4][16 * (P + 1)];              // rows a piece apart: all banks once
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, r = lane & 15;
   const int kt = w4_ktiles(k);
-  const int64_t part = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), tile = part >> 2;
-  if (part >= parts) return;
+  const int64_t part = (int64_t)blockIdx.x * 4 + wave, tile = part >> 2;
   const int t = (int)(part & 3);
   const int64_t row = tile / kt * 16 + r;
   const int k0 = (int)(tile % kt) * 512 + 128 * t + 32 * q;
+  if (part < parts) {
+#pragma unroll
+    for (int i = 0; i < 16 * P / 64; ++i) {            // 16 lanes read 256 adjacent bytes of an output
+      const int id = i * 64 + lane, piece = id % P;
+      const int64_t at = tile / kt * 16 + id / P;
+      const int c = (int)(tile % kt) * 512 + 128 * t + piece * V;
+      turn[wave][id / P * (P + 1) + piece] = __builtin_bit_cast(
+          uint4, __builtin_nontemporal_load(reinterpret_cast<const nt_u32x4*>(w + (at < n ? at : n - 1) * ldw + (c < k ? c : 0))));
+    }
+  }
+  __syncthreads();
+  if (part >= parts) return;
   uint32_t code[4] = {0, 0, 0, 0};
   int e = 0;             // of zeros, and beyond the matrix: products in fp16 want scales near 1
   if (row < n && k0 < k) {
@@ -482,7 +495,10 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const T* w, int64_t ldw, i
     f8 v[4];
     uint32_t top = 0;                  // the largest magnitude's bits as a float; above those of infinity: NaN
 #pragma unroll
-    for (int d = 0; d < 4; ++d) raw[d] = ld_raw8(w + row * ldw + k0 + 8 * d);
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+        raw[d].v[i] = turn[wave][r * (P + 1) + q * (P / 4) + d * (P / 16) + i];
     if constexpr (sizeof(T) == 2) {
       typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
       u16x2 most = {0, 0};
@@ -610,7 +626,7 @@ __global__ void __launch_bounds__(256) w4_unpack_kernel(const uint8_t* packed, i
   for (int i = 0; i < 16 * P / 64; ++i) {
     const int id = i * 64 + lane, row = id / P, piece = id % P;
     if (row0 + row < n && k0 + piece * V < k)
-      *reinterpret_cast<uint4*>(w + (row0 + row) * ldw + k0 + piece * V) = turn[wave][row * (P + 1) + piece];
+      store16_nt(w + (row0 + row) * ldw + k0 + piece * V, turn[wave][row * (P + 1) + piece]);
   }
 }
 
