@@ -443,7 +443,8 @@ size_t gdn_cache_workspace(int32_t n_slots);
  * Without rows (rows == 0) the tensors of rows may be NULL, in all calls here.
  * h may be the memory of res, or of x where the types are the same, and y
  * that of x (same row strides): other overlaps give undefined values.
- * NaN and infinities stay in their row.  No workspace. */
+ * The squares of a row's h have to be finite in fp32.  NaN and infinities stay
+ * in their row.  No workspace. */
 gdn_status gdn_add_norm_fwd(int64_t rows, int32_t n, gdn_dtype dtype, gdn_dtype res_dtype,
                             const void* x, int64_t ldx, const void* res, int64_t ldr,
                             const float* w, float eps, void* h, int64_t ldh, void* y, int64_t ldy,

@@ -249,6 +249,27 @@ def test_many_rows(T, n, dt, rt):
     check_bwd(norm.backward(h, d["w"], d["dy"], d["dh"]), h, d["w"], d["dy"], d["dh"])
 
 
+def test_more_rows_than_a_launch_and_offsets_beyond_32_bits():
+    """2^22 + 3 rows: more than a launch's workgroups, and elements beyond
+    2^32; rows here and there against the formula."""
+    T, n = (1 << 22) + 3, 1032
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.empty(T, n, dtype=torch.bfloat16, device=DEV)
+    for a in range(0, T, 1 << 20):
+        x[a:a + (1 << 20)].normal_(generator=g)
+    w = torch.randn(n, generator=g, device=DEV) * 0.3
+    norm = ResidualNorm(n, eps=EPS)
+    y, h = norm.forward(x, x, w)
+    at = [0, 1, 2, 77, (1 << 21) - 1, 1 << 21, (1 << 21) + 1, (1 << 22) - 2, (1 << 22) - 1, 1 << 22, T - 2, T - 1]
+    part = {"x": x[at], "res": x[at], "w": w}
+    check_fwd(y[at], h[at], part, torch.bfloat16)
+    del y
+    g2 = norm.backward(h, w, x, x)
+    one = norm.backward(h[at], w, x[at], x[at])
+    assert torch.equal(g2["dx"][at], one["dx"])
+    assert torch.isfinite(g2["dw"]).all()
+
+
 # ------------------------------------------------------------------ 8 bits
 def values8(rows):
     """The values that 8-bit rows stand for, in 64 bits."""

@@ -35,7 +35,7 @@ SIZES = [(1, 1, 32), (1, 16, 512), (2, 17, 64), (3, 15, 480), (16, 50, 544), (17
          (5, 1544, 2560), (9, 640, 6144), (33, 48, 1504), (40, 100, 8224), (64, 333, 2560), (130, 40, 96), (1, 8, 16416),
          (1, 8200, 512), (7, 8208, 1056), (30, 8216, 544), (70, 8200, 1568),
          (20, 8190, 4128), (33, 8100, 608), (100, 10250, 544), (300, 4100, 96),
-         (14, 100, 2080), (4, 16400, 544), (8, 9000, 4128), (2, 100, 16928), (10, 50, 12320)]
+         (14, 100, 2080), (4, 16400, 544), (8, 9000, 4128), (2, 100, 16928), (10, 50, 12320), (16, 40, 8192), (15, 33, 6656)]
 
 
 def half(dt):
@@ -272,6 +272,22 @@ def test_repeats_bit_by_bit(k):
     for x in (rows_of(30, k, torch.bfloat16, 5), rows8_of(30, k, torch.bfloat16, 5)):
         y = proj(x)
         assert all(torch.equal(proj(x), y) for _ in range(4))
+
+
+def test_weights_beyond_32_bits():
+    """More than 2^32 bytes of codes: outputs here and there."""
+    n, k = (1 << 22) - 5, 2080
+    g = torch.Generator(device=DEV).manual_seed(3)
+    codes = torch.empty(n, k // 2, dtype=torch.uint8, device=DEV).random_(0, 256, generator=g)
+    scales = torch.empty(n, k // 32, dtype=torch.uint8, device=DEV).random_(118, 122, generator=g)
+    proj = Linear4.from_codes(codes, scales)
+    at = [0, 15, 16, 1000, (1 << 21) + 7, (1 << 22) - 20, n - 17, n - 1]
+    W = values(codes[at].cpu(), scales[at].cpu())
+    for T in (1, 3, 20):
+        x = rows_of(T, k, torch.bfloat16, T)
+        check(proj(x)[:, at].contiguous(), x.cpu().double(), W, k // 32 + 64)
+    r = rows8_of(2, k, torch.bfloat16, 5)
+    check(proj(r)[:, at].contiguous(), values8(r), W, k // 128 + 160, cut(r, codes[at].cpu(), scales[at].cpu()))
 
 
 # ------------------------------------------------------------------ packing
