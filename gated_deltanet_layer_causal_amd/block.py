@@ -101,7 +101,8 @@ class Linear4:
         return w
 
     def __call__(self, x) -> torch.Tensor:
-        """x: a tensor [T, K] of a storage type (rows may be strided) or Rows8."""
+        """x: a tensor [T, K] of a storage type (rows may be strided) or Rows8.
+        Where N is not a multiple of 8 the rows of the result are strided."""
         rows, n = x.shape[0], self.n
         t = self.w4.packed if isinstance(x, Rows8) else x
         if n % 8 == 0:
@@ -140,7 +141,7 @@ class GDNLayer4:
         x, z, a, b = self.split(self.proj_in(X))
         out = self.core.step(x, w_conv, a, b, A_log, dt_bias, z, w_norm, cu_seqlens, cache, slot_in,
                              slot_out, slot_tok, layer)
-        return self.proj_out(out.view(X.shape[0], -1))
+        return self.proj_out(out.view(X.shape[0], self.cfg.hv * self.cfg.d))
 
     def prefill(self, X, w_conv, A_log, dt_bias, w_norm, cu_seqlens, cache, slot_in, slot_out=None,
                 layer=0):
@@ -148,4 +149,4 @@ class GDNLayer4:
         x, z, a, b = self.split(self.proj_in(X))
         out = self.core.prefill(x, w_conv, a.contiguous(), b.contiguous(), A_log, dt_bias,
                                 z.contiguous(), w_norm, cu_seqlens, cache, slot_in, slot_out, layer)
-        return self.proj_out(out.view(X.shape[0], -1))
+        return self.proj_out(out.view(X.shape[0], self.cfg.hv * self.cfg.d))

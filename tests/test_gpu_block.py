@@ -176,3 +176,41 @@ def test_layers_agree_on_weights_that_are_in_4_bits():
         cache = GDNStateCache(layer.cfg, 6)
         out.append(layer.step(X, p["w_conv"], p["A_log"], p["dt_bias"], p["w_norm"], cu, cache, ints([-1] * 6), slots))
     assert_close("Y", host(out[1]), host(out[0]), 2 * FWD_TOL_BF16)
+
+
+@pytest.mark.parametrize("hk,hv", [(1, 1), (1, 3), (3, 3)])
+def test_layer_of_odd_head_counts(hk, hv):
+    """Columns of the joined product that do not begin at 16 bytes, rows of a
+    width that is no multiple of 8: against the dense layer."""
+    g = torch.Generator().manual_seed(hk + 4 * hv)
+    C = 2 * hk * D + hv * D
+    dims = {"x": (C, 64), "z": (hv * D, 64), "a": (hv, 64), "b": (hv, 64), "out": (64, hv * D)}
+    W = {k: Linear4((torch.randn(s, generator=g) * s[1] ** -0.5).to(torch.bfloat16).to(DEV)).weight() for k, s in dims.items()}
+    p = [t.to(DEV) for t in (torch.randn(C, 4, generator=g) * 0.5, torch.rand(hv, generator=g) - 2,
+                             torch.randn(hv, generator=g) * 0.1, torch.randn(D, generator=g) * 0.1)]
+    cfg = CoreConfig(hk=hk, hv=hv, d=D, dtype=torch.bfloat16)
+    dense, four = GDNLayer(cfg, 64, W), GDNLayer4(cfg, 64, W)
+    X = torch.randn(5, 64, generator=g).to(torch.bfloat16).to(DEV)
+    cu = ints([0, 4, 5])
+    cache = [GDNStateCache(cfg, 2) for _ in range(4)]
+    want = dense.step(X, *p, cu, cache[0], ints([-1, -1]), ints([0, 1]))
+    for call, c in ((four.step, cache[1]), (four.prefill, cache[2])):
+        got = call(X, *p, cu, c, ints([-1, -1]), ints([0, 1]))
+        assert_close("Y", host(got), host(want), 2 * FWD_TOL_BF16)
+        assert_close("S", host(c.S()), host(cache[0].S()), 2 * FWD_TOL_BF16)
+
+
+def test_layer_without_tokens():
+    """A call of no tokens, in 16 and in 8 bits, leaves the states as they are."""
+    W, p = weights(7), {k: v.to(DEV) for k, v in params(7).items()}
+    layer, norm = GDNLayer4(CoreConfig(**CFG), H, W), ResidualNorm(H)
+    cache = GDNStateCache(layer.cfg, 2)
+    cache.buffer.fill_(7)
+    before = cache.buffer.clone()
+    none = torch.empty(0, H, dtype=torch.bfloat16, device=DEV)
+    eight, _ = norm.forward8(none, none, torch.zeros(H, device=DEV))
+    for X in (none, eight):
+        for call in (layer.step, layer.prefill):
+            Y = call(X, p["w_conv"], p["A_log"], p["dt_bias"], p["w_norm"], ints([0, 0]), cache, ints([1]))
+            assert Y.shape == (0, H) and Y.dtype is torch.bfloat16
+    assert torch.equal(cache.buffer, before)
