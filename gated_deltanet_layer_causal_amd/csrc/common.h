@@ -276,4 +276,12 @@ __device__ __forceinline__ floatx4 tile_mma(floatx4 acc, const SA* A, int lda, c
 
 __device__ __forceinline__ floatx4 zero4() { return floatx4{0.f, 0.f, 0.f, 0.f}; }
 
+// Between LDS reads of some lanes of a wave and writes of others to the same
+// words: a wave's LDS operations take effect in order, so only the compiler has
+// to keep them so (no instruction comes of it).
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 }  // namespace gdn

@@ -50,14 +50,6 @@ __device__ __forceinline__ float lane_of(float x, int l) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l));
 }
 
-// Between LDS reads of some lanes of a wave and writes of others to the same
-// words: a wave's LDS operations take effect in order, so only the compiler has
-// to keep them so (no instruction comes of it).
-__device__ __forceinline__ void wave_lds_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // Thread layout of the state: LPR lanes share a row of D columns; a lane
 // holds the columns 4 l + 4 LPR c + (0..3), c = 0 .. NC - 1, of R rows, so
 // that the lanes of a row touch whole 128-byte lines at a time (with two

@@ -223,7 +223,7 @@ __device__ __forceinline__ void products(const uint4 (&w)[NT], const uint32_t (&
 template <typename X, typename Y, int RP>
 __global__ void __launch_bounds__(1024) w4_kernel(W4Args a) {
   constexpr bool MX = __is_same(X, Mx8);
-  constexpr int E = Step<X>::E, TS = Step<X>::TS, PLANE = 2 * RP * Step<X>::PP, 
+  constexpr int E = Step<X>::E, TS = Step<X>::TS, PLANE = 2 * RP * Step<X>::PP,
                 AHEAD = E == 2 && RP * __is_same(X, fp16) < 8 ? 2 : 1;     // steps asked for together (registers)
   extern __shared__ uint4 stage[];      // [wave][plane][2 RP rows], then the waves' sums
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
@@ -266,15 +266,15 @@ __global__ void __launch_bounds__(1024) w4_kernel(W4Args a) {
         }
       // inputs beyond the matrix become zero: their weights are, but what was read may not be finite
       const bool in = (s * E + h) * 512 + piece * 16 < a.k * E;
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_order();
 #pragma unroll
       for (int i = 0; i < RP; ++i)
         Step<X>::put(mine, PLANE, 2 * i + (lane >> 5), piece, in ? raw[h % AHEAD][i] : make_uint4(0, 0, 0, 0));
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_order();
 #define GDN_W4_PART(T)                                                                              \
   if constexpr (T < TS) {                                                                           \
     RowPart<X> part[1];                                                                             \
-    part[0].read(mine, PLANE, rr, T, q);                                                                   \
+    part[0].read(mine, PLANE, rr, T, q);                                                            \
     if constexpr (MX) part[0].scale = (s * 16 + 4 * T + q) * 32 < a.k ? sx[T] : 127;                \
     const uint4 wt[1] = {w[MX ? T : h * TS + T]};                                                   \
     const uint32_t st[1] = {MX ? sc : sc >> (8 * (h * TS))};                                        \
