@@ -87,7 +87,14 @@ template <typename X> struct Step {
   static constexpr int E = sizeof(X), TERMS = E == 4 ? 3 : 1;
   static constexpr int COLS = 512 / E, TS = COLS / 128;      // inputs and t's of a step
   static constexpr int PP = COLS / 8;                        // pieces of a plane's row
-  __device__ __forceinline__ static int at(int row, int piece) { return row * PP + (piece ^ (row & 15)); }
+  // Pieces of a row change places by its number with the bit pairs exchanged: a
+  // 16-byte access is served for lanes 0-3, 12-15 and 20-27 together and so on,
+  // which read pieces d and d + 4 of different rows (by the number itself each
+  // group met half of the banks twice: 48 rows by 20480 x 8192, 3.9 M conflict
+  // cycles, none so).
+  __device__ __forceinline__ static int at(int row, int piece) {
+    return row * PP + (piece ^ ((row >> 2 & 3) | (row & 3) << 2));
+  }
   // piece i of row `row` in memory into planes `stride` pieces apart
   __device__ __forceinline__ static void put(uint4* planes, int stride, int row, int i, const uint4& raw) {
     if constexpr (TERMS == 1) {
@@ -654,7 +661,7 @@ static hipError_t w4_rows_go(const W4Args& args, hipStream_t st) {
 
 // A unit is a tile of 16 outputs by one of 16 rows.  The inputs are shared out
 // over as many waves a unit as leave all waves on the chip at once (about 16 a
-// CU, 12 with 8-bit rows); beyond that, workgroups take 32 rows.  Fewer waves
+// CU, 12 with 8-bit rows); beyond that, workgroups take 32 rows or more.  Fewer waves
 // a unit leave CUs idle, more wait for a second round.  Measured, us a launch
 // (outputs x inputs, rows: units; each with 4, 2 and 1 waves a unit, and with
 // 1 and 32 rows):
@@ -668,6 +675,18 @@ static hipError_t w4_rows_go(const W4Args& args, hipStream_t st) {
 //         10240 x 8192,  48: 1920  21.9  12.8  13.4  17.2
 //         10240 x 2560,  48: 1920  15.4   6.9   6.0   7.3
 //         16480 x 2560,  64: 4120  31.4  14.4  10.1   9.4
+// Many rows (as prompts have them): two tiles of outputs a wave and 32 to 64
+// rows, since a wave's reads of the rows from LDS and its conversions of the
+// weights then serve more products.  1 tile by 32 rows, 2 by 32, 48 and 64:
+//   bf16   2560 x 6144, 1024:10240  60.0  44.1  64.4  49.3
+//         10240 x 2560,  192: 7680  16.5  16.5  19.4  17.9
+//         20480 x 8192,  128:10240  63.9  57.6  53.8  66.8
+//         16480 x 2560,  256:16480  31.5  30.9  33.7  34.4
+//         20480 x 8192, 1024:81920   701   374   349   306 (1.1 PFLOP/s)
+//   8 bit 10240 x 2560,  128: 5120   9.8  10.0   9.7  11.2
+//         16480 x 2560,  128: 8240  14.1  14.2  12.4  19.6
+//         20480 x 8192,  256:20480  71.6  63.6  58.1  87.3
+//         20480 x 8192, 1024:81920   360   269   201   298
 //
 // Few rows: every wave its own inputs, all of the weights asked for at once;
 // against the above, of which one row takes as long as 16:
@@ -690,7 +709,11 @@ template <typename X, typename Y> static hipError_t w4_m(const W4Args& a, hipStr
   if (units <= 512 || (!MX && units <= 1024 && deep)) return w4_rows_go<X, Y, 2, 4, 1, 1>(a, st);
   if (units <= 1024 || (units <= 2048 && (!MX || deep))) return w4_rows_go<X, Y, 4, 2, 1, 1>(a, st);
   if (units <= 4096) return w4_rows_go<X, Y, 4, 1, 1, 1>(a, st);
-  return w4_rows_go<X, Y, 4, 1, 1, 2>(a, st);
+  if (units <= 8192) return w4_rows_go<X, Y, 4, 1, 1, 2>(a, st);
+  if (MX) return w4_rows_go<X, Y, 4, 1, 2, 3>(a, st);
+  // 64 rows in three terms do not fit into LDS
+  if (units <= 32768 || __is_same(X, float)) return w4_rows_go<X, Y, 4, 1, 2, 2>(a, st);
+  return w4_rows_go<X, Y, 4, 1, 2, sizeof(X) == 2 ? 4 : 2>(a, st);
 }
 
 hipError_t launch_w4(const W4Args& a, gdn_dtype dt, hipStream_t st) {

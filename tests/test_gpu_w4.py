@@ -125,6 +125,28 @@ def test_product_of_8_bit_rows(T, n, k, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,n,k", [(520, 4100, 544), (1030, 2057, 1056), (2050, 4100, 96)])
+def test_prompts(T, n, k, dt):
+    """Rows in hundreds and thousands, in 16 or 32 bits and in 8, into rows of
+    a wider buffer: last rows, outputs and inputs end inside tiles."""
+    codes, scales = make_codes(n, k, T + n + k, 110, 125)
+    proj, W = Linear4.from_codes(codes.to(DEV), scales.to(DEV)), values(codes, scales)
+    wide = n // 8 * 8 + 16
+    for eight in (False, True):
+        out = torch.full((T + 1, wide), 7.0, dtype=DT[dt], device=DEV)
+        y = out[:T, :n]
+        if eight:
+            r = rows8_of(T, k, DT[dt], T, 48)
+            L.w4_fwd_rows8(r, proj.w4, y)
+            check(y, values8(r), W, k // 128 + 160, cut(r, codes, scales))
+        else:
+            x = rows_of(T, k, DT[dt], T, 24)
+            L.gdn_w4_fwd(x, proj.w4, y)
+            check(y, x.cpu().double(), W, TERMS[dt] * (k // 32) + 64)
+        assert (out[T:] == 7).all() and (out[:, n:] == 7).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
 def test_every_code_value_and_position(dt):
     """Rows with a single one pick the weights out one by one, exactly."""
     n, k = 16, 544
