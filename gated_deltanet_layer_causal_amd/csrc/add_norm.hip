@@ -8,7 +8,9 @@
 // their weights in registers, and takes RB rows at a time, so that the loads
 // of RB rows are on their way together (PF: the next rows' while these are
 // worked on).  A row is owned by LPR lanes, or by all
-// waves of a workgroup where it is wider than a wave's 512 columns.
+// waves of a workgroup where it is wider than a wave's 512 columns.  Which
+// products and sums are fused is written out, so that a row's result does not
+// hang on the variant that a call's number of rows selects.
 #include "common.h"
 #include "launch.h"
 
@@ -126,6 +128,7 @@ __device__ __forceinline__ float in_row(const Cols& at, float a, float b) {
 
 template <typename T, typename R, bool MX8, int LPR, int P, int RB, bool NT, int MAXT>
 __global__ void __launch_bounds__(MAXT) add_norm_fwd_kernel(AddNormArgs a) {
+#pragma clang fp contract(off)
   constexpr bool SPLIT = sizeof(T) == 4 || sizeof(R) == 4;
   __shared__ float red[2][LPR == 64 ? 16 : 1][RB];
   const int waves = a.waves;                         // of a row; 1: rows of LPR lanes
@@ -167,8 +170,8 @@ __global__ void __launch_bounds__(MAXT) add_norm_fwd_kernel(AddNormArgs a) {
         float qa = 0.f, qb = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          qa += v[b][p].v[j] * v[b][p].v[j];
-          qb += v[b][p].v[j + 4] * v[b][p].v[j + 4];
+          qa = fmaf(v[b][p].v[j], v[b][p].v[j], qa);
+          qb = fmaf(v[b][p].v[j + 4], v[b][p].v[j + 4], qb);
         }
         ss[b] += in_row(at[p], qa, qb);
       }
@@ -177,7 +180,7 @@ __global__ void __launch_bounds__(MAXT) add_norm_fwd_kernel(AddNormArgs a) {
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
       const int64_t r = r1 + b * per;
-      const float rho = rsqrtf(ss[b] * inv + a.eps);
+      const float rho = rsqrtf(fmaf(ss[b], inv, a.eps));
       if (r < a.rows) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
@@ -228,6 +231,7 @@ __global__ void __launch_bounds__(MAXT) add_norm_fwd_kernel(AddNormArgs a) {
 // sums are added in a fixed order.
 template <typename T, typename R, int LPR, int P, int RB, bool NT, int MAXT, bool PF>
 __global__ void __launch_bounds__(MAXT) add_norm_bwd_kernel(AddNormBwdArgs a) {
+#pragma clang fp contract(off)
   constexpr bool SPLIT = sizeof(T) == 4 || sizeof(R) == 4;
   __shared__ float red[2][LPR == 64 ? 16 : 1][2 * RB];
   __shared__ float dws[MAXT == 256 ? 256 : 1][8 * P + 1];
@@ -286,10 +290,10 @@ __global__ void __launch_bounds__(MAXT) add_norm_bwd_kernel(AddNormBwdArgs a) {
         float qa = 0.f, qb = 0.f, ga = 0.f, gb = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          qa += hv.v[j] * hv.v[j];
-          ga += dv.v[j] * w[p].v[j] * hv.v[j];
-          qb += hv.v[j + 4] * hv.v[j + 4];
-          gb += dv.v[j + 4] * w[p].v[j + 4] * hv.v[j + 4];
+          qa = fmaf(hv.v[j], hv.v[j], qa);
+          ga = fmaf(dv.v[j] * w[p].v[j], hv.v[j], ga);
+          qb = fmaf(hv.v[j + 4], hv.v[j + 4], qb);
+          gb = fmaf(dv.v[j + 4] * w[p].v[j + 4], hv.v[j + 4], gb);
         }
         sums[2 * b] += in_row(at[p], qa, qb);
         sums[2 * b + 1] += in_row(at[p], ga, gb);
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(MAXT) add_norm_bwd_kernel(AddNormBwdArgs a) {
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
       const int64_t r = r1 + b * per;
-      const float rho = rsqrtf(sums[2 * b] * inv + a.eps);
+      const float rho = rsqrtf(fmaf(sums[2 * b], inv, a.eps));
       const float m = sums[2 * b + 1] * rho * inv;      // mean(dn n)
       if (r < a.rows) {
 #pragma unroll
@@ -310,8 +314,8 @@ __global__ void __launch_bounds__(MAXT) add_norm_bwd_kernel(AddNormBwdArgs a) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float n = hv.v[j] * rho;
-            d.v[j] = rho * (dv.v[j] * w[p].v[j] - n * m);
-            dw[p].v[j] += dv.v[j] * n;
+            d.v[j] = rho * fmaf(-n, m, dv.v[j] * w[p].v[j]);
+            dw[p].v[j] = fmaf(dv.v[j], n, dw[p].v[j]);
           }
           if (a.dh) {
             const f8 u = raw_f8(up[b][p]);
@@ -356,6 +360,14 @@ int64_t add_norm_blocks(int64_t rows, int32_t n) {
   return b < most ? b : most;
 }
 
+// Narrow rows: one at a time with the cache's help up to 1.5 times its 256 MB,
+// beyond that as wide ones.  262144 rows, us: bf16 x 128 (268 MB) 43.2, two at a
+// time and non-temporal 44.3; bf16 x 256 93.2 and 86.1, fp32 x 512 382 and 362,
+// its backward 439 and 378.
+template <typename T, typename R> static bool beyond_cache(int64_t values) {
+  return values * (int64_t)(sizeof(T) + sizeof(R)) * 2 >= (int64_t)3 << 27;
+}
+
 template <typename T, typename R, bool MX8, int LPR, int P, int RB, bool NT, int MAXT>
 static hipError_t fwd_go(AddNormArgs a, hipStream_t st) {
   a.waves = norm_waves(a.n);
@@ -374,9 +386,14 @@ static hipError_t fwd_go(AddNormArgs a, hipStream_t st) {
 // Rows of more than eight waves one at a time (8192 x 8192: 88 us).
 template <typename T, typename R, bool MX8>
 static hipError_t fwd_n(const AddNormArgs& a, hipStream_t st) {
+  const bool far = beyond_cache<T, R>(a.rows * a.n);
   if (a.n <= 64) return fwd_go<T, R, MX8, 8, 1, 1, false, 256>(a, st);
-  if (a.n <= 256) return fwd_go<T, R, MX8, 32, 1, 1, false, 256>(a, st);
-  if (a.n <= 512) return fwd_go<T, R, MX8, 64, 1, 1, false, 256>(a, st);
+  if (a.n <= 256)
+    return far ? fwd_go<T, R, MX8, 32, 1, 2, true, 256>(a, st)
+               : fwd_go<T, R, MX8, 32, 1, 1, false, 256>(a, st);
+  if (a.n <= 512)
+    return far ? fwd_go<T, R, MX8, 64, 1, 2, true, 256>(a, st)
+               : fwd_go<T, R, MX8, 64, 1, 1, false, 256>(a, st);
   if (a.n > 8192) return fwd_go<T, R, MX8, 64, 2, 1, true, 1024>(a, st);
   if (a.rows <= 2048) return fwd_go<T, R, MX8, 64, 1, 1, false, 1024>(a, st);
   if (a.n > 4096) return fwd_go<T, R, MX8, 64, 1, 1, true, 1024>(a, st);
@@ -397,9 +414,14 @@ static hipError_t bwd_go(AddNormBwdArgs a, hipStream_t st) {
 // 58.5, four 109).
 template <typename T, typename R>
 static hipError_t bwd_n(const AddNormBwdArgs& a, hipStream_t st) {
+  const bool far = beyond_cache<T, R>(a.rows * a.n);
   if (a.n <= 64) return bwd_go<T, R, 8, 1, 1, false, 256, false>(a, st);
-  if (a.n <= 256) return bwd_go<T, R, 32, 1, 1, false, 256, false>(a, st);
-  if (a.n <= 512) return bwd_go<T, R, 64, 1, 1, false, 256, false>(a, st);
+  if (a.n <= 256)
+    return far ? bwd_go<T, R, 32, 1, 2, true, 256, false>(a, st)
+               : bwd_go<T, R, 32, 1, 1, false, 256, false>(a, st);
+  if (a.n <= 512)
+    return far ? bwd_go<T, R, 64, 1, 2, true, 256, false>(a, st)
+               : bwd_go<T, R, 64, 1, 1, false, 256, false>(a, st);
   if (a.n > 8192) return bwd_go<T, R, 64, 2, 1, true, 1024, false>(a, st);
   if (a.n > 4096) return bwd_go<T, R, 64, 1, 1, true, 1024, true>(a, st);
   return bwd_go<T, R, 64, 1, 2, true, 512, false>(a, st);

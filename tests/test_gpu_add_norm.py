@@ -249,6 +249,35 @@ def test_many_rows(T, n, dt, rt):
     check_bwd(norm.backward(h, d["w"], d["dy"], d["dh"]), h, d["w"], d["dy"], d["dh"])
 
 
+@pytest.mark.parametrize("T,n,dt,rt", [(349601, 72, "fp32", "fp32"), (95407, 264, "fp32", "fp32"), (70001, 480, "bf16", "fp32"),
+                                       (105003, 512, "fp16", "fp16"), (211003, 256, "bf16", "bf16")])
+def test_narrow_rows_beyond_the_cache(T, n, dt, rt):
+    """The last rows against 64 bits, all of them against calls of fewer rows
+    bit by bit (in 8 bits as well), dw against 64 bits."""
+    g = torch.Generator(device=DEV).manual_seed(n)
+    x, res, up = (torch.randn(T, n, generator=g, device=DEV) for _ in range(3))
+    x, res, up, dy = x.to(DT[dt]), (res * 3).to(DT[rt]), up.to(DT[rt]), (up * 2).to(DT[dt])
+    w = torch.randn(n, generator=g, device=DEV) * 0.1
+    norm = ResidualNorm(n, DT[dt], DT[rt], EPS)
+    y, h = norm.forward(x, res, w)
+    b = norm.backward(h, w, dy, up)
+    eight = norm.forward8(x, res, w)[0] if n % 32 == 0 else None
+    for at in (0, T - 20000):
+        s = slice(at, at + 20000)
+        y1, h1 = norm.forward(x[s], res[s], w)
+        b1 = norm.backward(h1, w, dy[s], up[s])
+        assert torch.equal(y[s], y1) and torch.equal(h[s], h1)
+        assert torch.equal(b["dx"][s], b1["dx"]) and torch.equal(b["dres"][s], b1["dres"])
+        if eight is not None:
+            e1 = norm.forward8(x[s], res[s], w)[0]
+            assert torch.equal(eight.q[s].view(torch.uint8), e1.q.view(torch.uint8)) and torch.equal(eight.scale[s], e1.scale)
+    s = slice(T - 500, T)
+    check_fwd(y[s], h[s], {"x": x[s], "res": res[s], "w": w}, DT[rt])
+    hd, dyd = h.double(), dy.double()
+    t = dyd * hd * (hd.square().mean(1, keepdim=True) + EPS).rsqrt()
+    near(b["dw"], t.sum(0).cpu(), ((T + 48) * U * t.abs().sum(0) + 1e-300).cpu(), "dw")
+
+
 def test_more_rows_than_a_launch_and_offsets_beyond_32_bits():
     """2^22 + 3 rows: more than a launch's workgroups, and elements beyond
     2^32; rows here and there against the formula."""
