@@ -974,7 +974,8 @@ class Rows8:
     """Rows in 8 bits: q float8_e4m3fn [T, n] under a power of two for each 32
     columns, scale uint8 [T, n / 32] (2^(byte - 127)); rows may be strided.
     dtype: the storage type of the rows that they stand for, which a product's
-    outputs take.  Checked once and kept."""
+    outputs take.  Checked once and kept.  Addresses are asked of the tensors at
+    each call, so that copies (copy.deepcopy, pickle) have memory of their own."""
 
     def __init__(self, q, scale, dtype=torch.bfloat16):
         if q is None or q.dim() != 2 or q.shape[1] % 32 or q.shape[1] < 32:
@@ -984,20 +985,45 @@ class Rows8:
         (T, n), dev = q.shape, q.device
         ldq = _wide("q", q, torch.float8_e4m3fn, T, n, dev)
         lds = _wide("scale", scale, torch.uint8, T, n // 32, dev)
-        self.shape, self.dtype, self.device, self.index = (T, n), dtype, dev, q.get_device()
-        self.ptrs = q.data_ptr(), ldq, scale.data_ptr(), lds
+        self.shape, self.dtype, self._ld = (T, n), dtype, (ldq, lds)
         self._memory, self._views = None, (q, scale)
 
     @classmethod
     def empty(cls, T, n, dtype, like):
         """New memory for T rows of n columns on the device of `like`."""
         self = cls.__new__(cls)
-        self._memory = memory = like.new_empty(T * (n + n // 32), dtype=torch.uint8)
+        self._memory = like.new_empty(T * (n + n // 32), dtype=torch.uint8)
         self._views = None
-        at = memory.data_ptr()
-        self.shape, self.dtype, self.device, self.index = (T, n), dtype, memory.device, memory.get_device()
-        self.ptrs = at, n, at + T * n, n // 32
+        self.shape, self.dtype = (T, n), dtype
         return self
+
+    def __getstate__(self):
+        # a copy's views are made of its own memory; q as bytes, since torch does
+        # not pickle 8-bit floats
+        views = None if self._memory is not None else (self._views[0].view(torch.uint8), self._views[1])
+        return {**self.__dict__, "_views": views}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        if self._views is not None:
+            self._views = self._views[0].view(torch.float8_e4m3fn), self._views[1]
+
+    @property
+    def device(self) -> torch.device:
+        return (self._views[0] if self._memory is None else self._memory).device
+
+    @property
+    def index(self) -> int:
+        return (self._views[0] if self._memory is None else self._memory).get_device()
+
+    @property
+    def ptrs(self):
+        """What the C ABI takes: q, its row stride, scale and its row stride."""
+        if self._memory is None:
+            (q, scale), (ldq, lds) = self._views, self._ld
+            return q.data_ptr(), ldq, scale.data_ptr(), lds
+        (T, n), at = self.shape, self._memory.data_ptr()
+        return at, n, at + T * n, n // 32
 
     def _tensors(self):
         if self._views is None:
@@ -1099,7 +1125,9 @@ def gdn_w4_bytes(n, k):
 
 class W4:
     """Packed 4-bit weights of n outputs and k inputs, checked once and kept.
-    packed: a uint8 tensor, or where to make one (a tensor of any type)."""
+    packed: a uint8 tensor, or where to make one (a tensor of any type).  Its
+    address is asked at each call, so that copies (copy.deepcopy, pickle) are
+    weights of their own."""
 
     def __init__(self, packed, n, k, make=False):
         need = gdn_w4_bytes(n, k)
@@ -1110,8 +1138,19 @@ class W4:
         elif packed.dtype != torch.uint8 or not packed.is_contiguous() or packed.numel() < need:
             raise ValueError(f"the packed weights must be a contiguous uint8 tensor of {need} bytes")
         self.packed, self.n, self.k = packed, n, k
-        self.device, self.index = packed.device, packed.get_device()
-        self.args = packed.data_ptr(), packed.numel()
+
+    @property
+    def device(self) -> torch.device:
+        return self.packed.device
+
+    @property
+    def index(self) -> int:
+        return self.packed.get_device()
+
+    @property
+    def args(self):
+        """What the C ABI takes: the address and the size."""
+        return self.packed.data_ptr(), self.packed.numel()
 
 
 def _weight(w4, weight):
