@@ -830,7 +830,9 @@ def gdn_cache_workspace(n_slots):
 
 class Slots:
     """A cache's buffer [n_slots, slot], counts and workspace, checked once
-    and kept: what the calls below take instead of (buf, refs, ..., ws)."""
+    and kept: what the calls below take instead of (buf, refs, ..., ws).
+    Addresses are asked of the tensors at each call, so that copies
+    (copy.deepcopy, pickle) have memory of their own."""
 
     def __init__(self, buf, refs, ws):
         if buf.dim() != 2 or not buf.is_contiguous():
@@ -841,8 +843,20 @@ class Slots:
             _ws(ws)
             _on(buf.device, ("workspace", ws))
         self.buf, self.refs, self.ws = buf, refs, ws
-        self.device, self.index = buf.device, buf.get_device()
-        self.ptrs = _ptr(buf), _ptr(refs), _ptr(ws), 0 if ws is None else ws.numel()
+
+    @property
+    def device(self) -> torch.device:
+        return self.buf.device
+
+    @property
+    def index(self) -> int:
+        return self.buf.get_device()
+
+    @property
+    def ptrs(self):
+        """What the C ABI takes: buffer, counts, workspace and its size."""
+        ws = self.ws
+        return self.buf.data_ptr(), self.refs.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel()
 
     def _table(self, name, t, n=None):
         if t is None or not _is_flat(t, torch.int32, t.numel() if n is None else n, self.index):

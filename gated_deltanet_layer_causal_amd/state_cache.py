@@ -50,6 +50,10 @@ class GDNStateCache:
         self._slots = L.Slots(buffer, refs, torch.empty(L.gdn_cache_workspace(n_slots),
                                                         dtype=torch.uint8, device=buffer.device))
 
+    def __getstate__(self):
+        """A copy's views of its layers are made of its own buffer."""
+        return {**self.__dict__, "_layers": [None] * self.n_layers}
+
     @property
     def buffer(self) -> torch.Tensor:
         """All slots, uint8 [n_slots, slot_bytes]."""
