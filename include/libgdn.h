@@ -494,7 +494,10 @@ size_t gdn_add_norm_bwd_workspace(int64_t rows, int32_t n);
  * ties to even.  A group with a NaN or an infinity becomes NaN.
  * gdn_w4_arrange: weights that are in 4 bits already, codes [n][ldc] (input 2j
  * in the low four bits of byte j; 16-byte aligned, ldc a multiple of 16) and
- * scales [n][lds] (2^(byte - 127); 255: NaN).
+ * scales [n][lds] (2^(byte - 127); 255: NaN).  Values that fp32 does not hold
+ * (magnitudes from 4 on under the byte 253, from 2 on under 254) are infinities
+ * in gdn_w4_unpack, and gdn_w4_fwd's sums with them are infinite or NaN;
+ * gdn_w4_fwd_mx8 takes them as they are.
  * gdn_w4_unpack: the values, W [n][ldw] in dtype (exact in bf16 and fp32; in
  * fp16 within its range). */
 size_t gdn_w4_bytes(int32_t n, int32_t k);
