@@ -102,7 +102,8 @@ template <typename X> struct Step {
     } else {
       // A term is the value's upper 16 bits (8 significant ones), cut, not
       // rounded, so that what is left is exact and no term overflows.  What is
-      // not finite stays in the first term.
+      // not finite stays in the first term.  Bits below 2^-133, which no bf16 term
+      // holds, are lost (only values below 2^-109 have such).
       const float* p = reinterpret_cast<const float*>(&raw);
       float v[4];
 #pragma unroll

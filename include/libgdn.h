@@ -511,7 +511,8 @@ gdn_status gdn_w4_unpack(int32_t n, int32_t k, const void* packed, size_t bytes,
 
 /* y[t][j] = sum_i x[t][i] W[j][i], sums in fp32, rounded once.
  * gdn_w4_fwd: x [rows][ldx] and y [rows][ldy] in dtype; the rows' values are
- * not rounded (fp16 and fp32 values enter as sums of two or three bf16 ones).
+ * not rounded (fp16 and fp32 values enter as sums of two or three bf16 ones),
+ * but of fp32 values what lies below 2^-133, bf16's smallest value, is cut.
  * gdn_w4_fwd_mx8: rows as gdn_add_norm_fwd_mx8 writes them (q 16-byte aligned,
  * ldq a multiple of 16), y in dtype.  The matrix instruction for such rows
  * adds the products of eight adjacent inputs with 13 bits below the largest of

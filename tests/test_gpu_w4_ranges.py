@@ -1,4 +1,6 @@
-"""4-bit weights at the ends of their scales.  Tolerances as in test_gpu_w4."""
+"""4-bit weights at the ends of their scales, and rows at the low end of
+their types.  Tolerances as in test_gpu_w4; of fp32 rows what lies below
+2^-133, bf16's smallest value, is cut, so a sum may lose 2^-133 sum |w| more."""
 import pytest
 import torch
 
@@ -81,3 +83,24 @@ def test_scales_whose_larger_values_are_beyond_fp32(byte, dt, T):
     assert torch.equal(p.weight(DT[dt]).cpu().double(), want)
     check(p(r), values8(r), W, K // 128 + 160, cut(r, codes, scales))
     assert not p(x)[:, out.any(1).to(DEV)].isfinite().any()
+
+
+@pytest.mark.parametrize("T", [1, 3, 20])
+@pytest.mark.parametrize("e", [-109, -112, -126, -130, -134])
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_rows_at_the_low_end(dt, e, T):
+    """bf16 rows enter as they are, numbers below the normal ones too; of fp32
+    rows what lies below 2^-133 is cut."""
+    codes, scales, W = weights(227)
+    x = rows(T, 2.0 ** e, dt)
+    lost = 2.0 ** -133 * W.abs().sum(1) if dt == "fp32" else 0.0
+    check(proj(codes, scales)(x), x.cpu().double(), W, TERMS[dt] * (K // 32) + 64, lost)
+
+
+@pytest.mark.parametrize("T", [1, 3, 20])
+@pytest.mark.parametrize("byte", [120, 135, 141])
+def test_fp16_rows_below_the_normal_numbers(byte, T):
+    codes, scales, W = weights(byte)
+    x = rows(T, 2.0 ** -18, "fp16")
+    assert (x.abs() < 2.0 ** -14).all() and (x != 0).any()
+    check(proj(codes, scales)(x), x.cpu().double(), W, TERMS["fp16"] * (K // 32) + 64)
