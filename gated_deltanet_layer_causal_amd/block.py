@@ -119,8 +119,10 @@ class Linear4:
 class GDNLayer4:
     """GDNLayer's serving form with projections of 4 bits: hidden states X
     [T, H] (a tensor or Rows8, from ResidualNorm.forward8) -> Y [T, H].  The
-    four input projections are one product, whose columns the core reads where
-    they are: a layer is the norm, two products and the core's step."""
+    four input projections are one product, whose columns the core's step reads
+    where they are: a layer's step is the norm, two products and the core's step.
+    prefill copies the columns of z, a and b, which the chunked forward wants
+    contiguous."""
 
     def __init__(self, cfg, hidden: int, weights: dict, device="cuda"):
         """weights: GDNLayer's, name -> [out, in] tensors."""
@@ -145,7 +147,7 @@ class GDNLayer4:
 
     def prefill(self, X, w_conv, A_log, dt_bias, w_norm, cu_seqlens, cache, slot_in, slot_out=None,
                 layer=0):
-        """step() for prompts, through GDNCore.prefill."""
+        """step() for prompts, through GDNCore.prefill (and copies of z, a and b)."""
         x, z, a, b = self.split(self.proj_in(X))
         out = self.core.prefill(x, w_conv, a.contiguous(), b.contiguous(), A_log, dt_bias,
                                 z.contiguous(), w_norm, cu_seqlens, cache, slot_in, slot_out, layer)
