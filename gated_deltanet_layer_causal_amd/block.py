@@ -102,7 +102,8 @@ class Linear4:
 
     def __call__(self, x) -> torch.Tensor:
         """x: a tensor [T, K] of a storage type (rows may be strided) or Rows8.
-        Where N is not a multiple of 8 the rows of the result are strided."""
+        Where N is not a multiple of 8 the rows of the result are strided.  A
+        row's last bits may depend on T, which the order of its sums follows."""
         rows, n = x.shape[0], self.n
         t = self.w4.packed if isinstance(x, Rows8) else x
         if n % 8 == 0:

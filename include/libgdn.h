@@ -518,7 +518,9 @@ gdn_status gdn_w4_unpack(int32_t n, int32_t k, const void* packed, size_t bytes,
  * adds the products of eight adjacent inputs with 13 bits below the largest of
  * them (2^9 times finer than the rows' own steps); all other sums are fp32.
  * For few rows: the time is that of reading W up to a few dozen rows.  Any
- * number of rows is served.  y may not overlap what is read. */
+ * number of rows is served.  The order of a sum follows from rows, n, k and the
+ * types: a call repeats bit by bit, but a row in a batch of another size may
+ * differ by the roundings of its fp32 sums.  y may not overlap what is read. */
 gdn_status gdn_w4_fwd(int64_t rows, int32_t n, int32_t k, gdn_dtype dtype, const void* x,
                       int64_t ldx, const void* packed, size_t bytes, void* y, int64_t ldy,
                       void* stream);
