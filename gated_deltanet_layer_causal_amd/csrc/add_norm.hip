@@ -188,7 +188,10 @@ __global__ void __launch_bounds__(MAXT) add_norm_fwd_kernel(AddNormArgs a) {
           f8 y;
 #pragma unroll
           for (int j = 0; j < 8; ++j) y.v[j] = v[b][p].v[j] * rho * w[p].v[j];
-          if constexpr (MX8) {         // groups of 32 columns: 4 adjacent lanes, or 8 of each run
+          // 8 bits: groups of 32 columns are 4 adjacent lanes, or 8 of each run.  They go
+          // out in plain stores of 8 or 4 bytes a lane, which is near enough to the floor
+          // (65536 x 2560 in bf16: 187 us for 176 us of bytes, fp32 32768 x 2560 167 for 163).
+          if constexpr (MX8) {
             uint8_t* q = (uint8_t*)a.y + r * a.ldy;
             uint8_t* scale = a.scale + r * a.lds;
             float ma = amax4(y.v), mb = amax4(y.v + 4);
@@ -350,8 +353,12 @@ __global__ void __launch_bounds__(MAXT) add_norm_bwd_kernel(AddNormBwdArgs a) {
 static int norm_waves(int n) { return n <= 512 ? 1 : n <= 8192 ? (n + 511) / 512 : 16; }
 static int norm_lanes(int n) { return n <= 64 ? 8 : n <= 256 ? 32 : 64; }
 
-// Workgroups of the backward: about ten to sixteen waves a CU.  More only add
-// partial sums of dw, fewer leave loads unasked.  Measured, us by workgroups
+// Workgroups of the backward: six to sixteen waves a CU (1024 workgroups of two
+// waves at 1024 columns, 512 of three at 1032, 512 of eight at 4096, 256 of
+// sixteen at 8192).  More only add partial sums of dw, fewer leave loads unasked.
+// Where rows are taken two at a time and there are fewer than two for each
+// workgroup, some workgroups get none and leave a partial sum of zeros.
+// Measured, us by workgroups
 // 256 / 512 / 1024: 16384 x 1000 - / 28 / 25, 16384 x 2560 - / 54.6 / 65,
 // 3001 x 8192 34 / 38 / 43 (bf16).
 int64_t add_norm_blocks(int64_t rows, int32_t n) {
@@ -361,9 +368,10 @@ int64_t add_norm_blocks(int64_t rows, int32_t n) {
 }
 
 // Narrow rows: one at a time with the cache's help up to 1.5 times its 256 MB,
-// beyond that as wide ones.  262144 rows, us: bf16 x 128 (268 MB) 43.2, two at a
-// time and non-temporal 44.3; bf16 x 256 93.2 and 86.1, fp32 x 512 382 and 362,
-// its backward 439 and 378.
+// beyond that as wide ones, from 65 columns on (narrower ones always one at a
+// time).  262144 rows, us: bf16 x 128 (268 MB) 43.2, two at a time and
+// non-temporal 44.3; bf16 x 256 93.2 and 86.1, fp32 x 512 382 and 362, its
+// backward 439 and 378.
 template <typename T, typename R> static bool beyond_cache(int64_t values) {
   return values * (int64_t)(sizeof(T) + sizeof(R)) * 2 >= (int64_t)3 << 27;
 }
