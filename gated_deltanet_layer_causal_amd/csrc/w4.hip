@@ -688,6 +688,13 @@ static hipError_t w4_rows_go(const W4Args& args, hipStream_t st) {
 //         16480 x 2560,  128: 8240  14.1  14.2  12.4  19.6
 //         20480 x 8192,  256:20480  71.6  63.6  58.1  87.3
 //         20480 x 8192, 1024:81920   360   269   201   298
+// (each on one set of values, pass after pass; the largest depend on the values and
+// on the card's clock: under the profiler, random codes in three sets, 1024 rows
+// by 20480 x 8192 take 348 to 406 us, 324 at best, and 8-bit rows 221 to 259.)
+//
+// fp16 rows of such calls take longer than bf16 ones (1024 rows by 20480 x 8192 538
+// us against 348, by 2560 x 6144 62 against 50), fp32 rows, three terms, 2.4 to
+// 3 times as long (1054 and 119).
 //
 // Few rows: every wave its own inputs, all of the weights asked for at once;
 // against the above, of which one row takes as long as 16:
