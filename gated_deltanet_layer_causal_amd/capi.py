@@ -1164,7 +1164,10 @@ class W4:
     @property
     def args(self):
         """What the C ABI takes: the address and the size."""
-        return self.packed.data_ptr(), self.packed.numel()
+        packed = self.packed
+        if not packed.is_contiguous():      # put there after the check above
+            raise ValueError("the packed weights must be contiguous")
+        return packed.data_ptr(), packed.numel()
 
 
 def _weight(w4, weight):

@@ -91,6 +91,14 @@ def test_weights_follow_their_tensor():
     assert p.w4.device.type == "meta"
 
 
+def test_weights_that_are_not_in_a_row_are_refused():
+    """Their size says nothing of the memory behind the address."""
+    p = proj()
+    p.w4.packed = p.w4.packed[:1].expand(p.w4.packed.numel())
+    with pytest.raises(ValueError, match="contiguous"):
+        p.w4.args
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("how", COPIES)
 def test_copies_on_the_device(how):
